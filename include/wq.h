@@ -287,6 +287,129 @@ int wq_gemm_grouped(const void *base, const wq_desc *table_dev, int count,
                     int64_t total_tiles, int64_t M, void *workspace,
                     uint64_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------ between the projections
+ * The operators a decoder layer needs between its packed projections: attention
+ * over a prompt, a key/value cache in the int4 block-32 format above with the
+ * attention that reads it, and the norms around a block. Activations are fp32,
+ * as everywhere in the library. Rows of q, k, v and out may be slices of a wider
+ * row (a fused q|k|v projection): consecutive tokens are `*_stride` floats
+ * apart (a multiple of 4, at least heads * head_dim), heads follow each other
+ * within a row. head_dim is 64 or 128, heads a multiple of kv_heads, and query
+ * head j reads key/value head j / (heads / kv_heads). Lengths and page numbers
+ * are device data, so they are not checked on the host: the kernels bound every
+ * index by the sizes given to the call, with the outcome stated at each entry.
+ * Packed sequences are given by cu [B + 1] (int32, nondecreasing, cu[0] >= 0):
+ * sequence b is the tokens cu[b] <= t < cu[b + 1] of the T given ones, possibly
+ * none; cu may be null when B == 1 (all T tokens). Tokens of no sequence are
+ * not read, and their output rows keep what they held.
+ */
+#define WQ_KV_PAGE 64         /* tokens per page of the key/value cache */
+
+/*
+ * Bytes of device workspace wq_attn_prefill needs (256-byte aligned, used only
+ * during the call's work on its stream). 0 on bad arguments, and where the
+ * call needs none.
+ */
+uint64_t wq_attn_prefill_ws(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * wq_attn_prefill -- causal attention of B packed prompts, grouped heads:
+ *   out[t, j] = sum_{u <= t} p_u v[u, j'],  p = softmax over u of
+ *   scale * <q[t, j], k[u, j']>,  j' = j / (heads / kv_heads),
+ * u over the tokens of t's own sequence. fp32 in and out. The products run on
+ * the fp16 matrix cores with every operand split into two binary16 parts (22
+ * bits) after power-of-two normalisation of each query row and of every 32
+ * consecutive keys or values of a head, partial sums, softmax maximum and sum
+ * in fp32. Error: logits within (2^-20 + 2^-38 r) |scale| |q|_2 |k|_2, r the
+ * largest magnitude of the 32 keys over the key's own norm; weights and sums add 2^-20 sum p |v| +
+ * 2^-36 max |v| per output, the maximum over the visible values of the head.
+ * Non-finite data stays with the rows that see it: a NaN or infinity in a
+ * query makes its row NaN, in a key every row that sees the key, in element d of a
+ * value element d of every row that sees the value; no other output changes.
+ * T, heads * head_dim and the strides are below 2^30, B below 2^24; T * heads
+ * below 2^31. out must not alias an input.
+ */
+int wq_attn_prefill(const float *q, int64_t q_stride, const float *k, int64_t k_stride,
+                    const float *v, int64_t v_stride, int64_t T, const int32_t *cu, int64_t B,
+                    int64_t heads, int64_t kv_heads, int64_t head_dim, float scale,
+                    float *out, int64_t out_stride, void *workspace, uint64_t workspace_bytes,
+                    hipStream_t stream);
+
+/*
+ * A paged key/value cache in int4 block-32: each key or value row of a head is
+ * one packed row of head_dim codes (head_dim / 2 bytes) and head_dim / 32
+ * binary16 scales, laid out exactly as the packed tensors above, so a cache
+ * read as a [n_pages * kv_heads * 64][head_dim] tensor works with wq_unpack
+ * and wq_embed. All four arrays are 16-byte aligned.
+ */
+typedef struct wq_kv_cache {
+    void *kq;              /* keys    uint8    [n_pages][kv_heads][64][head_dim / 2] */
+    uint16_t *ks;          /*         binary16 [n_pages][kv_heads][64][head_dim / 32] */
+    void *vq;              /* values, as the keys */
+    uint16_t *vs;
+    int64_t n_pages;       /* below 2^31 */
+    int32_t kv_heads;      /* 1..1024 */
+    int32_t head_dim;      /* 64 or 128 */
+} wq_kv_cache;
+
+/*
+ * wq_kv_append -- quantize new key and value rows into the cache by wq_pack's
+ * rule (bit-exact). Token t of sequence b goes to position
+ * start[b] + t - cu[b] of its sequence (start [B], null for 0): row
+ * position % 64 of page table[b][position / 64] (table [B][max_pages], int32).
+ * A row whose position lies outside [0, 64 * max_pages) or whose page lies
+ * outside [0, n_pages) is dropped; nothing else in the cache is touched. Two
+ * tokens sent to one row (a page listed twice) leave codes and scales of
+ * either, block by block. A block that holds a NaN or an infinity, or whose
+ * scale would pass binary16's range (max |x| / 7 rounds above 65504), is stored
+ * as a NaN scale with codes 0, so it reads back as NaN. T * kv_heads below 2^31.
+ */
+int wq_kv_append(const wq_kv_cache *cache, const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                 int64_t T, const int32_t *cu, const int32_t *start, int64_t B,
+                 const int32_t *table, int64_t max_pages, hipStream_t stream);
+
+/* Bytes of device workspace wq_attn_decode needs, as wq_attn_prefill_ws. */
+uint64_t wq_attn_decode_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages);
+
+/*
+ * wq_attn_decode -- attention of one query token per sequence over the cache:
+ *   out[b, j] = sum_{u < lens[b]} p_u v_u,  p = softmax over u of
+ *   scale * <q[b, j], k_u>,
+ * k_u and v_u the cached rows of head j / (heads / kv_heads) at position u, dequantized
+ * inside the kernel (the token itself is appended first). The codes are exact
+ * operands of the fp16 matrix cores; q, and the weights times the value
+ * scales, are split into two binary16 parts after power-of-two normalisation;
+ * sums, softmax maximum and sum in fp32. Long sequences are split over
+ * workgroups and joined in a fixed order. lens[b] == 0 gives a row of zeros;
+ * a non-finite query value makes its head NaN;
+ * a length outside [0, 64 * max_pages], or a page outside [0, n_pages) among
+ * those the length covers, gives rows of NaN for that sequence and reads
+ * nothing outside the cache. Rows past lens[b] may hold anything.
+ * B * heads * max_pages below 2^40.
+ */
+int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
+                   const int32_t *lens, int64_t B, const int32_t *table, int64_t max_pages, float scale,
+                   float *out, int64_t out_stride, void *workspace, uint64_t workspace_bytes,
+                   hipStream_t stream);
+
+/*
+ * wq_residual_norm -- the norms around a block, its gate and its residual, in
+ * one pass over [M][N] rows:
+ *   t = y * rsqrt(mean(y^2) + eps) * post_weight    (post_weight null: t = y)
+ *   h_out = h + alpha * gate * t                    (gate null: 1)
+ *   x_out = h_out * rsqrt(mean(h_out^2) + eps) * pre_weight
+ * y is the block's output, h the residual stream, x_out the next block's
+ * input. y null: h_out = h (post_weight and gate must be null too), the norm
+ * before the first block. h_out or x_out may be null when not wanted (not
+ * both); pre_weight null: weight 1. gate is [M][N] (gate_stride N) or one row
+ * for all (gate_stride 0). h_out may be h itself; no other outputs alias an
+ * input or each other. Rows are contiguous, N >= 1 of any size, and pointers need only
+ * 4-byte alignment here. Sums in fp32 (rows above 32768: in fp64).
+ */
+int wq_residual_norm(const float *h, const float *y, const float *post_weight, const float *gate,
+                     int64_t gate_stride, float alpha, const float *pre_weight, float eps,
+                     int64_t M, int64_t N, float *h_out, float *x_out, hipStream_t stream);
+
 /* Human-readable text for a wq_status value (static storage). */
 const char *wq_strerror(int status);
 

@@ -12,11 +12,21 @@ device memory and the current stream):
     embed(ids, q, scales, K, bits)      tied-embedding rows of a packed table, fp32
     Package / GroupedCall               64-byte-aligned package + one-launch decode step
 
+Between the projections of a layer:
+
+    attn_prefill(q, k, v, cu)           causal attention over packed prompts
+    KVCache                             paged key/value cache in int4 block-32
+    kv_append(cache, k, v, table, cu)   quantize new rows into the cache
+    attn_decode(q, cache, table, lens)  attention of one token per sequence over the cache
+    residual_norm(h, y, ...)            norms around a block, its gate and its residual
+
 The library is loaded on first use and must have been built
 (``python -m weight_only_bit_block_amd.build``); there is no fallback.
 """
 from .wq import (BLOCK, GEMV_MAX_M, GroupedCall, Package, WqError, embed, gemm, gemm_noalloc, gemv,
                  header_symbols, linear, load, pack, table_layout, table_plan, table_plan_gemm, unpack)
+from .layer import KV_PAGE, KVCache, attn_decode, attn_prefill, kv_append, residual_norm
 
 __all__ = ["BLOCK", "GEMV_MAX_M", "GroupedCall", "Package", "WqError", "embed", "gemm", "gemm_noalloc", "gemv",
-           "header_symbols", "linear", "load", "pack", "table_layout", "table_plan", "table_plan_gemm", "unpack"]
+           "header_symbols", "linear", "load", "pack", "table_layout", "table_plan", "table_plan_gemm", "unpack",
+           "KV_PAGE", "KVCache", "attn_decode", "attn_prefill", "kv_append", "residual_norm"]

@@ -19,7 +19,8 @@ OUT = os.path.join(HERE, "libwq.so")
 OBJDIR = os.path.join(ROOT, "_build", "wq")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["wq_abi.cpp", "wq_pack.hip", "wq_gemv.hip", "wq_mgemv.hip", "wq_gemm.hip", "wq_embed.hip"]
+SOURCES = ["wq_abi.cpp", "wq_pack.hip", "wq_gemv.hip", "wq_mgemv.hip", "wq_gemm.hip", "wq_embed.hip",
+           "wq_layer_abi.cpp", "wq_prompt.hip", "wq_kv.hip", "wq_norm.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",
@@ -55,7 +56,7 @@ def _compile(src: str) -> str:
 def build(verbose: bool = False) -> str:
     """Compile every source and link libwq.so; returns its path."""
     os.makedirs(OBJDIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = OUT + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]

@@ -196,6 +196,61 @@ hipError_t launch_mgemv_grouped(const void *base, const wq_desc *table_dev, int 
 hipError_t launch_embed(const int32_t *ids, int64_t n_ids, int64_t K, int64_t N, int bits,
                         const void *q, const uint16_t *scales, float *out, hipStream_t stream);
 
+// ---------------------------------------------------------------- between the projections
+// Arguments of the attention and cache kernels as the C ABI takes them (wq.h),
+// already validated.
+struct PromptArgs {
+    const float *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;       // floats between tokens
+    int64_t T;
+    const int32_t *cu;                          // null: one sequence of T tokens
+    int B;
+    int heads, kv_heads, head_dim;
+    float scale;
+    float *out;
+    int64_t out_stride;
+    void *ws;
+};
+struct AppendArgs {
+    wq_kv_cache cache;
+    const float *k, *v;
+    int64_t k_stride, v_stride;
+    int64_t T;
+    const int32_t *cu, *start;
+    int B;
+    const int32_t *table;
+    int64_t max_pages;
+};
+struct DecodeArgs {
+    wq_kv_cache cache;
+    const float *q;
+    int64_t q_stride;
+    int heads;
+    const int32_t *lens;
+    int B;
+    const int32_t *table;
+    int64_t max_pages;
+    float scale;
+    float *out;
+    int64_t out_stride;
+    void *ws;
+};
+struct NormArgs {
+    const float *h, *y, *post, *gate;
+    int64_t gate_stride;
+    float alpha;
+    const float *pre;
+    float eps;
+    int64_t M, N;
+    float *h_out, *x_out;
+};
+uint64_t prompt_ws_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim);
+uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages);
+hipError_t launch_attn_prefill(const PromptArgs &a, hipStream_t stream);
+hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream);
+hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream);
+hipError_t launch_residual_norm(const NormArgs &a, hipStream_t stream);
+
 }  // namespace wq
 
 static_assert(sizeof(wq_desc) == WQ_TABLE_ALIGN, "tensor-table entries are 64 bytes");

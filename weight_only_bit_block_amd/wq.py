@@ -48,6 +48,19 @@ class WqDesc(ctypes.Structure):
 assert ctypes.sizeof(WqDesc) == 64
 
 
+class WqKVCache(ctypes.Structure):
+    """Mirror of `struct wq_kv_cache`."""
+    _fields_ = [
+        ("kq", ctypes.c_void_p),
+        ("ks", ctypes.c_void_p),
+        ("vq", ctypes.c_void_p),
+        ("vs", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+    ]
+
+
 def load(path: Optional[str] = None):
     """Load libwq.so (once). Raises if the library has not been built."""
     global _lib
@@ -73,12 +86,21 @@ def load(path: Optional[str] = None):
     lib.wq_gemv_grouped.argtypes = [P, P, I, I64, I64, P]
     lib.wq_gemm_grouped.argtypes = [P, P, I, I64, I64, P, ctypes.c_uint64, P]
     lib.wq_embed.argtypes = [P, I64, I64, I64, I, P, P, P, P]
+    U64, F, C = ctypes.c_uint64, ctypes.c_float, ctypes.POINTER(WqKVCache)
+    lib.wq_attn_prefill_ws.argtypes = [I64] * 5
+    lib.wq_attn_prefill_ws.restype = U64
+    lib.wq_attn_prefill.argtypes = [P, I64, P, I64, P, I64, I64, P, I64, I64, I64, I64, F, P, I64, P, U64, P]
+    lib.wq_kv_append.argtypes = [C, P, I64, P, I64, I64, P, P, I64, P, I64, P]
+    lib.wq_attn_decode_ws.argtypes = [I64] * 5
+    lib.wq_attn_decode_ws.restype = U64
+    lib.wq_attn_decode.argtypes = [C, P, I64, I64, P, I64, P, I64, F, P, I64, P, U64, P]
+    lib.wq_residual_norm.argtypes = [P, P, P, P, I64, F, P, F, I64, I64, P, P, P]
     lib.wq_strerror.argtypes = [I]
     lib.wq_strerror.restype = ctypes.c_char_p
     lib.wq_abi_version.argtypes = []
     for f in ("wq_pack", "wq_unpack", "wq_gemv", "wq_gemm", "wq_linear", "wq_gemm_noalloc", "wq_table_layout",
               "wq_table_plan", "wq_table_plan_gemm", "wq_gemv_grouped", "wq_gemm_grouped", "wq_embed",
-              "wq_abi_version"):
+              "wq_attn_prefill", "wq_kv_append", "wq_attn_decode", "wq_residual_norm", "wq_abi_version"):
         getattr(lib, f).restype = I
     _lib = lib
     return lib
