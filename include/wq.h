@@ -326,8 +326,8 @@ uint64_t wq_attn_prefill_ws(int64_t T, int64_t B, int64_t heads, int64_t kv_head
  * Non-finite data stays with the rows that see it: a NaN or infinity in a
  * query makes its row NaN, in a key every row that sees the key, in element d of a
  * value element d of every row that sees the value; no other output changes.
- * T, heads * head_dim and the strides are below 2^30, B below 2^24; T * heads
- * below 2^31. out must not alias an input.
+ * T, heads * head_dim and the strides are below 2^30, and
+ * (T / 32 + B) * heads below 2^24. out must not alias an input.
  */
 int wq_attn_prefill(const float *q, int64_t q_stride, const float *k, int64_t k_stride,
                     const float *v, int64_t v_stride, int64_t T, const int32_t *cu, int64_t B,
@@ -362,7 +362,7 @@ typedef struct wq_kv_cache {
  * tokens sent to one row (a page listed twice) leave codes and scales of
  * either, block by block. A block that holds a NaN or an infinity, or whose
  * scale would pass binary16's range (max |x| / 7 rounds above 65504), is stored
- * as a NaN scale with codes 0, so it reads back as NaN. T * kv_heads below 2^31.
+ * as a NaN scale with codes 0, so it reads back as NaN. T * kv_heads below 2^27.
  */
 int wq_kv_append(const wq_kv_cache *cache, const float *k, int64_t k_stride, const float *v, int64_t v_stride,
                  int64_t T, const int32_t *cu, const int32_t *start, int64_t B,
@@ -385,7 +385,7 @@ uint64_t wq_attn_decode_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t h
  * a length outside [0, 64 * max_pages], or a page outside [0, n_pages) among
  * those the length covers, gives rows of NaN for that sequence and reads
  * nothing outside the cache. Rows past lens[b] may hold anything.
- * B * heads * max_pages below 2^40.
+ * B * heads is below 2^24, max_pages below 2^25.
  */
 int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
                    const int32_t *lens, int64_t B, const int32_t *table, int64_t max_pages, float scale,

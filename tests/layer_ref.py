@@ -60,11 +60,14 @@ def bound(sums, n, d):
     Weights and values: two parts each (3 2^-22), one fp32 rounding per
     partial sum (n 3 / 16 of the product, n / 2 of the weight sum), 8 for the
     normalisation, rescaling and final division; values
-    far below the largest one of the head keep an absolute error of 2^-36 of it.
+    far below the largest one of the head keep an absolute error of 2^-36 of it,
+    and every weight one of 2^-37 of the largest: a weight of 1 is held as 2^12
+    or more, in parts that go down to 2^-24, off by half of that, so n keys
+    may add n 2^-37 of the largest value.
     """
     logit = 2.0 * (3 * 2.0 ** -22 + (3 * d / 16 + 4) * U32)
     value = 3 * 2.0 ** -22 + 2.0 ** -21 + (3 * n / 16 + n / 2 + 8) * U32
-    return logit * sums[1] + value * sums[0] + 2.0 ** -36 * sums[2] + 1e-44
+    return logit * sums[1] + value * sums[0] + (2.0 ** -36 + n * 2.0 ** -37) * sums[2] + 1e-44
 
 
 def quantize(x):

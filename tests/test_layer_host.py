@@ -32,7 +32,7 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, T=0) == OK and _prefill(lib, B=0) == OK
     assert _prefill(lib, T=0, q=None, k=None, v=None, out=None, cu=None, ws=None) == OK
     for bad in (dict(D=96), dict(D=0), dict(H=15), dict(H=0), dict(Hk=0), dict(H=2048, Hk=1025), dict(T=-1), dict(B=-1),
-                dict(T=1 << 30), dict(B=1 << 24), dict(T=1 << 28, H=16), dict(qs=2047), dict(qs=2050), dict(ks=1020),
+                dict(T=1 << 30), dict(B=1 << 24), dict(T=1 << 25, H=16), dict(T=8, B=1 << 20), dict(qs=2047), dict(qs=2050), dict(ks=1020),
                 dict(vs=1 << 30), dict(os=1024)):
         assert _prefill(lib, **bad) == SHAPE, bad
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(cu=None)):
@@ -71,7 +71,7 @@ def test_append_refusals(lib):
     assert lib.wq_kv_append(None, FAKE, 1024, FAKE, 1024, 8, FAKE, FAKE, 2, FAKE, 4, None) == NULL
     for bad in (dict(head_dim=32), dict(kv_heads=0), dict(n_pages=-1), dict(n_pages=1 << 31)):
         assert _append(lib, _cache(**bad)) == SHAPE, bad
-    for bad in (dict(T=-1), dict(T=1 << 30), dict(T=1 << 28), dict(B=-1), dict(W=-1), dict(W=1 << 25), dict(ks=1000),
+    for bad in (dict(T=-1), dict(T=1 << 30), dict(T=1 << 24), dict(B=-1), dict(W=-1), dict(W=1 << 25), dict(ks=1000),
                 dict(vs=1026)):
         assert _append(lib, **bad) == SHAPE, bad
     for bad in (dict(k=None), dict(v=None), dict(cu=None), dict(table=None)):
@@ -96,7 +96,7 @@ def test_decode_refusals(lib):
     for bad in (dict(head_dim=256), dict(kv_heads=3), dict(n_pages=-1)):
         assert _decode(lib, _cache(**bad)) == SHAPE, bad
     for bad in (dict(H=12), dict(H=0), dict(B=-1), dict(W=-1), dict(W=1 << 25), dict(qs=1024), dict(os=2046),
-                dict(B=1 << 23, H=256, qs=1 << 15, os=1 << 15), dict(B=1 << 16, H=16, W=1 << 21)):
+                dict(B=1 << 16, H=256, qs=1 << 15, os=1 << 15), dict(B=1 << 20, H=16)):
         assert _decode(lib, **bad) == SHAPE, bad
     for bad in (dict(q=None), dict(lens=None), dict(out=None), dict(table=None)):
         assert _decode(lib, **bad) == NULL, bad

@@ -10,6 +10,7 @@ namespace {
 
 constexpr int64_t kLim = (int64_t)1 << 30;        // tokens, rows, strides
 constexpr int64_t kMaxSeqs = (int64_t)1 << 24;
+constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // workgroups of a launch
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline int hip_status(hipError_t e) { return e == hipSuccess ? WQ_OK : WQ_ERR_HIP; }
@@ -33,7 +34,8 @@ int check_prompt(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     int st = check_heads(heads, kv_heads, head_dim);
     if (st) return st;
     if (T < 0 || T >= kLim || B < 0 || B >= kMaxSeqs) return WQ_ERR_SHAPE;
-    if (T * heads >= (int64_t)1 << 31) return WQ_ERR_SHAPE;
+    // workgroups of at most 256 threads, below 2^32 threads in all
+    if ((T / 32 + B) * heads >= kMaxGroups) return WQ_ERR_SHAPE;
     return WQ_OK;
 }
 
@@ -63,9 +65,7 @@ int check_decode(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, i
     int st = check_heads(heads, kv_heads, head_dim);
     if (st) return st;
     if (B < 0 || B >= kMaxSeqs || max_pages < 0 || max_pages >= (int64_t)1 << 25) return WQ_ERR_SHAPE;
-    // below 2^40, without overflow: each factor is below 2^30
-    if (B * heads >= (int64_t)1 << 31) return WQ_ERR_SHAPE;
-    if (max_pages > 0 && B * heads >= (((int64_t)1 << 40) + max_pages - 1) / max_pages) return WQ_ERR_SHAPE;
+    if (B * heads >= kMaxGroups) return WQ_ERR_SHAPE;
     return WQ_OK;
 }
 
@@ -114,7 +114,7 @@ int wq_kv_append(const wq_kv_cache *cache, const float *k, int64_t k_stride, con
 {
     int st = check_cache(cache, B, max_pages);
     if (st) return st;
-    if (T < 0 || T >= kLim || T * cache->kv_heads >= (int64_t)1 << 31) return WQ_ERR_SHAPE;
+    if (T < 0 || T >= kLim || T * cache->kv_heads >= (int64_t)1 << 27) return WQ_ERR_SHAPE;
     if (T == 0 || B == 0) return WQ_OK;
     if ((st = check_stride(k_stride, cache->kv_heads, cache->head_dim)) ||
         (st = check_stride(v_stride, cache->kv_heads, cache->head_dim)))
