@@ -93,8 +93,11 @@ def values(codes, scales):
     return codes.astype(np.float64) * np.repeat(scales.astype(np.float64), 32, -1)
 
 
-def decode(q, kval, vval, table, lens, scale):
-    """q [b, heads, d], kval and vval [pages, kv, PAGE, d] in float64."""
+def decode(q, kval, vval, vscale, table, lens, scale):
+    """q [b, heads, d], kval and vval [pages, kv, PAGE, d] in float64, vscale the
+    scales of vval [pages, kv, PAGE, d / 32]. The largest value of a head is
+    taken as 16 of its largest scale: weights times scales are held against the
+    power of two above the largest scale (at most twice it), and codes reach 8."""
     q = q.astype(np.float64)
     out = np.zeros(q.shape)
     sums = np.zeros((3,) + q.shape)
@@ -107,10 +110,11 @@ def decode(q, kval, vval, table, lens, scale):
         for j in range(kv):
             kk = kval[ids, j].reshape(-1, q.shape[2])[:n]
             vv = vval[ids, j].reshape(-1, q.shape[2])[:n]
+            sc = vscale[ids, j].astype(np.float64).reshape(-1, q.shape[2] // 32)[:n]
             mine = slice(j * group, (j + 1) * group)
             o, pv, first = _attend(q[b, mine], kk, vv, scale, np.ones((group, n), bool))
             out[b, mine] = o
-            sums[0, b, mine], sums[1, b, mine], sums[2, b, mine] = pv, first, np.abs(vv).max()
+            sums[0, b, mine], sums[1, b, mine], sums[2, b, mine] = pv, first, 16 * float(sc.max())
     return out, sums
 
 

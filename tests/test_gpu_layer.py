@@ -298,7 +298,7 @@ def test_append_drops_rows_without_a_page():
 # ------------------------------------------------------------------ decode attention
 def check_decode(out, q, host, table, lens, scale, what=""):
     kval, vval = ref.values(*host[:2]), ref.values(*host[2:])
-    want, sums = ref.decode(q, kval, vval, table, lens, scale)
+    want, sums = ref.decode(q, kval, vval, host[3], table, lens, scale)
     got = out.cpu().numpy().astype(np.float64)
     lim = ref.bound(sums, max(lens), q.shape[2])
     err = np.abs(got - want)
@@ -446,7 +446,7 @@ def test_decode_non_finite_data():
         out = torch.full(q.shape, 0.0, device="cuda")
         wqa.attn_decode(dev(qq), cache_on(host), dev(table), dev(np.array(lens, np.int32)), out=out)
         got = out.cpu().numpy()[0]
-        want, sums = ref.decode(q, ref.values(*clean[:2]), ref.values(*clean[2:]), table, lens, d ** -0.5)
+        want, sums = ref.decode(q, ref.values(*clean[:2]), ref.values(*clean[2:]), clean[3], table, lens, d ** -0.5)
         lim = ref.bound(sums, 90, d)[0]
         assert np.isnan(got[hit]).all(), which
         assert (np.abs(got - want[0])[~hit] <= lim[~hit]).all(), which
