@@ -83,35 +83,43 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 // bytes a value pair of k and v, read once for all query heads that share it.
 //
 // A wavefront walks tiles of 64 tokens (a page of one key/value head), copied
-// one tile ahead into its own LDS by direct-to-LDS loads. All arithmetic on
-// codes is on the matrix cores, 16 x 16 x 32, whose 32 is one quantization
-// block or 32 tokens:
-//   scores   A = k codes (16 tokens x one block), B = q, 16 columns. q is split
-//     into two binary16 parts; a column is (part, block of BC, head of H), zero
-//     outside its block, so that one chain of BC products gives BC blocks'
-//     partial sums side by side. Each lane then scales its 4 tokens by its
-//     block's scale and the columns of a head are added by cross-lane moves.
-//   output   A = weights p_u s_u (16 rows (part, block of BC, head of H) x 32
-//     tokens): every lane forms the weight for its own block's scales and keeps its
-//     own part of it, where the scores left the token; B = v codes. Only the
-//     rows of a column's own block are used at the end.
-// BC * H = 8: few heads put blocks side by side, so that no lane repeats
-// another's scaling; more heads take that room.
+// into its own LDS by direct-to-LDS loads. All arithmetic on codes is on the
+// matrix cores, 16 x 16 x 32, whose 32 is one quantization block or 32 tokens,
+// with the query heads' side split into two binary16 parts (22 bits):
+//   scores   A = q, 16 rows (part, head of H, block of BC), zero outside the
+//     row's block, B = k codes (one block x 16 tokens): a chain of BC products
+//     gives BC blocks' partial sums side by side. A lane holds one token and the
+//     BC blocks of H / 2 heads, scales and adds them, and exchanges the part
+//     with the lane 32 away: a score per lane, none computed twice over.
+//   output   A = weights p_u s_u, rows as above (each block of the row's BC has
+//     its own scale), 32 tokens; B = v codes. Every lane makes its token's 4 rows
+//     and they change sides through 2 KiB of LDS (ds_read_b64_tr_b16). Only the
+//     columns of a row's own block are used at the end.
+// BC H = 8: few heads put blocks side by side, so that a lane has more to do per
+// token; more heads take that room.
 //
-// Codes become binary16 without conversions. k: the offset code (c + 8) as the
-// low mantissa bits of a subnormal, (c + 8) 2^-24 or 16 times that (q carries
-// 1/16 there), 5 operations for 8 codes; the chain starts at -8 2^-24 sum q, so
-// the offset costs nothing (the matrix cores keep subnormals). v: the same
-// would cancel a sum that grows with the length, so its codes are made exact
-// signed ones, (1024 + 8 + c) - 1032. v is wanted with tokens along
-// the lane's registers: ds_read_b64_tr_b4 transposes 16 x 16 codes on the way.
+// Codes become exact binary16 values by the mantissa of 1024: (1024 + 8 + c) -
+// 1032. (Offset codes as subnormals, (c + 8) 2^-24 with the offset's share
+// taken off the sum, need 5 operations for 8 codes instead of 9, but the matrix
+// cores' sums of the larger products cost three bits: error 2.4e-6 against
+// 4e-7.) v is wanted with tokens along the lane's registers:
+// ds_read_b64_tr_b4 transposes 16 x 16 codes on the way.
 //
 // The weights carry 2^kWeightBits over the largest value scale seen (v_exp), so
 // both binary16 parts stay normal; m moves only when a score passes it by
-// kSlack. The longest sequence decides how many workgroups share one (host),
-// every workgroup takes `chunk` tokens, and a second kernel joins them.
+// kSlack.
+//
+// One buffer each for k and v per wavefront: the copies of the next k go out
+// when the scores are done with this one, those of v after the output, so that
+// 12 wavefronts of 11 KiB share a compute unit's LDS.
+//
+// Lengths are device data, so the split is made on the device: every workgroup
+// adds up the lengths, cuts the sequences into equal chunks that fill the card
+// once and finds its own; a second kernel joins the chunks in order.
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
 
 constexpr int kDecodeWaves = 4;
@@ -124,38 +132,39 @@ constexpr int kMinScaleExp = -24;                      // 2^-24 is binary16's sm
 
 __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// Sum over the 16 lanes' columns of one head: c = part * 8 + bc * H + h.
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x)
+// x plus the value 32 lanes away.
+__device__ __forceinline__ float add_halves(float x)
 {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+    const uint32_t v = __builtin_bit_cast(uint32_t, x);
+    const auto both = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const uint32_t lo = both[0], hi = both[1];       // (a bit cast of a vector's element takes element 0)
+    return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
 }
-template <int H>
-__device__ __forceinline__ float add_columns(float x)
+
+// Transposed LDS reads, with their wait. (As builtins they make the compiler
+// wait for every direct-to-LDS copy under way, also those into other buffers.)
+// Four tokens of 16 rows each, 512 bytes apart.
+__device__ __forceinline__ void read_rows(const uint8_t *p, h4 &a, h4 &b, h4 &c, h4 &d)
 {
-    x += dpp<0x128>(x);                      // row_ror:8, the other part
-    if constexpr (H <= 4) x += dpp<0x124>(x);      // row_ror:4
-    if constexpr (H <= 2) x += dpp<0x4E>(x);       // quad_perm 2,3,0,1
-    return x;
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
+    asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:512\n\t"
+                 "ds_read_b64_tr_b16 %2, %4 offset:1024\n\tds_read_b64_tr_b16 %3, %4 offset:1536\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d) : "v"(at) : "memory");
+}
+// 16 tokens of 16 values each, and of the next 16 values.
+__device__ __forceinline__ void read_codes(const uint8_t *p, i2 &a, i2 &b)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
+    asm volatile("ds_read_b64_tr_b4 %0, %2\n\tds_read_b64_tr_b4 %1, %2 offset:8\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b) : "v"(at) : "memory");
 }
 
 // 8 codes of a dword, in the order of nibbles 0 4 1 5 2 6 3 7.
 __device__ __forceinline__ int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
 
-// Offset codes (c + 8) 2^-24; the pairs of nibbles 1 and 3 come 16 times larger.
-__device__ __forceinline__ h8 k_codes(uint32_t x)
-{
-    u4 r;
-    const uint32_t y = x >> 8;
-    r.x = (x & 0x000F000Fu) ^ 0x00080008u;
-    r.y = (x & 0x00F000F0u) ^ 0x00800080u;
-    r.z = (y & 0x000F000Fu) ^ 0x00080008u;
-    r.w = (y & 0x00F000F0u) ^ 0x00800080u;
-    return __builtin_bit_cast(h8, r);
-}
-
-// Signed codes.
-__device__ __forceinline__ h8 v_codes(uint32_t x)
+// The codes of a dword as exact binary16 values.
+__device__ __forceinline__ h8 codes8(uint32_t x)
 {
     const h2 off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
     const h2 off16 = {(_Float16)-72.0f, (_Float16)-72.0f}, inv16 = {(_Float16)0.0625f, (_Float16)0.0625f};
@@ -167,53 +176,155 @@ __device__ __forceinline__ h8 v_codes(uint32_t x)
     return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-struct DecodePlan {
-    int64_t chunk;           // tokens of a workgroup, multiple of kDecodeStep
-    int64_t splits;          // workgroups of the longest possible sequence
+// ---- how sequences are cut (host: decode_ws_bytes and the launch sizes agree with it)
+// A step is 4 tiles, one per wavefront. Sequences are cut into chunks of equally
+// many steps, as few as give about kFill workgroups in all (4 on each of 256
+// compute units). Cutting needs every workgroup to look at all lengths, so it
+// is left out for many sequences (they fill the card by themselves) and where
+// no sequence can be longer than a step.
+constexpr int kFill = 1024;
+constexpr int kCutMaxSeqs = 512;
+
+__host__ __device__ inline int head_groups(int heads, int kv_heads) { return (heads / kv_heads + kMaxGroup - 1) / kMaxGroup; }
+__host__ __device__ inline bool cut_sequences(int64_t B, int64_t max_pages)
+{
+    return B <= kCutMaxSeqs && max_pages > kDecodeWaves;
+}
+// Most chunks times workgroups per chunk: sum ceil(n_b / c) <= sum n_b / c + B, c >= sum n_b per / kFill.
+__host__ __device__ inline int64_t max_items(int64_t B, int64_t per_chunk) { return kFill + B * per_chunk; }
+
+struct Cut {
+    int b;               // the sequence, -1: none
+    int first;           // number of its first chunk among all
+    int chunks;          // of the sequence
+    int64_t steps;       // of a chunk, below 2^31
 };
+
+__device__ __forceinline__ int steps_of(const DecodeArgs &a, int b)
+{
+    const int64_t len = b < a.B ? a.lens[b] : 0;
+    return len < 0 || len > a.max_pages * kTile ? 0 : (int)((len + kDecodeStep - 1) / kDecodeStep);
+}
+
+// The cut, and the sequence that holds chunk `chunk` (or the one of number seq
+// when seq >= 0). A whole wavefront calls it.
+__device__ __forceinline__ Cut find_cut(const DecodeArgs &a, int per_chunk, int64_t chunk, int seq)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        int n = steps_of(a, b0 + lane);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
+        total += n;
+    }
+    const int64_t steps = total * per_chunk <= kFill ? 1 : (total * per_chunk + kFill - 1) / kFill;
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        const int n = steps_of(a, b0 + lane);
+        const int mine = (int)((n + steps - 1) / steps);
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(upto, o);
+            if (lane >= o) upto += x;
+        }
+        const int first = before + upto - mine;
+        const bool hit = seq >= 0 ? b0 + lane == seq : chunk >= first && chunk < first + mine;
+        const uint64_t who = __ballot(hit);
+        if (who) {
+            const int l = __ffsll((unsigned long long)who) - 1;
+            return {b0 + l, __shfl(first, l), __shfl(mine, l), steps};
+        }
+        before += __shfl(upto, 63);
+    }
+    return {-1, 0, 0, steps};
+}
 
 constexpr int kPartialExtra = 2;             // a partial result: D values, then m and l
 
-template <int D, int H>
-__global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs a, int64_t chunk, int splits, int groups,
-                                                                      float c_man, int c_exp)
+template <int D, int H, int WPS>
+__global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeArgs a, int groups, bool cut, float c_man, int c_exp)
 {
-    constexpr int NB = D / 32, BC = 8 / H < NB ? 8 / H : NB, R = NB / BC;      // blocks, of them side by side, chains
-    static_assert(BC * H <= 8 && BC * R == NB, "columns");
-    constexpr int kCodeBytes = kTile * D / 2, kScaleBytes = kTile * NB * 2;
-    constexpr int kBuf = 2 * kCodeBytes + 2 * kScaleBytes;
-    static_assert(kBuf >= 16 * D * 4, "the wave's result fits its buffer");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kDecodeWaves][2][kBuf];
+    constexpr int NB = D / 32, BC = 8 / H, R = NB / BC;          // blocks, of them side by side, chains
+    constexpr int HL = H / 2;                                    // heads of a lane's scores
+    static_assert(BC * H == 8 && BC * R == NB, "rows");
+    constexpr int kCodeBytes = kTile * D / 2, kScaleBytes = kTile * NB * 2, kHalf = kCodeBytes + kScaleBytes;
+    constexpr int kWeightBytes = kTile * 32;
+    static_assert(2 * kHalf >= 16 * D * 4, "the wave's result fits its buffers");
+    typedef _Float16 hb __attribute__((ext_vector_type(NB)));    // a token's scales
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kDecodeWaves][2 * kHalf + kWeightBytes];
     __shared__ float state[kDecodeWaves][H][2];
-    const int kv = a.cache.kv_heads, group = a.heads / kv;
-    int id = blockIdx.x;
-    const int kh = id % kv;
-    id /= kv;
-    const int hg = id % groups;
-    id /= groups;
-    const int split = id % splits, b = id / splits;
+    const int kv = a.cache.kv_heads, group = a.heads / kv, per_chunk = kv * groups;
+    const int kh = blockIdx.x % kv, hg = blockIdx.x / kv % groups;
+    int b = blockIdx.x / per_chunk, chunks = 1;
+    int64_t t0 = 0, span = a.max_pages * kTile;
+    if (cut) {
+        const Cut at = find_cut(a, per_chunk, b, -1);
+        const int seq = __builtin_amdgcn_readfirstlane(at.b);
+        if (seq < 0) return;
+        span = (int64_t)__builtin_amdgcn_readfirstlane((int)at.steps) * kDecodeStep;
+        t0 = (b - __builtin_amdgcn_readfirstlane(at.first)) * span;
+        b = seq;
+        chunks = __builtin_amdgcn_readfirstlane(at.chunks);
+    }
     const int per = (group + groups - 1) / groups;               // heads of this workgroup: per or fewer
     const int head0 = kh * group + hg * per, heads = group - hg * per < per ? group - hg * per : per;
-    const int64_t len = a.lens[b], cap = a.max_pages * kTile;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool bad_len = len < 0 || len > cap;
-    const int64_t t0 = split * chunk;
-    if (splits > 1 && (bad_len || t0 >= len)) return;            // the join knows
-    if (bad_len || len == 0) {
+    const int64_t len = a.lens[b];
+    if (len <= 0 || len > a.max_pages * kTile) {                 // (not reached where sequences are cut)
         for (int i = tid; i < heads * D; i += 64 * kDecodeWaves)
-            a.out[(int64_t)b * a.out_stride + head0 * D + i] = bad_len ? __builtin_nanf("") : 0.0f;
+            a.out[(int64_t)b * a.out_stride + head0 * D + i] = len == 0 ? 0.0f : __builtin_nanf("");
         return;
     }
-    const int64_t end = len < t0 + chunk ? len : t0 + chunk;
+    const int64_t end = len < t0 + span ? len : t0 + span;
     const int tile0 = (int)(t0 / kTile) + wave, tile_end = (int)((end + kTile - 1) / kTile);
     const int32_t *pages = a.table + (int64_t)b * a.max_pages;
+    const int c = lane & 15, g = lane >> 4;
 
-    const int c = lane & 15, g = lane >> 4, part = c >> 3, h = c & (H - 1), bc = (c / H) & (BC - 1);
-    // the query: column c holds part `part` of head h, its blocks r BC + bc
+    // copies of a tile: 16-byte pieces (a block of a token each), swizzled by token so that the reads below
+    // take 64 banks
+    const int64_t rows = (int64_t)kv * kTile;
+    bool bad = false;
+    auto row_of = [&](int tile) -> int64_t {
+        int page = pages[tile];
+        if (page < 0 || page >= a.cache.n_pages) {
+            bad = true;
+            page = 0;
+        }
+        return (int64_t)page * rows + (int64_t)kh * kTile;
+    };
+    auto copy = [&](const void *codes, const uint16_t *scales, int64_t row, uint8_t *dst, bool values) {
+        const uint8_t *src = (const uint8_t *)codes + row * (D / 2);
+#pragma unroll
+        for (int i = 0; i < kCodeBytes / 1024; ++i) {
+            const int p = i * 64 + lane, t = p / NB, s = p % NB;
+            const int blk = s ^ ((t >> (values ? 4 : D == 128 ? 2 : 3)) & (NB - 1));
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(src + t * (D / 2) + blk * 16),
+                                             (__attribute__((address_space(3))) void *)(dst + i * 1024), 16, 0, kNonTemporal);
+        }
+        if (lane < kScaleBytes / 16)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((const uint8_t *)(scales + row * NB) + lane * 16),
+                                             (__attribute__((address_space(3))) void *)(dst + kCodeBytes), 16, 0, kNonTemporal);
+    };
+    constexpr int kCopies = kCodeBytes / 1024 + 1;               // instructions of one copy
+    uint8_t *kbuf = lds[wave], *vbuf = kbuf + kHalf, *pbuf = vbuf + kHalf;
+    const bool any_page = a.cache.n_pages > 0;
+    if (tile0 < tile_end) {
+        const int64_t row = row_of(tile0);
+        if (any_page) {
+            copy(a.cache.kq, a.cache.ks, row, kbuf, false);
+            copy(a.cache.vq, a.cache.vs, row, vbuf, true);
+        }
+    }
+
+    // the query: row n = c of the operand is part c / 8 of head (c / 4 % 2) HL + c % 4 / BC, and of blocks
+    // r BC + c % BC
     h8 q[NB];
-    float f;                                                     // scores in powers of two = sums times this
+    float f[HL];                                                 // scores in powers of two = sums times this
     {
-        const bool live = h < heads && (c & 7) < BC * H;
+        const int part = c >> 3, bc = c & (BC - 1), h = ((c >> 2) & 1) * HL + (c & 3) / BC;
+        const bool live = h < heads;
         const float *src = a.q + (int64_t)b * a.q_stride + (head0 + (live ? h : 0)) * D;
         float x[R][8], top = 0.0f;
 #pragma unroll
@@ -225,10 +336,12 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
                 if (y <= 3.4028235e38f) top = fmaxf(top, y);
             }
 #pragma unroll
-        for (int o = H; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+        for (int o = 1; o < 64; o <<= 1)
+            if (o < BC || o >= 16) top = fmaxf(top, __shfl_xor(top, o));
         const int e2 = top > 0.0f ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-        const int fe = 24 + c_exp - e2;
-        f = ldexpf(1.0f, fe > 127 ? 127 : fe);
+        const float fe = ldexpf(1.0f, c_exp - e2 > 127 ? 127 : c_exp - e2);
+#pragma unroll
+        for (int i = 0; i < HL; ++i) f[i] = __shfl(fe, 4 * (g & 1) + i * BC);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             h8 v;
@@ -237,185 +350,174 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
                 float y = ldexpf(x[r][e], e2) * c_man;
                 asm("" : "+v"(y));                               // one rounding of y, whoever uses it
                 const _Float16 hi = (_Float16)y;
-                const float z = part ? y - (float)hi : (float)hi;
-                v[e] = (_Float16)((nibble_of(e) & 1) ? z * 0.0625f : z);
+                v[e] = part ? (_Float16)(y - (float)hi) : hi;
             }
 #pragma unroll
             for (int i = 0; i < BC; ++i) q[r * BC + i] = i == bc ? v : h8{};
         }
     }
-    f4 start[R];                                                 // minus the codes' offset
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        f4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < BC; ++i) z = mfma16(k_codes(0), q[r * BC + i], z);
-        start[r] = -z;
-    }
 
-    // copies of a tile: 16-byte pieces (a block of a token each), swizzled by token so that the reads below
-    // take 64 banks; both kinds of scales in one instruction
-    const int64_t rows = (int64_t)kv * kTile;
-    bool bad = false;
-    auto copy = [&](int tile, int buf) {
-        int page = pages[tile];
-        if (page < 0 || page >= a.cache.n_pages) {
-            bad = true;
-            page = 0;
-            if (a.cache.n_pages == 0) return;
-        }
-        const int64_t row = (int64_t)page * rows + (int64_t)kh * kTile;
-        uint8_t *dst = lds[wave][buf];
-        const uint8_t *kq = (const uint8_t *)a.cache.kq + row * (D / 2), *vq = (const uint8_t *)a.cache.vq + row * (D / 2);
-#pragma unroll
-        for (int i = 0; i < kCodeBytes / 1024; ++i) {
-            const int p = i * 64 + lane, t = p / NB, s = p % NB;
-            const int bk = D == 128 ? s ^ ((t >> 2) & 3) : s ^ ((t >> 3) & 1);
-            const int bv = s ^ ((t >> 4) & (NB - 1));
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(kq + t * (D / 2) + bk * 16),
-                                             (__attribute__((address_space(3))) void *)(dst + i * 1024), 16, 0, kNonTemporal);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(vq + t * (D / 2) + bv * 16),
-                                             (__attribute__((address_space(3))) void *)(dst + kCodeBytes + i * 1024), 16, 0, kNonTemporal);
-        }
-        constexpr int kPieces = kScaleBytes / 16;                // of each kind
-        const uint8_t *sc = lane < kPieces ? (const uint8_t *)(a.cache.ks + row * NB) + lane * 16
-                                           : (const uint8_t *)(a.cache.vs + row * NB) + (lane - kPieces) * 16;
-        if (lane < 2 * kPieces)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)sc,
-                                             (__attribute__((address_space(3))) void *)(dst + 2 * kCodeBytes), 16, 0, kNonTemporal);
-    };
-    constexpr int kCopies = 2 * (kCodeBytes / 1024) + 1;
-
+    // From here on a lane is token 16 u + c of a tile, and the 4 rows 4 g + i: part g / 2, heads (g % 2) HL + i / BC
     f4 acc[D / 16];
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) acc[n] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -3.0e38f, l = 0.0f;
+    float m[HL], l[HL];
+#pragma unroll
+    for (int i = 0; i < HL; ++i) {
+        m[i] = -3.0e38f;
+        l[i] = 0.0f;
+    }
     int v_exp = kMinScaleExp;
-    // tokens of the transposed reads: register nibble n of dword x is token 16 (2 x + e / 4) + 4 g + e % 4,
-    // nibble_of(e) = n, so that weights stay where the scores came out
+    const float minus = g >> 1 ? -1.0f : 0.0f;                   // this lane keeps the second part of a weight
+    // Tokens of the output's operands: element e of product x is token 16 (2 x + e / 4) + 4 g + e % 4. The
+    // codes' transposed read puts row c of the lanes into nibble c % 8 of dword c / 8, nibble_of(e) = c % 8.
     const int vn = c & 7, ve = vn < 4 ? 2 * vn : 2 * (vn - 4) + 1;
     const int vt = 16 * (2 * (c >> 3) + (ve >> 2)) + 4 * g + (ve & 3);
+    uint8_t *const pw = pbuf + c * 32 + g * 8;                                    // weights are written by token
+    uint8_t *const pr = pbuf + (4 * g + (c >> 2)) * 32 + (c & 3) * 8;             // and read by row
 
-    if (tile0 < tile_end) copy(tile0, 0);
-    int buf = 0;
-    for (int tile = tile0; tile < tile_end; tile += kDecodeWaves, buf ^= 1) {
+    for (int tile = tile0; tile < tile_end; tile += kDecodeWaves) {
         const bool more = tile + kDecodeWaves < tile_end;
-        if (more) {
-            copy(tile + kDecodeWaves, buf ^ 1);
-            __builtin_amdgcn_s_waitcnt(0x0F70 | kCopies);        // vmcnt(kCopies): this tile has arrived
-        } else {
-            __builtin_amdgcn_s_waitcnt(0x0F70);                  // vmcnt(0)
-        }
+        int64_t next = 0;
+        if (more) next = row_of(tile + kDecodeWaves);
+        __builtin_amdgcn_s_waitcnt(0x0F70 | kCopies);            // vmcnt(kCopies): k has arrived, v may be on its way
         asm volatile("" ::: "memory");
-        const uint8_t *base = lds[wave][buf];
-        const _Float16 *ks = (const _Float16 *)(base + 2 * kCodeBytes), *vs = ks + kTile * NB;
         const int left = (int)(len - (int64_t)tile * kTile);     // tokens of the tile that count
-        float x[16];
+        float x[HL][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             const int t = 16 * u + c;
+            const hb ks = *(const hb *)(kbuf + kCodeBytes + t * NB * 2);
+            float s[HL];
+#pragma unroll
+            for (int i = 0; i < HL; ++i) s[i] = 0.0f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                f4 z = start[r];
+                f4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < BC; ++i) {
-                    const int blk = r * BC + i, sw = D == 128 ? blk ^ ((t >> 2) & 3) : blk ^ ((t >> 3) & 1);
-                    z = mfma16(k_codes(*(const uint32_t *)(base + t * (D / 2) + sw * 16 + g * 4)), q[blk], z);
+                    const int blk = r * BC + i, sw = blk ^ ((t >> (D == 128 ? 2 : 3)) & (NB - 1));
+                    z = mfma16(q[blk], codes8(*(const uint32_t *)(kbuf + t * (D / 2) + sw * 16 + g * 4)), z);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = fmaf(z[i], (float)ks[(16 * u + 4 * g + i) * NB + r * BC + bc], s[i]);
+                for (int i = 0; i < 4; ++i) s[i / BC] = fmaf(z[i], (float)ks[r * BC + i % BC], s[i / BC]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * u + i] = add_columns<BC == 1 ? 8 : 8 / BC>(s[i]);
-        }
-        float w[R][16];                                          // value scales of this lane's blocks
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[r][i] = (float)vs[(16 * (i >> 2) + 4 * g + (i & 3)) * NB + r * BC + bc];
-        if (left < kTile) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (16 * (i >> 2) + 4 * g + (i & 3) >= left) {
-                    x[i] = -__builtin_inff();
-#pragma unroll
-                    for (int r = 0; r < R; ++r) w[r][i] = 0.0f;
-                }
-        }
-        float top = x[0], vtop = w[0][0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) vtop = fmaxf(vtop, w[r][i]);
-        top *= f;
-        if (__any(top > m + kSlack || vtop > ldexpf(1.0f, v_exp))) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) vtop = fmaxf(vtop, __shfl_xor(vtop, o));
-            const float mn = fmaxf(m, top);
-            const int en = vtop > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vtop) : v_exp;
-            const float by = ldexpf(__builtin_amdgcn_exp2f(m - mn), v_exp - en);
-            l *= by;
-            // the factor of row 4 g + i of the output belongs to the lanes of that column
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float rb = __shfl(by, 4 * g + i);
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n) acc[n][i] *= rb;
-            }
-            m = mn;
-            v_exp = en;
-        }
-        const float up = (float)(kWeightBits - v_exp) - m;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], f, up));
-            l += x[i];
-        }
-        h8 wp[R][2];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float y = x[i] * w[r][i];
-                asm("" : "+v"(y));
-                const _Float16 hi = (_Float16)y;
-                wp[r][i >> 3][i & 7] = part ? (_Float16)(y - (float)hi) : hi;
-            }
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-            const int blk = n >> 1, sw = blk ^ ((vt >> 4) & (NB - 1));
-            const i2 v = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                (__attribute__((address_space(3))) i2 *)(base + kCodeBytes + vt * (D / 2) + sw * 16 + (n & 1) * 8));
-            acc[n] = mfma16(wp[blk / BC][0], v_codes((uint32_t)v.x), acc[n]);
-            acc[n] = mfma16(wp[blk / BC][1], v_codes((uint32_t)v.y), acc[n]);
+            for (int i = 0; i < HL; ++i) x[i][u] = add_halves(s[i]);      // the other part is 32 lanes away
         }
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xC07F);                      // the reads are done: the buffer may be filled again
+        __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0): the reads of k are done
+        if (more && any_page) {
+            copy(a.cache.kq, a.cache.ks, next, kbuf, false);
+            __builtin_amdgcn_s_waitcnt(0x0F70 | kCopies);        // v has arrived
+        } else {
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+        }
+        asm volatile("" ::: "memory");
+        hb w[4];                                                 // value scales of the lane's tokens
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = *(const hb *)(vbuf + kCodeBytes + (16 * u + c) * NB * 2);
+        if (left < kTile) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (16 * u + c >= left) {
+                    w[u] = hb{};
+#pragma unroll
+                    for (int i = 0; i < HL; ++i) x[i][u] = -__builtin_inff();
+                }
+        }
+        hb wmax = __builtin_elementwise_max(__builtin_elementwise_max(w[0], w[1]), __builtin_elementwise_max(w[2], w[3]));
+        _Float16 vtop = wmax[0];
+#pragma unroll
+        for (int i = 1; i < NB; ++i) vtop = __builtin_fmaxf16(vtop, wmax[i]);
+        float top[HL];
+        bool raise = (float)vtop > ldexpf(1.0f, v_exp);
+#pragma unroll
+        for (int i = 0; i < HL; ++i) {
+            top[i] = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) * f[i];
+            raise |= top[i] > m[i] + kSlack;
+        }
+        if (__any(raise)) {
+            float vmax = (float)vtop;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, o));
+            const int en = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
+#pragma unroll
+            for (int i = 0; i < HL; ++i) {
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) top[i] = fmaxf(top[i], __shfl_xor(top[i], o));
+                const float mn = fmaxf(m[i], top[i]);
+                const float by = ldexpf(__builtin_amdgcn_exp2f(m[i] - mn), v_exp - en);
+                l[i] *= by;
+                m[i] = mn;
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                    for (int k = 0; k < BC; ++k) acc[n][i * BC + k] *= by;
+            }
+            v_exp = en;
+        }
+#pragma unroll
+        for (int i = 0; i < HL; ++i) {
+            const float up = (float)(kWeightBits - v_exp) - m[i];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x[i][u] = __builtin_amdgcn_exp2f(fmaf(x[i][u], f[i], up));
+                l[i] += x[i][u];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                h4 p;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y = x[i / BC][u] * (float)w[u][r * BC + i % BC];
+                    asm("" : "+v"(y));
+                    p[i] = (_Float16)fmaf(minus, (float)(_Float16)y, y);
+                }
+                *(h4 *)(pw + u * 512) = p;
+            }
+            h4 w0, w1, w2, w3;
+            read_rows(pr, w0, w1, w2, w3);
+            const h8 p0 = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
+            const h8 p1 = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+            for (int i = 0; i < BC; ++i) {
+                const int blk = r * BC + i, sw = blk ^ ((vt >> 4) & (NB - 1));
+                i2 x0, x1;
+                read_codes(vbuf + vt * (D / 2) + sw * 16, x0, x1);
+                acc[2 * blk] = mfma16(p0, codes8((uint32_t)x0.x), acc[2 * blk]);
+                acc[2 * blk + 1] = mfma16(p0, codes8((uint32_t)x1.x), acc[2 * blk + 1]);
+                acc[2 * blk] = mfma16(p1, codes8((uint32_t)x0.y), acc[2 * blk]);
+                acc[2 * blk + 1] = mfma16(p1, codes8((uint32_t)x1.y), acc[2 * blk + 1]);
+            }
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);                      // the reads of v are done
+        if (more && any_page) copy(a.cache.vq, a.cache.vs, next, vbuf, true);
     }
 
-    // join the waves: rows (part, bc, h) of a wave's result go through its buffer
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    l = ldexpf(l, v_exp - kWeightBits);
-    if (bad) l = __builtin_nanf("");
-    float *res = (float *)lds[wave][0];
-    __syncthreads();
+    // join the waves: the 16 rows of a wave's result go through its buffers
+    float *res = (float *)lds[wave];
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int n = 0; n < D / 16; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) res[(4 * g + i) * D + 16 * n + c] = ldexpf(acc[n][i], v_exp - kWeightBits);
-    if (lane < H) {
-        state[wave][lane][0] = m;
-        state[wave][lane][1] = l;
+#pragma unroll
+    for (int i = 0; i < HL; ++i) {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor(l[i], o);
+        if (c == 0 && g < 2) {
+            state[wave][g * HL + i][0] = m[i];
+            state[wave][g * HL + i][1] = bad ? __builtin_nanf("") : ldexpf(l[i], v_exp - kWeightBits);
+        }
     }
     __syncthreads();
     for (int i = tid; i < heads * D; i += 64 * kDecodeWaves) {
-        const int hh = i / D, d = i % D, row = ((d / 32) & (BC - 1)) * H + hh;
+        const int hh = i / D, d = i % D, rw = hh / HL * 4 + hh % HL * BC + ((d / 32) & (BC - 1));
         float mm = state[0][hh][0];
 #pragma unroll
         for (int w = 1; w < kDecodeWaves; ++w) mm = fmaxf(mm, state[w][hh][0]);
@@ -423,14 +525,14 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
 #pragma unroll
         for (int w = 0; w < kDecodeWaves; ++w) {
             const float by = __builtin_amdgcn_exp2f(state[w][hh][0] - mm);
-            const float *rw = (const float *)lds[w][0];
+            const float *rs = (const float *)lds[w];
             ll = fmaf(by, state[w][hh][1], ll);
-            o = fmaf(by, rw[row * D + d] + rw[(8 + row) * D + d], o);
+            o = fmaf(by, rs[rw * D + d] + rs[(8 + rw) * D + d], o);
         }
-        if (splits == 1) {
+        if (chunks == 1) {
             a.out[(int64_t)b * a.out_stride + head0 * D + i] = o / ll;
         } else {
-            float *p = (float *)a.ws + (((int64_t)b * a.heads + head0 + hh) * splits + split) * (D + kPartialExtra);
+            float *p = (float *)a.ws + ((int64_t)blockIdx.x * kMaxGroup + hh) * (D + kPartialExtra);
             p[d] = o;
             if (d == 0) {
                 p[D] = mm;
@@ -440,29 +542,56 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
     }
 }
 
-// Joins the partial results of a head's splits, in order.
+// Joins the chunks of a head in order; writes the rows of empty sequences and
+// of lengths out of range. D lanes add up a quarter of the chunks each.
+constexpr int kJoinParts = 4;
+constexpr int kJoinBlock = 256;              // chunks whose factors are held at once
+
 template <int D>
-__global__ __launch_bounds__(D) void join_kernel(DecodeArgs a, int64_t chunk, int splits)
+__global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int groups)
 {
-    const int b = blockIdx.x / a.heads, j = blockIdx.x % a.heads, d = threadIdx.x;
+    __shared__ float factor[kJoinBlock], red[kJoinParts][D + 1], top[D * kJoinParts / 64];
+    const int b = blockIdx.x / a.heads, j = blockIdx.x % a.heads, d = threadIdx.x % D, part = threadIdx.x / D;
     const int64_t len = a.lens[b];
     float *out = a.out + (int64_t)b * a.out_stride + j * D + d;
-    if (len < 0 || len > a.max_pages * kTile || len == 0) {
-        *out = len == 0 ? 0.0f : __builtin_nanf("");
+    if (len <= 0 || len > a.max_pages * kTile) {
+        if (part == 0) *out = len == 0 ? 0.0f : __builtin_nanf("");
         return;
     }
-    const int n = (int)((len + chunk - 1) / chunk);
-    const float *p = (const float *)a.ws + (int64_t)blockIdx.x * splits * (D + kPartialExtra);
+    const int kv = a.cache.kv_heads, group = a.heads / kv, per_chunk = kv * groups, per = (group + groups - 1) / groups;
+    const Cut at = find_cut(a, per_chunk, 0, b);
+    if (at.chunks == 1) return;                  // written already
+    const int kh = j / group, hg = j % group / per, hh = j % group % per;
+    const float *p = (const float *)a.ws +
+                     (((int64_t)at.first * per_chunk + hg * kv + kh) * kMaxGroup + hh) * (D + kPartialExtra);
+    const int64_t stride = (int64_t)per_chunk * kMaxGroup * (D + kPartialExtra);
     float m = -3.0e38f;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, p[i * (D + kPartialExtra) + D]);
+    for (int i = threadIdx.x; i < at.chunks; i += D * kJoinParts) m = fmaxf(m, p[i * stride + D]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < D * kJoinParts / 64; ++w) m = fmaxf(m, top[w]);
     float l = 0.0f, o = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        const float *s = p + i * (D + kPartialExtra);
-        const float by = __builtin_amdgcn_exp2f(s[D] - m);
-        l = fmaf(by, s[D + 1], l);
-        o = fmaf(by, s[d], o);
+    for (int i0 = 0; i0 < at.chunks; i0 += kJoinBlock) {
+        const int n = at.chunks - i0 < kJoinBlock ? at.chunks - i0 : kJoinBlock;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += D * kJoinParts) factor[i] = __builtin_amdgcn_exp2f(p[(i0 + i) * stride + D] - m);
+        __syncthreads();
+        if (d == 0)
+            for (int i = part; i < n; i += kJoinParts) l = fmaf(factor[i], p[(i0 + i) * stride + D + 1], l);
+#pragma unroll 8
+        for (int i = part; i < n; i += kJoinParts) o = fmaf(factor[i], p[(i0 + i) * stride + d], o);
     }
-    *out = o / l;
+    red[part][d] = o;
+    if (d == 0) red[part][D] = l;
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+        for (int w = 1; w < kJoinParts; ++w) o += red[w][d];
+        *out = o / (red[0][D] + red[1][D] + red[2][D] + red[3][D]);
+    }
 }
 
 }  // namespace
@@ -475,61 +604,36 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-namespace {
-
-int head_groups(int64_t heads, int64_t kv_heads) { return (int)((heads / kv_heads + kMaxGroup - 1) / kMaxGroup); }
-
-// Workgroups that the longest possible sequence is split over: enough to fill
-// the card with B such sequences (2 workgroups on each of 256 compute units, two
-// rounds of them to even out unequal lengths), at least kDecodeStep tokens each.
-DecodePlan plan_decode(int64_t B, int64_t heads, int64_t kv_heads, int64_t max_pages)
-{
-    const int64_t cap = max_pages * kTile, each = B * kv_heads * head_groups(heads, kv_heads);
-    int64_t want = 1024 / each;
-    if (want < 1) want = 1;
-    int64_t steps = (cap + kDecodeStep - 1) / kDecodeStep;
-    if (steps < 1) steps = 1;
-    if (want > steps) want = steps;
-    DecodePlan p;
-    p.chunk = (steps + want - 1) / want * kDecodeStep;
-    p.splits = (steps * kDecodeStep + p.chunk - 1) / p.chunk;
-    return p;
-}
-
-template <int D, int H>
-void run_decode(const DecodeArgs &a, const DecodePlan &p, hipStream_t stream)
-{
-    const int groups = head_groups(a.heads, a.cache.kv_heads);
-    int c_exp = 0;
-    const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);
-    const unsigned grid = (unsigned)((int64_t)a.B * a.cache.kv_heads * groups * p.splits);
-    decode_kernel<D, H><<<grid, 64 * kDecodeWaves, 0, stream>>>(a, p.chunk, (int)p.splits, groups, (float)(2.0 * c), c_exp - 1);
-}
-
-}  // namespace
-
 uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages)
 {
-    const DecodePlan p = plan_decode(B, heads, kv_heads, max_pages);
-    return p.splits == 1 ? 0 : (uint64_t)(B * heads * p.splits) * (uint64_t)(head_dim + kPartialExtra) * 4;
+    if (!cut_sequences(B, max_pages)) return 0;
+    const int64_t per_chunk = kv_heads * head_groups((int)heads, (int)kv_heads);
+    return (uint64_t)max_items(B, per_chunk) * kMaxGroup * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
 
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
 {
-    const DecodePlan p = plan_decode(a.B, a.heads, a.cache.kv_heads, a.max_pages);
-    const int group = a.heads / a.cache.kv_heads;
+    const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv);
+    const bool cut = cut_sequences(a.B, a.max_pages);
+    const unsigned grid = (unsigned)(cut ? max_items(a.B, (int64_t)kv * groups) : (int64_t)a.B * kv * groups);
+    int c_exp = 0;
+    const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
+    const float c_man = (float)(2.0 * c);
+    const int per = (group + groups - 1) / groups;
+    constexpr int T = 64 * kDecodeWaves;
     if (a.cache.head_dim == 128) {
-        if (group <= 2) run_decode<128, 2>(a, p, stream);
-        else if (group <= 4) run_decode<128, 4>(a, p, stream);
-        else run_decode<128, 8>(a, p, stream);
+        if (per <= 2) decode_kernel<128, 2, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        else if (per <= 4) decode_kernel<128, 4, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        else decode_kernel<128, 8, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
     } else {
-        if (group <= 4) run_decode<64, 4>(a, p, stream);
-        else run_decode<64, 8>(a, p, stream);
+        if (per <= 4) decode_kernel<64, 4, 4><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        else decode_kernel<64, 8, 4><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    if (a.cache.head_dim == 128) join_kernel<128><<<(unsigned)(a.B * a.heads), 128, 0, stream>>>(a, p.chunk, (int)p.splits);
-    else join_kernel<64><<<(unsigned)(a.B * a.heads), 64, 0, stream>>>(a, p.chunk, (int)p.splits);
+    if (e != hipSuccess || !cut) return e;
+    const unsigned jobs = (unsigned)(a.B * a.heads);
+    if (a.cache.head_dim == 128) join_kernel<128><<<jobs, 128 * kJoinParts, 0, stream>>>(a, groups);
+    else join_kernel<64><<<jobs, 64 * kJoinParts, 0, stream>>>(a, groups);
     return hipGetLastError();
 }
 
