@@ -109,9 +109,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 // both binary16 parts stay normal; m moves only when a score passes it by
 // kSlack.
 //
-// One buffer each for k and v per wavefront: the copies of the next k go out
-// when the scores are done with this one, those of v after the output, so that
-// 12 wavefronts of 11 KiB share a compute unit's LDS.
+// A tile goes from LDS to registers at once and the copies of the next tile
+// into the same LDS go out before anything is computed, so that copies are
+// under way all the time and 12 wavefronts of 11 KiB share a compute unit's LDS.
 //
 // Lengths are device data, so the split is made on the device: every workgroup
 // adds up the lengths, cuts the sequences into equal chunks that fill the card
@@ -141,9 +141,9 @@ __device__ __forceinline__ float add_halves(float x)
     return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
 }
 
-// Transposed LDS reads, with their wait. (As builtins they make the compiler
-// wait for every direct-to-LDS copy under way, also those into other buffers.)
-// Four tokens of 16 rows each, 512 bytes apart.
+// Transposed LDS read of four tokens of 16 rows each, 512 bytes apart, with its
+// wait. (As builtins these make the compiler wait for every direct-to-LDS copy
+// under way, also those into other buffers.)
 __device__ __forceinline__ void read_rows(const uint8_t *p, h4 &a, h4 &b, h4 &c, h4 &d)
 {
     const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
@@ -151,13 +151,6 @@ __device__ __forceinline__ void read_rows(const uint8_t *p, h4 &a, h4 &b, h4 &c,
                  "ds_read_b64_tr_b16 %2, %4 offset:1024\n\tds_read_b64_tr_b16 %3, %4 offset:1536\n\t"
                  "s_waitcnt lgkmcnt(0)"
                  : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d) : "v"(at) : "memory");
-}
-// 16 tokens of 16 values each, and of the next 16 values.
-__device__ __forceinline__ void read_codes(const uint8_t *p, i2 &a, i2 &b)
-{
-    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
-    asm volatile("ds_read_b64_tr_b4 %0, %2\n\tds_read_b64_tr_b4 %1, %2 offset:8\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(a), "=&v"(b) : "v"(at) : "memory");
 }
 
 // 8 codes of a dword, in the order of nibbles 0 4 1 5 2 6 3 7.
@@ -279,15 +272,16 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
     }
     const int64_t end = len < t0 + span ? len : t0 + span;
     const int tile0 = (int)(t0 / kTile) + wave, tile_end = (int)((end + kTile - 1) / kTile);
-    const int32_t *pages = a.table + (int64_t)b * a.max_pages;
+    // (constant address space: scalar loads, which wait for nothing else)
+    const __attribute__((address_space(4))) int32_t *pages =
+        (const __attribute__((address_space(4))) int32_t *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
     const int c = lane & 15, g = lane >> 4;
 
     // copies of a tile: 16-byte pieces (a block of a token each), swizzled by token so that the reads below
     // take 64 banks
     const int64_t rows = (int64_t)kv * kTile;
     bool bad = false;
-    auto row_of = [&](int tile) -> int64_t {
-        int page = pages[tile];
+    auto row_of = [&](int page) -> int64_t {
         if (page < 0 || page >= a.cache.n_pages) {
             bad = true;
             page = 0;
@@ -307,11 +301,12 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((const uint8_t *)(scales + row * NB) + lane * 16),
                                              (__attribute__((address_space(3))) void *)(dst + kCodeBytes), 16, 0, kNonTemporal);
     };
-    constexpr int kCopies = kCodeBytes / 1024 + 1;               // instructions of one copy
     uint8_t *kbuf = lds[wave], *vbuf = kbuf + kHalf, *pbuf = vbuf + kHalf;
     const bool any_page = a.cache.n_pages > 0;
+    int page2 = 0;                                               // page of the tile after the next
     if (tile0 < tile_end) {
-        const int64_t row = row_of(tile0);
+        const int64_t row = row_of(pages[tile0]);
+        if (tile0 + kDecodeWaves < tile_end) page2 = pages[tile0 + kDecodeWaves];
         if (any_page) {
             copy(a.cache.kq, a.cache.ks, row, kbuf, false);
             copy(a.cache.vq, a.cache.vs, row, vbuf, true);
@@ -379,15 +374,36 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
     for (int tile = tile0; tile < tile_end; tile += kDecodeWaves) {
         const bool more = tile + kDecodeWaves < tile_end;
         int64_t next = 0;
-        if (more) next = row_of(tile + kDecodeWaves);
-        __builtin_amdgcn_s_waitcnt(0x0F70 | kCopies);            // vmcnt(kCopies): k has arrived, v may be on its way
+        if (more) next = row_of(page2);
+        if (tile + 2 * kDecodeWaves < tile_end) page2 = pages[tile + 2 * kDecodeWaves];
+        __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): the tile has arrived
         asm volatile("" ::: "memory");
+        uint32_t kc[4][NB];                                      // codes of the lane's tokens, 8 of each block
+        hb ks[4], w[4];                                          // scales of the lane's tokens
+        i2 vc[D / 16];                                           // codes of 16 tokens, one value each
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int t = 16 * u + c;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                kc[u][i] = *(const uint32_t *)(kbuf + t * (D / 2) + (i ^ ((t >> (D == 128 ? 2 : 3)) & (NB - 1))) * 16 + g * 4);
+            ks[u] = *(const hb *)(kbuf + kCodeBytes + t * NB * 2);
+            w[u] = *(const hb *)(vbuf + kCodeBytes + t * NB * 2);
+        }
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n)
+            vc[n] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i2 *)(
+                vbuf + vt * (D / 2) + ((n >> 1) ^ ((vt >> 4) & (NB - 1))) * 16 + (n & 1) * 8));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0): read, the buffers may be filled again
+        if (more && any_page) {
+            copy(a.cache.kq, a.cache.ks, next, kbuf, false);
+            copy(a.cache.vq, a.cache.vs, next, vbuf, true);
+        }
         const int left = (int)(len - (int64_t)tile * kTile);     // tokens of the tile that count
         float x[HL][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int t = 16 * u + c;
-            const hb ks = *(const hb *)(kbuf + kCodeBytes + t * NB * 2);
             float s[HL];
 #pragma unroll
             for (int i = 0; i < HL; ++i) s[i] = 0.0f;
@@ -395,28 +411,13 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
             for (int r = 0; r < R; ++r) {
                 f4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < BC; ++i) {
-                    const int blk = r * BC + i, sw = blk ^ ((t >> (D == 128 ? 2 : 3)) & (NB - 1));
-                    z = mfma16(q[blk], codes8(*(const uint32_t *)(kbuf + t * (D / 2) + sw * 16 + g * 4)), z);
-                }
+                for (int i = 0; i < BC; ++i) z = mfma16(q[r * BC + i], codes8(kc[u][r * BC + i]), z);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i / BC] = fmaf(z[i], (float)ks[r * BC + i % BC], s[i / BC]);
+                for (int i = 0; i < 4; ++i) s[i / BC] = fmaf(z[i], (float)ks[u][r * BC + i % BC], s[i / BC]);
             }
 #pragma unroll
             for (int i = 0; i < HL; ++i) x[i][u] = add_halves(s[i]);      // the other part is 32 lanes away
         }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0): the reads of k are done
-        if (more && any_page) {
-            copy(a.cache.kq, a.cache.ks, next, kbuf, false);
-            __builtin_amdgcn_s_waitcnt(0x0F70 | kCopies);        // v has arrived
-        } else {
-            __builtin_amdgcn_s_waitcnt(0x0F70);
-        }
-        asm volatile("" ::: "memory");
-        hb w[4];                                                 // value scales of the lane's tokens
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = *(const hb *)(vbuf + kCodeBytes + (16 * u + c) * NB * 2);
         if (left < kTile) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -484,19 +485,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
             const h8 p0 = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
             const h8 p1 = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-            for (int i = 0; i < BC; ++i) {
-                const int blk = r * BC + i, sw = blk ^ ((vt >> 4) & (NB - 1));
-                i2 x0, x1;
-                read_codes(vbuf + vt * (D / 2) + sw * 16, x0, x1);
-                acc[2 * blk] = mfma16(p0, codes8((uint32_t)x0.x), acc[2 * blk]);
-                acc[2 * blk + 1] = mfma16(p0, codes8((uint32_t)x1.x), acc[2 * blk + 1]);
-                acc[2 * blk] = mfma16(p1, codes8((uint32_t)x0.y), acc[2 * blk]);
-                acc[2 * blk + 1] = mfma16(p1, codes8((uint32_t)x1.y), acc[2 * blk + 1]);
-            }
+            for (int n = 2 * r * BC; n < 2 * (r + 1) * BC; ++n) acc[n] = mfma16(p0, codes8((uint32_t)vc[n].x), acc[n]);
+#pragma unroll
+            for (int n = 2 * r * BC; n < 2 * (r + 1) * BC; ++n) acc[n] = mfma16(p1, codes8((uint32_t)vc[n].y), acc[n]);
         }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xC07F);                      // the reads of v are done
-        if (more && any_page) copy(a.cache.vq, a.cache.vs, next, vbuf, true);
     }
 
     // join the waves: the 16 rows of a wave's result go through its buffers
