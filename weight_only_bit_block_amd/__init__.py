@@ -25,7 +25,18 @@ The library is loaded on first use and must have been built
 """
 from .wq import (BLOCK, GEMV_MAX_M, GroupedCall, Package, WqError, embed, gemm, gemm_noalloc, gemv,
                  header_symbols, linear, load, pack, table_layout, table_plan, table_plan_gemm, unpack)
-from .layer import KV_PAGE, KVCache, attn_decode, attn_prefill, kv_append, residual_norm
+
+_LAYER = ("KV_PAGE", "KVCache", "attn_decode", "attn_prefill", "kv_append", "residual_norm")
+
+
+def __getattr__(name):
+    # imported on first use, since it imports torch
+    if name in _LAYER:
+        from . import layer
+        globals().update({n: getattr(layer, n) for n in _LAYER})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __all__ = ["BLOCK", "GEMV_MAX_M", "GroupedCall", "Package", "WqError", "embed", "gemm", "gemm_noalloc", "gemv",
            "header_symbols", "linear", "load", "pack", "table_layout", "table_plan", "table_plan_gemm", "unpack",

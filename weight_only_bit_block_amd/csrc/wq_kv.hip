@@ -12,68 +12,109 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- append
-// 8 lanes per block of 32 values, 4 consecutive values each: a wavefront reads
-// 1 KiB of consecutive floats and writes 128 bytes of codes. The maximum of a
-// block and its code dwords go over the 8 lanes by cross-lane moves. Division
-// is the correctly rounded fp32 one, as in wq_pack.
-__global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
+// HBM-bound: 8 D bytes read and 1.125 D written for a token and head. A row of
+// D values is D / 4 lanes, 4 values each: a wavefront reads 1 KiB of consecutive
+// floats, the maximum of a block goes over its 8 lanes by cross-lane moves.
+// Every thread takes kAppendRows rows, keys and values, and asks for all of
+// them before it looks up where they go (three dependent reads).
+//
+// The quotients of wq_pack's rule are correctly rounded; here they cost three
+// operations each instead of a division's ten: q0 = x r, q = q0 + r (x - q0 s)
+// with r the correctly rounded 1 / s is the correctly rounded x / s unless s has
+// a mantissa of all ones (s is a binary16 number, or 7) or the quotient is far below 1,
+// where the code is 0 either way (Markstein's theorem).
+constexpr int kAppendRows = 2;
+
+__device__ __forceinline__ float quotient(float x, float s, float r)
 {
-    const int D = a.cache.head_dim, H = a.cache.kv_heads;
-    const int per_row = D / 4;                           // threads per row of one head
-    const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = gid / per_row;                   // (token, head)
-    const int c = (int)(gid - row * per_row);            // 4-value group within the row
-    const bool values = blockIdx.y != 0;
-    const int64_t t = row / H;
-    const int h = (int)(row - t * H);
-    int64_t dst = -1;                                    // cache row
-    f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (t < a.T) {
-        const int b = seq_of_token(a.cu, a.B, (int)t);
-        const SeqRange r = seq_range(a.cu, (int)a.T, b);
-        if (t >= r.begin && t < r.end) {
-            const int64_t pos = (a.start ? (int64_t)a.start[b] : 0) + (t - r.begin);
-            if (pos >= 0 && pos < a.max_pages * WQ_KV_PAGE) {
-                const int64_t page = a.table[(int64_t)b * a.max_pages + pos / WQ_KV_PAGE];
-                if (page >= 0 && page < a.cache.n_pages)
-                    dst = (page * H + h) * WQ_KV_PAGE + pos % WQ_KV_PAGE;
-            }
-        }
-        if (dst >= 0) {
-            const float *src = values ? a.v + t * a.v_stride : a.k + t * a.k_stride;
-            x = *reinterpret_cast<const f4 *>(src + h * D + c * 4);
-        }
-    }
-    float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-    // not finite anywhere: a NaN block (fmaxf drops NaN, so it is asked for apart)
-    const float big = 3.4028235e38f;
-    bool bad = !(fabsf(x.x) <= big && fabsf(x.y) <= big && fabsf(x.z) <= big && fabsf(x.w) <= big);
-    int badi = bad;
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+}
+
+// Largest of the block's 8 lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x)
+{
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+    return x > y ? x : y;
+}
+
+__device__ __forceinline__ void quantize4(f4 x, uint16_t &codes, uint16_t &scale)
+{
+    // magnitudes as whole numbers: what is not finite is the largest
+    uint32_t top = 0;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        amax = fmaxf(amax, __shfl_xor(amax, o));
-        badi |= __shfl_xor(badi, o);
+    for (int j = 0; j < 4; ++j) {
+        const float y = x[j];
+        const uint32_t m = __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu;
+        top = m > top ? m : top;
     }
-    const _Float16 s16 = (_Float16)(amax / 7.0f);
-    const float sf = (float)s16;
-    uint16_t sbits = __builtin_bit_cast(uint16_t, s16);
-    uint32_t codes = 0;
-    if (badi || !(sf <= 65504.0f)) {
-        sbits = 0x7E00;
+    top = max_dpp<0xB1>(top);                            // quad_perm 1 0 3 2
+    top = max_dpp<0x4E>(top);                            // quad_perm 2 3 0 1
+    top = max_dpp<0x141>(top);                           // row_half_mirror: the other quad of 8
+    const float amax = __builtin_bit_cast(float, top);
+    const _Float16 s16 = (_Float16)quotient(amax, 7.0f, 1.0f / 7.0f);
+    const float sf = (float)s16, r = 1.0f / sf;
+    scale = __builtin_bit_cast(uint16_t, s16);
+    uint32_t c = 0;
+    if (!(amax <= 3.4028235e38f) || !(sf <= 65504.0f)) {
+        scale = 0x7E00;
     } else if (sf != 0.0f) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float q = fminf(fmaxf(rintf(x[j] / sf), -8.0f), 7.0f);
-            codes |= ((uint32_t)(int)q & 0xFu) << (4 * j);
+            const float q = fminf(fmaxf(rintf(quotient(x[j], sf, r)), -8.0f), 7.0f);
+            c |= ((uint32_t)(int)q & 0xFu) << (4 * j);
         }
-    } else {
-        sbits = 0;
     }
-    if (dst < 0) return;
-    uint16_t *q = reinterpret_cast<uint16_t *>(values ? a.cache.vq : a.cache.kq);
-    uint16_t *s = values ? a.cache.vs : a.cache.ks;
-    q[dst * per_row + c] = (uint16_t)codes;              // D / 2 bytes a row, 2 bytes a thread
-    if ((c & 7) == 0) s[dst * (D / 32) + (c >> 3)] = sbits;
+    codes = (uint16_t)c;
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
+{
+    constexpr int kLanes = D / 4, kRows = 256 / kLanes;  // lanes of a row, rows of a workgroup at a time
+    const uint32_t H = a.cache.kv_heads, rows = (uint32_t)(a.T * H);
+    const int c = threadIdx.x % kLanes;                  // 4-value group within the row
+    f4 k[kAppendRows], v[kAppendRows];
+    int64_t dst[kAppendRows];                            // cache row
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+        const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = row / H, h = row % H;
+        k[i] = v[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (row < rows) {
+            k[i] = *reinterpret_cast<const f4 *>(a.k + t * a.k_stride + h * D + c * 4);
+            v[i] = *reinterpret_cast<const f4 *>(a.v + t * a.v_stride + h * D + c * 4);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+        const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = row / H, h = row % H;
+        dst[i] = -1;
+        if (row < rows) {
+            const int b = seq_of_token(a.cu, a.B, (int)t);
+            const SeqRange r = seq_range(a.cu, (int)a.T, b);
+            if ((int)t >= r.begin && (int)t < r.end) {
+                const int64_t pos = (a.start ? (int64_t)a.start[b] : 0) + ((int)t - r.begin);
+                if (pos >= 0 && pos < a.max_pages * WQ_KV_PAGE) {
+                    const int64_t page = a.table[(int64_t)b * a.max_pages + pos / WQ_KV_PAGE];
+                    if (page >= 0 && page < a.cache.n_pages) dst[i] = (page * H + h) * WQ_KV_PAGE + pos % WQ_KV_PAGE;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+        uint16_t kc, ks, vc, vs;
+        quantize4(k[i], kc, ks);
+        quantize4(v[i], vc, vs);
+        if (dst[i] < 0) continue;
+        reinterpret_cast<uint16_t *>(a.cache.kq)[dst[i] * kLanes + c] = kc;      // D / 2 bytes a row, 2 bytes a thread
+        reinterpret_cast<uint16_t *>(a.cache.vq)[dst[i] * kLanes + c] = vc;
+        if ((c & 7) == 0) {
+            a.cache.ks[dst[i] * (D / 32) + (c >> 3)] = ks;
+            a.cache.vs[dst[i] * (D / 32) + (c >> 3)] = vs;
+        }
+    }
 }
 
 // ---------------------------------------------------------------- decode attention
@@ -113,9 +154,11 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 // into the same LDS go out before anything is computed, so that copies are
 // under way all the time and 12 wavefronts of 11 KiB share a compute unit's LDS.
 //
-// Lengths are device data, so the split is made on the device: every workgroup
-// adds up the lengths, cuts the sequences into equal chunks that fill the card
-// once and finds its own; a second kernel joins the chunks in order.
+// Lengths are device data, so the split is made on the device: the sequences'
+// steps of 256 tokens (4 tiles, one per wavefront) are laid end to end and every
+// workgroup takes an equal run of them, whatever sequences it meets. A sequence
+// that lies in one run is finished there; the pieces of others go to a workspace
+// and a second kernel joins them in order.
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -169,13 +212,12 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
     return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// ---- how sequences are cut (host: decode_ws_bytes and the launch sizes agree with it)
-// A step is 4 tiles, one per wavefront. Sequences are cut into chunks of equally
-// many steps, as few as give about kFill workgroups in all (4 on each of 256
-// compute units). Cutting needs every workgroup to look at all lengths, so it
-// is left out for many sequences (they fill the card by themselves) and where
-// no sequence can be longer than a step.
-constexpr int kFill = 1024;
+// ---- how the work is cut
+// kFill workgroups in all, 2 on each of 256 compute units; for every kv head and
+// group of query heads equally many. Finding its place makes every workgroup look at all
+// lengths, so many sequences (they fill the card by themselves) are not cut,
+// one workgroup each, and neither are tables without room for two steps.
+constexpr int kFill = 512;
 constexpr int kCutMaxSeqs = 512;
 
 __host__ __device__ inline int head_groups(int heads, int kv_heads) { return (heads / kv_heads + kMaxGroup - 1) / kMaxGroup; }
@@ -183,58 +225,70 @@ __host__ __device__ inline bool cut_sequences(int64_t B, int64_t max_pages)
 {
     return B <= kCutMaxSeqs && max_pages > kDecodeWaves;
 }
-// Most chunks times workgroups per chunk: sum ceil(n_b / c) <= sum n_b / c + B, c >= sum n_b per / kFill.
-__host__ __device__ inline int64_t max_items(int64_t B, int64_t per_chunk) { return kFill + B * per_chunk; }
+__host__ __device__ inline int runs_per_head(int per_step) { return per_step < kFill ? kFill / per_step : 1; }
 
-struct Cut {
-    int b;               // the sequence, -1: none
-    int first;           // number of its first chunk among all
-    int chunks;          // of the sequence
-    int64_t steps;       // of a chunk, below 2^31
+// Where a sequence's pieces are: runs first .. first + count - 1; the first one's
+// piece is its run's last, slot 1, unless the run begins with it.
+struct Pieces {
+    int first, count, slot, pad;
 };
+constexpr int kSlots = 2;                    // pieces of a run that are not whole sequences: its first and its last
 
 __device__ __forceinline__ int steps_of(const DecodeArgs &a, int b)
 {
-    const int64_t len = b < a.B ? a.lens[b] : 0;
+    const int64_t len = a.lens[b];
     return len < 0 || len > a.max_pages * kTile ? 0 : (int)((len + kDecodeStep - 1) / kDecodeStep);
 }
 
-// The cut, and the sequence that holds chunk `chunk` (or the one of number seq
-// when seq >= 0). A whole wavefront calls it.
-__device__ __forceinline__ Cut find_cut(const DecodeArgs &a, int per_chunk, int64_t chunk, int seq)
+// A run of steps: sequence b from its step `skip` on, `left` steps in all.
+struct Run {
+    int b, skip, left;
+    int span;                                // of a run
+};
+
+// A whole wavefront calls it. left <= 0: nothing.
+__device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
 {
     const int lane = threadIdx.x & 63;
     int64_t total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
-        int n = steps_of(a, b0 + lane);
+        int n = b0 + lane < a.B ? steps_of(a, b0 + lane) : 0;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
         total += n;
     }
-    const int64_t steps = total * per_chunk <= kFill ? 1 : (total * per_chunk + kFill - 1) / kFill;
-    int before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        const int n = steps_of(a, b0 + lane);
-        const int mine = (int)((n + steps - 1) / steps);
-        int upto = mine;
+    const int64_t span = (total + runs - 1) / runs, from = run * span;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B && from < total; b0 += 64) {
+        const int n = b0 + lane < a.B ? steps_of(a, b0 + lane) : 0;
+        int upto = n;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int x = __shfl_up(upto, o);
             if (lane >= o) upto += x;
         }
-        const int first = before + upto - mine;
-        const bool hit = seq >= 0 ? b0 + lane == seq : chunk >= first && chunk < first + mine;
-        const uint64_t who = __ballot(hit);
+        const int64_t first = before + upto - n;
+        const uint64_t who = __ballot(from >= first && from < first + n);
         if (who) {
             const int l = __ffsll((unsigned long long)who) - 1;
-            return {b0 + l, __shfl(first, l), __shfl(mine, l), steps};
+            const int skip = __shfl((int)(from - first), l);
+            return {__builtin_amdgcn_readfirstlane(b0 + l), __builtin_amdgcn_readfirstlane(skip),
+                    __builtin_amdgcn_readfirstlane((int)(total - from < span ? total - from : span)),
+                    __builtin_amdgcn_readfirstlane((int)span)};
         }
         before += __shfl(upto, 63);
     }
-    return {-1, 0, 0, steps};
+    return {0, 0, 0, 0};
 }
 
 constexpr int kPartialExtra = 2;             // a partial result: D values, then m and l
+
+// Piece `slot` of a workgroup, head hh.
+template <int D>
+__device__ __forceinline__ float *partial(const DecodeArgs &a, int64_t group, int slot, int hh)
+{
+    return (float *)((Pieces *)a.ws + kCutMaxSeqs) + ((group * kSlots + slot) * kMaxGroup + hh) * (D + kPartialExtra);
+}
 
 template <int D, int H, int WPS>
 __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeArgs a, int groups, bool cut, float c_man, int c_exp)
@@ -248,29 +302,30 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
     typedef _Float16 hb __attribute__((ext_vector_type(NB)));    // a token's scales
     __shared__ __attribute__((aligned(16))) uint8_t lds[kDecodeWaves][2 * kHalf + kWeightBytes];
     __shared__ float state[kDecodeWaves][H][2];
-    const int kv = a.cache.kv_heads, group = a.heads / kv, per_chunk = kv * groups;
-    const int kh = blockIdx.x % kv, hg = blockIdx.x / kv % groups;
-    int b = blockIdx.x / per_chunk, chunks = 1;
-    int64_t t0 = 0, span = a.max_pages * kTile;
-    if (cut) {
-        const Cut at = find_cut(a, per_chunk, b, -1);
-        const int seq = __builtin_amdgcn_readfirstlane(at.b);
-        if (seq < 0) return;
-        span = (int64_t)__builtin_amdgcn_readfirstlane((int)at.steps) * kDecodeStep;
-        t0 = (b - __builtin_amdgcn_readfirstlane(at.first)) * span;
-        b = seq;
-        chunks = __builtin_amdgcn_readfirstlane(at.chunks);
-    }
+    const int kv = a.cache.kv_heads, group = a.heads / kv, per_step = kv * groups;
+    const int kh = blockIdx.x % kv, hg = blockIdx.x / kv % groups, run = blockIdx.x / per_step;
     const int per = (group + groups - 1) / groups;               // heads of this workgroup: per or fewer
     const int head0 = kh * group + hg * per, heads = group - hg * per < per ? group - hg * per : per;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t len = a.lens[b];
-    if (len <= 0 || len > a.max_pages * kTile) {                 // (not reached where sequences are cut)
+    const int64_t cap = a.max_pages * kTile;
+    Run at = {run, 0, 0x7FFFFFFF, 0};                            // not cut: a whole sequence
+    if (cut) {
+        at = find_run(a, run, runs_per_head(per_step));
+        if (at.left <= 0) return;
+    } else if (a.lens[run] <= 0 || a.lens[run] > cap) {
         for (int i = tid; i < heads * D; i += 64 * kDecodeWaves)
-            a.out[(int64_t)b * a.out_stride + head0 * D + i] = len == 0 ? 0.0f : __builtin_nanf("");
+            a.out[(int64_t)run * a.out_stride + head0 * D + i] = a.lens[run] == 0 ? 0.0f : __builtin_nanf("");
         return;
     }
-    const int64_t end = len < t0 + span ? len : t0 + span;
+    int done = 0;                                                // steps of the run that are finished
+next_sequence:
+    // (one value for the whole wavefront: said so, for the compiler's loops and descriptors)
+    const int b = __builtin_amdgcn_readfirstlane(at.b);
+    const int64_t len = __builtin_amdgcn_readfirstlane(a.lens[b]);
+    const int all = (int)((len + kDecodeStep - 1) / kDecodeStep);      // steps of the sequence
+    const int mine = __builtin_amdgcn_readfirstlane(all - at.skip < at.left - done ? all - at.skip : at.left - done);
+    const bool whole = mine == all;
+    const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane(at.skip) * kDecodeStep, end = len < t0 + (int64_t)mine * kDecodeStep ? len : t0 + (int64_t)mine * kDecodeStep;
     const int tile0 = (int)(t0 / kTile) + wave, tile_end = (int)((end + kTile - 1) / kTile);
     // (constant address space: scalar loads, which wait for nothing else)
     const __attribute__((address_space(4))) int32_t *pages =
@@ -281,25 +336,28 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
     // take 64 banks
     const int64_t rows = (int64_t)kv * kTile;
     bool bad = false;
-    auto row_of = [&](int page) -> int64_t {
+    auto row_of = [&](int id) -> int64_t {
+        int page = __builtin_amdgcn_readfirstlane(id);
         if (page < 0 || page >= a.cache.n_pages) {
             bad = true;
             page = 0;
         }
         return (int64_t)page * rows + (int64_t)kh * kTile;
     };
+    // Instruction i brings tokens (64 / NB) i + lane / NB: its swizzle of k does not depend on i, that of v
+    // is block ^ i at 128 values.
+    const int kat = lane / NB * (D / 2) + (lane % NB ^ (lane >> 4 & (NB - 1))) * 16;
+    const int vat = lane / NB * (D / 2) + (D == 128 ? lane % NB : lane % NB ^ (lane >> 5)) * 16;
     auto copy = [&](const void *codes, const uint16_t *scales, int64_t row, uint8_t *dst, bool values) {
-        const uint8_t *src = (const uint8_t *)codes + row * (D / 2);
+        const __amdgpu_buffer_rsrc_t r = make_rsrc((const uint8_t *)codes + row * (D / 2), kCodeBytes);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales + row * NB, kScaleBytes);
 #pragma unroll
-        for (int i = 0; i < kCodeBytes / 1024; ++i) {
-            const int p = i * 64 + lane, t = p / NB, s = p % NB;
-            const int blk = s ^ ((t >> (values ? 4 : D == 128 ? 2 : 3)) & (NB - 1));
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(src + t * (D / 2) + blk * 16),
-                                             (__attribute__((address_space(3))) void *)(dst + i * 1024), 16, 0, kNonTemporal);
-        }
+        for (int i = 0; i < kCodeBytes / 1024; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(dst + i * 1024), 16,
+                                                     values ? (D == 128 ? vat ^ i << 4 : vat) : kat, i * 1024, 0, kNonTemporal);
         if (lane < kScaleBytes / 16)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((const uint8_t *)(scales + row * NB) + lane * 16),
-                                             (__attribute__((address_space(3))) void *)(dst + kCodeBytes), 16, 0, kNonTemporal);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)(dst + kCodeBytes), 16,
+                                                     lane * 16, 0, 0, kNonTemporal);
     };
     uint8_t *kbuf = lds[wave], *vbuf = kbuf + kHalf, *pbuf = vbuf + kHalf;
     const bool any_page = a.cache.n_pages > 0;
@@ -363,7 +421,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
         l[i] = 0.0f;
     }
     int v_exp = kMinScaleExp;
-    const float minus = g >> 1 ? -1.0f : 0.0f;                   // this lane keeps the second part of a weight
+    const uint16_t second = g >> 1 ? 0xFFFF : 0;                 // this lane keeps the second part of a weight
     // Tokens of the output's operands: element e of product x is token 16 (2 x + e / 4) + 4 g + e % 4. The
     // codes' transposed read puts row c of the lanes into nibble c % 8 of dword c / 8, nibble_of(e) = c % 8.
     const int vn = c & 7, ve = vn < 4 ? 2 * vn : 2 * (vn - 4) + 1;
@@ -474,9 +532,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
                 h4 p;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float y = x[i / BC][u] * (float)w[u][r * BC + i % BC];
-                    asm("" : "+v"(y));
-                    p[i] = (_Float16)fmaf(minus, (float)(_Float16)y, y);
+                    const float xs = x[i / BC][u], ws = (float)w[u][r * BC + i % BC];
+                    // the first part, taken off for the lanes of the second (in bits, so that it is rounded once)
+                    const uint16_t hi = __builtin_bit_cast(uint16_t, (_Float16)(xs * ws)) & second;
+                    p[i] = (_Float16)fmaf(xs, ws, -(float)__builtin_bit_cast(_Float16, hi));
                 }
                 *(h4 *)(pw + u * 512) = p;
             }
@@ -521,10 +580,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
             ll = fmaf(by, state[w][hh][1], ll);
             o = fmaf(by, rs[rw * D + d] + rs[(8 + rw) * D + d], o);
         }
-        if (chunks == 1) {
+        if (whole) {
             a.out[(int64_t)b * a.out_stride + head0 * D + i] = o / ll;
         } else {
-            float *p = (float *)a.ws + ((int64_t)blockIdx.x * kMaxGroup + hh) * (D + kPartialExtra);
+            float *p = partial<D>(a, blockIdx.x, done != 0, hh);
             p[d] = o;
             if (d == 0) {
                 p[D] = mm;
@@ -532,57 +591,91 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
             }
         }
     }
+    if (!cut) return;
+    if (at.skip == 0 && kh == 0 && hg == 0 && tid == 0) {
+        // the rest of the sequence fills runs of `span` from the next run's beginning on
+        const int rest = all - mine;
+        Pieces *p = (Pieces *)a.ws + b;
+        *p = Pieces{run, 1 + (rest + at.span - 1) / at.span, done != 0, 0};
+    }
+    done += mine;
+    if (done >= at.left) return;
+    do {
+        ++at.b;
+        if (at.b >= a.B) return;                                 // (not reached: `left` steps are there)
+    } while (a.lens[at.b] <= 0 || a.lens[at.b] > cap);
+    at.skip = 0;
+    __syncthreads();                                             // the results have been read
+    goto next_sequence;
 }
 
-// Joins the chunks of a head in order; writes the rows of empty sequences and
-// of lengths out of range. D lanes add up a quarter of the chunks each.
-constexpr int kJoinParts = 4;
-constexpr int kJoinBlock = 256;              // chunks whose factors are held at once
+// Joins the pieces of a head in order; writes the rows of empty sequences and
+// of lengths out of range. kJoinParts lanes share a value's pieces: everything a
+// lane needs of 8 pieces is asked for at once, since the kernel is all latency.
+constexpr int kJoinParts = 8;
 
 template <int D>
 __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int groups)
 {
-    __shared__ float factor[kJoinBlock], red[kJoinParts][D + 1], top[D * kJoinParts / 64];
+    __shared__ float red[kJoinParts][D], ml[kJoinParts][2];
     const int b = blockIdx.x / a.heads, j = blockIdx.x % a.heads, d = threadIdx.x % D, part = threadIdx.x / D;
+    const Pieces at = ((const Pieces *)a.ws)[b];
     const int64_t len = a.lens[b];
     float *out = a.out + (int64_t)b * a.out_stride + j * D + d;
     if (len <= 0 || len > a.max_pages * kTile) {
         if (part == 0) *out = len == 0 ? 0.0f : __builtin_nanf("");
         return;
     }
-    const int kv = a.cache.kv_heads, group = a.heads / kv, per_chunk = kv * groups, per = (group + groups - 1) / groups;
-    const Cut at = find_cut(a, per_chunk, 0, b);
-    if (at.chunks == 1) return;                  // written already
+    if (at.count == 1) return;                   // written already
+    const int kv = a.cache.kv_heads, group = a.heads / kv, per_step = kv * groups, per = (group + groups - 1) / groups;
     const int kh = j / group, hg = j % group / per, hh = j % group % per;
-    const float *p = (const float *)a.ws +
-                     (((int64_t)at.first * per_chunk + hg * kv + kh) * kMaxGroup + hh) * (D + kPartialExtra);
-    const int64_t stride = (int64_t)per_chunk * kMaxGroup * (D + kPartialExtra);
-    float m = -3.0e38f;
-    for (int i = threadIdx.x; i < at.chunks; i += D * kJoinParts) m = fmaxf(m, p[i * stride + D]);
+    float m = -3.0e38f, l = 0.0f, o = 0.0f;
+    for (int i0 = part; i0 < at.count; i0 += 8 * kJoinParts) {
+        float pm[8], pl[8], po[8];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
-    __syncthreads();
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kJoinParts;
+            pm[k] = -3.0e38f;
+            pl[k] = po[k] = 0.0f;
+            if (i < at.count) {
+                const float *p = partial<D>(a, (int64_t)(at.first + i) * per_step + hg * kv + kh, i == 0 ? at.slot : 0, hh);
+                pm[k] = p[D];
+                pl[k] = p[D + 1];
+                po[k] = p[d];
+            }
+        }
+        float mn = m;
 #pragma unroll
-    for (int w = 0; w < D * kJoinParts / 64; ++w) m = fmaxf(m, top[w]);
-    float l = 0.0f, o = 0.0f;
-    for (int i0 = 0; i0 < at.chunks; i0 += kJoinBlock) {
-        const int n = at.chunks - i0 < kJoinBlock ? at.chunks - i0 : kJoinBlock;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += D * kJoinParts) factor[i] = __builtin_amdgcn_exp2f(p[(i0 + i) * stride + D] - m);
-        __syncthreads();
-        if (d == 0)
-            for (int i = part; i < n; i += kJoinParts) l = fmaf(factor[i], p[(i0 + i) * stride + D + 1], l);
-#pragma unroll 8
-        for (int i = part; i < n; i += kJoinParts) o = fmaf(factor[i], p[(i0 + i) * stride + d], o);
+        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, pm[k]);
+        const float by = __builtin_amdgcn_exp2f(m - mn);
+        l *= by;
+        o *= by;
+        m = mn;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float f = __builtin_amdgcn_exp2f(pm[k] - m);
+            l = fmaf(f, pl[k], l);
+            o = fmaf(f, po[k], o);
+        }
     }
     red[part][d] = o;
-    if (d == 0) red[part][D] = l;
+    if (d == 0) {
+        ml[part][0] = m;
+        ml[part][1] = l;
+    }
     __syncthreads();
     if (part == 0) {
+        float mn = ml[0][0];
 #pragma unroll
-        for (int w = 1; w < kJoinParts; ++w) o += red[w][d];
-        *out = o / (red[0][D] + red[1][D] + red[2][D] + red[3][D]);
+        for (int w = 1; w < kJoinParts; ++w) mn = fmaxf(mn, ml[w][0]);
+        float ll = 0.0f, oo = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinParts; ++w) {
+            const float f = __builtin_amdgcn_exp2f(ml[w][0] - mn);
+            ll = fmaf(f, ml[w][1], ll);
+            oo = fmaf(f, red[w][d], oo);
+        }
+        *out = oo / ll;
     }
 }
 
@@ -590,36 +683,38 @@ __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int 
 
 hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream)
 {
-    const int64_t threads = a.T * a.cache.kv_heads * (a.cache.head_dim / 4);
-    const dim3 grid((unsigned)((threads + 255) / 256), 2);
-    append_kernel<<<grid, 256, 0, stream>>>(a);
+    const int64_t rows = a.T * a.cache.kv_heads, each = kAppendRows * 256 / (a.cache.head_dim / 4);
+    const unsigned grid = (unsigned)((rows + each - 1) / each);
+    if (a.cache.head_dim == 128) append_kernel<128><<<grid, 256, 0, stream>>>(a);
+    else append_kernel<64><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages)
 {
     if (!cut_sequences(B, max_pages)) return 0;
-    const int64_t per_chunk = kv_heads * head_groups((int)heads, (int)kv_heads);
-    return (uint64_t)max_items(B, per_chunk) * kMaxGroup * (uint64_t)(head_dim + kPartialExtra) * 4;
+    const int per_step = (int)kv_heads * head_groups((int)heads, (int)kv_heads);
+    return kCutMaxSeqs * sizeof(Pieces) +
+           (uint64_t)per_step * runs_per_head(per_step) * kSlots * kMaxGroup * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
 
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
 {
-    const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv);
+    const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv), per_step = kv * groups;
     const bool cut = cut_sequences(a.B, a.max_pages);
-    const unsigned grid = (unsigned)(cut ? max_items(a.B, (int64_t)kv * groups) : (int64_t)a.B * kv * groups);
+    const unsigned grid = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : a.B));
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
     const float c_man = (float)(2.0 * c);
     const int per = (group + groups - 1) / groups;
     constexpr int T = 64 * kDecodeWaves;
     if (a.cache.head_dim == 128) {
-        if (per <= 2) decode_kernel<128, 2, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-        else if (per <= 4) decode_kernel<128, 4, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-        else decode_kernel<128, 8, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        if (per <= 2) decode_kernel<128, 2, 2><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        else if (per <= 4) decode_kernel<128, 4, 2><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        else decode_kernel<128, 8, 2><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
     } else {
-        if (per <= 4) decode_kernel<64, 4, 4><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-        else decode_kernel<64, 8, 4><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        if (per <= 4) decode_kernel<64, 4, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
+        else decode_kernel<64, 8, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !cut) return e;

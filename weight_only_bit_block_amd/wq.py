@@ -263,8 +263,8 @@ def embed(ids, q, scales, K: int, bits: int, out=None, stream=None):
     else:
         _dev_tensor(out, torch.float32, "out")
         _need(tuple(out.shape) == (n, K), "out must be [len(ids), K]")
-    _check(load().wq_embed(_ptr(ids), n, K, N, bits, _ptr(q), _ptr(scales), _ptr(out), _stream(stream)),
-           "wq_embed")
+    _check(load().wq_embed(_ptr(ids), n, K, N, bits, _ptr(q), _ptr(scales), _ptr(out),
+                           _stream(stream, ids.get_device())), "wq_embed")
     return out
 
 
