@@ -33,6 +33,7 @@
 #include "wq_seq.h"
 
 #include <math.h>
+#include <stdlib.h>
 
 namespace wq {
 namespace {
@@ -57,6 +58,17 @@ struct TileMeta {
     int k_row[kTileKeys];
     int v_row[kTileKeys];
 };
+typedef int i4 __attribute__((ext_vector_type(4)));
+
+// The first four numbers, by a scalar load: asked for a tile ahead, since each is a miss.
+struct TileHead {
+    int k_exp, v_exp, flags;
+};
+__device__ __forceinline__ TileHead head_of(const TileMeta *m)
+{
+    const i4 x = *(const __attribute__((address_space(4))) i4 *)(uintptr_t)m;
+    return {x.x, x.y, x.z};
+}
 enum { kWildK = 1, kWildV = 2, kOddV = 4 };      // kOddV: v holds values that are not finite (0 in the operands)
 constexpr int kNoExp = -100000;      // of a row of zeros
 
@@ -239,21 +251,26 @@ __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32);
 // wave holds half of the output's values and half of the keys of each tile.
 template <int D>
 struct Rows {
-    h8 q1[D / 16], q2[D / 16];
     f16v o[D / 32];                  // value 32 db + 8 (i / 4) + 4 half + i % 4
     float m, l;                      // running maximum (log2), sum of weights of this lane's keys
     int q_exp;                       // scores are 2^(q_exp - k_exp) times the products
     int v_exp;                       // o is in units of 2^(v_exp - kWeightBits)
+    float f, up, unit;               // of the tile at hand: weight = 2^(f score + up), worth `unit` of 1
 };
 
 template <int D>
-__device__ __forceinline__ void load_query(Rows<D> &s, const float *q, bool live, float c_man, int c_exp, int half)
+struct Query {
+    h8 q1[D / 16], q2[D / 16];
+};
+
+// The lane's half of a query, and the power of two that brings it below 2^14;
+// starts the rows' state.
+template <int D>
+__device__ __forceinline__ int load_query(Rows<D> &s, float (&x)[D / 16][8], const float *q, bool live, int c_exp, int half)
 {
-    constexpr int F = D / 16;
-    float x[F][8];
     float top = 0.0f;
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+    for (int f = 0; f < D / 16; ++f)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -265,45 +282,69 @@ __device__ __forceinline__ void load_query(Rows<D> &s, const float *q, bool live
             }
         }
     top = fmaxf(top, other_half(top));
-    const int e = normaliser(top, 14);           // |c_man| < 2 keeps the product below 2^15
+    const int e = normaliser(top, 14);
     s.q_exp = c_exp - e;
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            _Float16 hi, lo;
-            split(ldexpf(x[f][j], e) * c_man, hi, lo);
-            s.q1[f][j] = hi;
-            s.q2[f][j] = lo;
-        }
 #pragma unroll
     for (int db = 0; db < D / 32; ++db) s.o[db] = f16v{};
     s.m = -3.0e38f;
     s.l = 0.0f;
     s.v_exp = kNoExp;
+    return e;
 }
 
-// One tile of 32 keys. `tile` (LDS or global memory) holds its operands.
-// `first`: position of its first key minus that of this lane's query (keys
-// with first + u > 0 are masked), looked at where `edge`.
-template <int D>
-__device__ __forceinline__ void tile_step(Rows<D> &s, const _Float16 *tile, const TileMeta *meta, bool edge, int first,
-                                          const float *v_rows, int64_t v_stride, int live_keys, int lane)
+// Operands of 16 values of the query: |c_man| < 2 keeps the products below 2^15.
+__device__ __forceinline__ void split_query(const float (&x)[8], int e, float c_man, h8 &q1, h8 &q2)
 {
-    constexpr int F = D / 16;
-    const int half = lane >> 5;
-    const h8 *k1 = reinterpret_cast<const h8 *>(tile) + lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        _Float16 hi, lo;
+        split(ldexpf(x[j], e) * c_man, hi, lo);
+        q1[j] = hi;
+        q2[j] = lo;
+    }
+}
+
+// Scores of a tile: k' operands in LDS or global memory.
+template <int D>
+__device__ __forceinline__ f16v scores(const Query<D> &s, const h8 *k1)
+{
     const h8 *k2 = k1 + D * kTileKeys / 8;
     f16v x = {};
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
+    for (int f = 0; f < D / 16; ++f) {
         const h8 a1 = k1[64 * f], a2 = k2[64 * f];
         x = mfma(a2, s.q1[f], x);
         x = mfma(a1, s.q2[f], x);
         x = mfma(a1, s.q1[f], x);
     }
-    const int flags = meta->flags;
-    int e = s.q_exp - meta->k_exp;
+    return x;
+}
+
+// The same from k in registers (k1 then k2) and queries in LDS (q1 then q2).
+template <int D>
+__device__ __forceinline__ f16v scores(const h8 *q, const h8 (&k)[D / 8])
+{
+    f16v x = {};
+#pragma unroll
+    for (int f = 0; f < D / 16; ++f) {
+        const h8 b1 = q[64 * f], b2 = q[64 * (D / 16 + f)];
+        x = mfma(k[D / 16 + f], b1, x);
+        x = mfma(k[f], b2, x);
+        x = mfma(k[f], b1, x);
+    }
+    return x;
+}
+
+// A tile's scores made ready: rows of wild k scaled, keys this query does not
+// see masked (where `edge`; `first`: position of the tile's first key minus
+// that of this lane's query), the running maximum and the units of the output
+// moved where they have to be. Leaves in s.f and s.up what turns a score into a
+// weight.
+template <int D>
+__device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const TileMeta *meta, bool edge, int first, int half)
+{
+    const int flags = h.flags;
+    int e = s.q_exp - h.k_exp, ve = h.v_exp;
     if (flags & kWildK) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = ldexpf(x[i], s.q_exp - meta->k_row[8 * (i >> 2) + 4 * half + (i & 3)]);
@@ -319,7 +360,6 @@ __device__ __forceinline__ void tile_step(Rows<D> &s, const _Float16 *tile, cons
 #pragma unroll
     for (int i = 2; i < 16; ++i) top = fmaxf(top, x[i]);
     top = fmaxf(top, other_half(top)) * f;
-    int ve = meta->v_exp;
     if (flags & kWildV) {                        // the largest row this query sees
         ve = kNoExp;
 #pragma unroll
@@ -345,63 +385,86 @@ __device__ __forceinline__ void tile_step(Rows<D> &s, const _Float16 *tile, cons
     }
     // weights in units of 2^-(kWeightBits + d), d <= 0 the distance of this tile's values below the largest
     const int d = (flags & kWildV) ? 0 : ve - s.v_exp < -60 ? -60 : ve - s.v_exp;
-    const float up = (float)(kWeightBits + d) - s.m;
+    s.f = f;
+    s.up = (float)(kWeightBits + d) - s.m;
+    s.unit = ldexpf(1.0f, -kWeightBits - d);
+}
+
+// Scores become weights, and their sum is taken.
+template <int D>
+__device__ __forceinline__ void weigh(Rows<D> &s, f16v &x)
+{
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], f, up));
+        x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], s.f, s.up));
         sum += x[i];
     }
-    s.l = fmaf(sum, ldexpf(1.0f, -kWeightBits - d), s.l);
-    if (flags & kWildV) {
+    s.l = fmaf(sum, s.unit, s.l);
+}
+
+__device__ __forceinline__ void split8(const f16v &x, int t, h8 &p1, h8 &p2)
+{
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = meta->v_row[8 * (i >> 2) + 4 * half + (i & 3)] - s.v_exp;
-            x[i] = ldexpf(x[i], r < 0 ? r : 0);
-        }
+    for (int i = 0; i < 8; ++i) {
+        _Float16 hi, lo;
+        split(x[8 * t + i], hi, lo);
+        p1[i] = hi;
+        p2[i] = lo;
     }
-    const h8 *v1 = reinterpret_cast<const h8 *>(tile) + 2 * D * kTileKeys / 8 + lane;
+}
+
+// Adds the weighted values of a tile, 16 keys at a time.
+template <int D>
+__device__ __forceinline__ void accumulate(Rows<D> &s, const h8 *v1, int t, h8 p1, h8 p2)
+{
     const h8 *v2 = v1 + D * kTileKeys / 8;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        h8 p1, p2;
+    for (int db = 0; db < D / 32; ++db) {
+        const h8 a1 = v1[64 * (2 * db + t)], a2 = v2[64 * (2 * db + t)];
+        s.o[db] = mfma(a2, p1, s.o[db]);
+        s.o[db] = mfma(a1, p2, s.o[db]);
+        s.o[db] = mfma(a1, p1, s.o[db]);
+    }
+}
+
+// Weights of a tile with wild v, whose rows have a factor each.
+template <int D>
+__device__ __forceinline__ void weigh_rows(const Rows<D> &s, f16v &x, const TileMeta *meta, int half)
+{
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            _Float16 hi, lo;
-            split(x[8 * t + i], hi, lo);
-            p1[i] = hi;
-            p2[i] = lo;
-        }
+    for (int i = 0; i < 16; ++i) {
+        const int r = meta->v_row[8 * (i >> 2) + 4 * half + (i & 3)] - s.v_exp;
+        x[i] = ldexpf(x[i], r < 0 ? r : 0);
+    }
+}
+
+// Values that are not finite (0 in the operands): counts, for each output, the
+// visible ones as a product of two masks.
+template <int D>
+__device__ __forceinline__ void odd_values(Rows<D> &s, bool edge, int first, const float *v_rows, int64_t v_stride,
+                                           int live_keys, int lane)
+{
+    const int half = lane >> 5;
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+        h8 seen;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            seen[e] = !edge || first + 16 * t + 8 * (e >> 2) + 4 * half + (e & 3) <= 0 ? (_Float16)1.0f : (_Float16)0.0f;
 #pragma unroll
         for (int db = 0; db < D / 32; ++db) {
-            const h8 a1 = v1[64 * (2 * db + t)], a2 = v2[64 * (2 * db + t)];
-            s.o[db] = mfma(a2, p1, s.o[db]);
-            s.o[db] = mfma(a1, p2, s.o[db]);
-            s.o[db] = mfma(a1, p1, s.o[db]);
-        }
-    }
-    if (flags & kOddV) {
-        // count, for each output, the visible values that are not finite: a product of two masks
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-            h8 seen;
+            h8 odd;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                seen[e] = !edge || first + 16 * t + 8 * (e >> 2) + 4 * half + (e & 3) <= 0 ? (_Float16)1.0f : (_Float16)0.0f;
-#pragma unroll
-            for (int db = 0; db < D / 32; ++db) {
-                h8 odd;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int u = 16 * t + 8 * (e >> 2) + 4 * half + (e & 3);
-                    const float y = v_rows[(u < live_keys ? u : 0) * v_stride + 32 * db + (lane & 31)];
-                    odd[e] = u < live_keys && !(fabsf(y) <= kBig) ? (_Float16)1.0f : (_Float16)0.0f;
-                }
-                const f16v n = mfma(odd, seen, f16v{});
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (n[i] > 0.0f) s.o[db][i] = __builtin_nanf("");
+            for (int e = 0; e < 8; ++e) {
+                const int u = 16 * t + 8 * (e >> 2) + 4 * half + (e & 3);
+                const float y = v_rows[(u < live_keys ? u : 0) * v_stride + 32 * db + (lane & 31)];
+                odd[e] = u < live_keys && !(fabsf(y) <= kBig) ? (_Float16)1.0f : (_Float16)0.0f;
             }
+            const f16v n = mfma(odd, seen, f16v{});
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (n[i] > 0.0f) s.o[db][i] = __builtin_nanf("");
         }
     }
 }
@@ -444,33 +507,219 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
     const int wrow = row0 + 32 * wave, pos = wrow + (lane & 31);
     const bool live = pos < len;
     Rows<D> s;
-    load_query<D>(s, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D, live, c_man, c_exp, half);
-    const int last = (len - 1 < row0 + kRows - 1 ? len - 1 : row0 + kRows - 1) / kTileKeys;      // last tile of the block
-    const int64_t step = a.kv_heads;
-    const int64_t at0 = (int64_t)first_slot(r.begin, b, kTileKeys) * step + kvh;
-    auto copy = [&](int tile) {
-        const char *src = reinterpret_cast<const char *>(tiles + (at0 + tile * step) * tile_halves(D)) + wave * 1024 + lane * 16;
-        char *dst = reinterpret_cast<char *>(buf[tile & 1]) + wave * 1024;
+    Query<D> q;
+    {
+        float x[D / 16][8];
+        const int e = load_query<D>(s, x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D, live, c_exp, half);
 #pragma unroll
-        for (int i = 0; i < kBytes / 1024 / W; ++i)
+        for (int f = 0; f < D / 16; ++f) split_query(x[f], e, c_man, q.q1[f], q.q2[f]);
+    }
+    // last tile of the block
+    const int last = __builtin_amdgcn_readfirstlane((len - 1 < row0 + kRows - 1 ? len - 1 : row0 + kRows - 1) / kTileKeys);
+    const int step = a.kv_heads, at0 = __builtin_amdgcn_readfirstlane(first_slot(r.begin, b, kTileKeys) * step + kvh);
+    // k of tile t is wanted one step before v of tile t: two buffers of each, t & 1
+    auto copy = [&](int tile, int values) {
+        const char *src = reinterpret_cast<const char *>(tiles + (int64_t)(at0 + tile * step) * tile_halves(D)) + values * (kBytes / 2) +
+                          wave * 1024 + lane * 16;
+        char *dst = reinterpret_cast<char *>(buf[tile & 1]) + values * (kBytes / 2) + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < kBytes / 2048 / W; ++i)
             __builtin_amdgcn_global_load_lds(
                 (const __attribute__((address_space(1))) void *)(src + i * 1024 * W),
                 (__attribute__((address_space(3))) void *)(dst + i * 1024 * W), 16, 0, 0);
     };
-    copy(0);
-    for (int t = 0; t <= last; ++t) {
-        __builtin_amdgcn_s_waitcnt(0x0070);      // this wave's copies of tile t have arrived; its reads of t - 1 are done
+    auto meet = [&]() {                          // this wave's copies have arrived, its reads are done; so have all waves'
+        __builtin_amdgcn_s_waitcnt(0x0070);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (t < last) copy(t + 1);
-        if (t * kTileKeys <= wrow + 31 && wrow < len)
-            tile_step<D>(s, buf[t & 1], metas + at0 + t * step, t * kTileKeys + 31 > wrow, t * kTileKeys - pos,
-                         a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
-                         len - t * kTileKeys, lane);
+    };
+    const int mine = wrow < len ? wrow / kTileKeys : -1;         // this wave's last tile
+    int odd = 0;
+    copy(0, 0);
+    TileHead now = head_of(metas + at0), next = head_of(metas + at0 + (last > 0 ? step : 0));
+    meet();
+    copy(0, 1);
+    if (last > 0) copy(1, 0);
+    f16v x = {};
+    if (mine >= 0) {
+        x = scores<D>(q, reinterpret_cast<const h8 *>(buf[0]) + lane);
+        settle<D>(s, x, now, metas + at0, mine == 0, -pos, half);
     }
+    for (int t = 0; t <= last; ++t) {
+        const TileHead after = head_of(metas + at0 + (t + 2 <= last ? t + 2 : last) * step);
+        meet();                                  // v of tile t and k of tile t + 1
+        if (t < last) copy(t + 1, 1);
+        if (t + 1 < last) copy(t + 2, 0);
+        if (t <= mine) {
+            const TileMeta *meta = metas + at0 + t * step;
+            const int flags = now.flags;
+            const h8 *v1 = reinterpret_cast<const h8 *>(buf[t & 1]) + 2 * D * kTileKeys / 8 + lane;
+            const h8 *k1 = reinterpret_cast<const h8 *>(buf[(t + 1) & 1]) + lane;
+            // the next tile's scores are computed while this one's become weights (after the last tile: of
+            // whatever the buffer holds, to no use)
+            f16v y;
+            h8 p1[2], p2[2];
+            if (flags == 0) {
+                y = scores<D>(q, k1);
+                weigh<D>(s, x);
+                split8(x, 0, p1[0], p2[0]);
+                split8(x, 1, p1[1], p2[1]);
+                // one matrix instruction, the vector instructions that fit beside it, and the reads of a later one
+                __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+                for (int i = 0; i < 3 * D / 16; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x402, 128 / (3 * D / 16), 0);
+                    if (i % 3 != 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+            } else {
+                weigh<D>(s, x);
+                if (flags & kWildV) weigh_rows<D>(s, x, meta, half);
+                split8(x, 0, p1[0], p2[0]);
+                split8(x, 1, p1[1], p2[1]);
+                y = scores<D>(q, k1);
+            }
+            accumulate<D>(s, v1, 0, p1[0], p2[0]);
+            accumulate<D>(s, v1, 1, p1[1], p2[1]);
+            odd |= flags & kOddV;
+            if (t < mine) {
+                x = y;
+                settle<D>(s, x, next, meta + step, t + 1 == mine, (t + 1) * kTileKeys - pos, half);
+            }
+        }
+        now = next;
+        next = after;
+    }
+    if (odd)                                     // (apart from the loop, whose registers it would take)
+        for (int t = 0; t <= mine; ++t)
+            if (metas[at0 + t * step].flags & kOddV)
+                odd_values<D>(s, t == mine, t * kTileKeys - pos,
+                              a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
+                              len - t * kTileKeys, lane);
     if (wrow < len)
         store_rows<D>(s, live ? a.out + (int64_t)(r.begin + pos) * a.out_stride + head * D : nullptr, half);
+}
+
+// Few rows: the 4 wavefronts of a workgroup share 32 rows and take every fourth
+// tile each, so that short prompts fill the card and no wavefront walks far; what
+// they found is joined through LDS. k and v come from L2 straight into
+// registers, a tile ahead; the queries, the same for all, stay in LDS.
+constexpr int kShare = 4;
+
+template <int D>
+__global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArgs a, const _Float16 *__restrict__ tiles,
+                                                                      const TileMeta *__restrict__ metas, float c_man,
+                                                                      int c_exp, int slots)
+{
+    constexpr int F = D / 8, kPitch = D + 4;     // operands of k or v (both parts); floats between rows of LDS
+    __shared__ __attribute__((aligned(16))) float res[kShare][32 * kPitch];
+    __shared__ float top[kShare][32], sum[kShare][32];
+    const int id = blockIdx.x, group = a.heads / a.kv_heads;
+    const int hp = id % a.heads, kvh = hp % a.kv_heads, head = kvh * group + hp / a.kv_heads;
+    // long blocks first, then short ones: a compute unit that begins with a long one gets a short one beside it
+    const int rank = id / a.heads, slot = rank < (slots + 1) / 2 ? slots - 1 - rank : rank - (slots + 1) / 2;
+    const int b = seq_of_slot(a.cu, (int)a.T, a.B, 32, slot);
+    const SeqRange r = seq_range(a.cu, (int)a.T, b);
+    const int len = r.end - r.begin, last = __builtin_amdgcn_readfirstlane(slot - first_slot(r.begin, b, 32)), row0 = last * 32;
+    if (row0 < 0 || row0 >= len) return;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int pos = row0 + (lane & 31);
+    const int step = a.kv_heads, at0 = __builtin_amdgcn_readfirstlane(first_slot(r.begin, b, kTileKeys) * step + kvh);
+    auto load = [&](int tile, int values, h8 (&x)[F]) {
+        const h8 *src = reinterpret_cast<const h8 *>(tiles + (int64_t)(at0 + tile * step) * tile_halves(D)) + values * (2 * D * kTileKeys / 8);
+#pragma unroll
+        for (int f = 0; f < F; ++f) x[f] = (src + 64 * f)[lane];
+    };
+    const auto head_at = [&](int t) { return head_of(metas + at0 + (t <= last ? t : last) * step); };
+    h8 k[F], v[F];
+    TileHead now = head_at(wave);
+    int odd = 0;
+    if (wave <= last) load(wave, 0, k);
+    Rows<D> s;
+    h8 *const qs = reinterpret_cast<h8 *>(res[0]) + lane;        // until the join
+    {
+        float x[D / 16][8];
+        const int e = load_query<D>(s, x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D, pos < len, c_exp, half);
+#pragma unroll
+        for (int f = 0; f < D / 16; ++f)
+            if (f % kShare == wave) split_query(x[f], e, c_man, qs[64 * f], qs[64 * (D / 16 + f)]);
+    }
+    if (wave <= last) load(wave, 1, v);
+    __syncthreads();
+    for (int t = wave; t <= last; t += kShare) {
+        const TileMeta *meta = metas + at0 + t * step;
+        const TileHead next = head_at(t + kShare);
+        const bool edge = t == last;
+        const int first = t * kTileKeys - pos;
+        __builtin_amdgcn_sched_barrier(0);
+        f16v x = scores<D>(qs, k);
+        // two reads of queries ahead, not all of them: registers are what is short
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int f = 0; f < D / 16; ++f) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);       // (moved up, the loads would need registers of their own)
+        if (t + kShare <= last) load(t + kShare, 0, k);
+        settle<D>(s, x, now, meta, edge, first, half);
+        weigh<D>(s, x);
+        if (now.flags & kWildV) weigh_rows<D>(s, x, meta, half);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            h8 p1, p2;
+            split8(x, h, p1, p2);
+#pragma unroll
+            for (int db = 0; db < D / 32; ++db) {
+                s.o[db] = mfma(v[F / 2 + 2 * db + h], p1, s.o[db]);
+                s.o[db] = mfma(v[2 * db + h], p2, s.o[db]);
+                s.o[db] = mfma(v[2 * db + h], p1, s.o[db]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + kShare <= last) load(t + kShare, 1, v);
+        odd |= now.flags & kOddV;
+        now = next;
+    }
+    if (odd)                                     // (apart from the loop, whose registers it would take)
+        for (int t = wave; t <= last; t += kShare)
+            if (metas[at0 + t * step].flags & kOddV)
+                odd_values<D>(s, t == last, t * kTileKeys - pos,
+                              a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
+                              len - t * kTileKeys, lane);
+    // join: results in units of the largest maximum (the queries have been read when all meet)
+    if (half == 0) top[wave][lane] = s.m;
+    __syncthreads();
+    float m = top[0][lane & 31];
+#pragma unroll
+    for (int w = 1; w < kShare; ++w) m = fmaxf(m, top[w][lane & 31]);
+    const float by = __builtin_amdgcn_exp2f(s.m - m), l = (s.l + other_half(s.l)) * by;
+    if (half == 0) sum[wave][lane] = l;
+    float *mine = res[wave] + (lane & 31) * kPitch + 4 * half;
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f4 y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = ldexpf(s.o[db][4 * g + j] * by, s.v_exp - kWeightBits);
+            *reinterpret_cast<f4 *>(mine + 32 * db + 8 * g) = y;
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * D / 4; i += 64 * kShare) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        if (row0 + row >= len) break;
+        f4 y = *reinterpret_cast<const f4 *>(res[0] + row * kPitch + d);
+        float total = sum[0][row];
+#pragma unroll
+        for (int w = 1; w < kShare; ++w) {
+            y += *reinterpret_cast<const f4 *>(res[w] + row * kPitch + d);
+            total += sum[w][row];
+        }
+        *reinterpret_cast<f4 *>(a.out + (int64_t)(r.begin + row0 + row) * a.out_stride + head * D + d) = y * (1.0f / total);
+    }
 }
 
 inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
@@ -488,6 +737,11 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     if (e != hipSuccess) return e;
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
+    if (getenv("WQSHARE") && atoi(getenv("WQSHARE"))) {
+        const int64_t blocks = tile_slots(a.T, a.B, 32);
+        attend_shared_kernel<D><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c), c_exp - 1, (int)blocks);
+        return hipGetLastError();
+    }
     const int64_t rows = tile_slots(a.T, a.B, 32 * W);
     attend_kernel<D, W><<<(unsigned)(rows * a.heads), 64 * W, 0, stream>>>(a, tiles, metas, (float)(2.0 * c), c_exp - 1, (int)rows);
     return hipGetLastError();
