@@ -33,7 +33,6 @@
 #include "wq_seq.h"
 
 #include <math.h>
-#include <stdlib.h>
 
 namespace wq {
 namespace {
@@ -51,10 +50,8 @@ constexpr float kSlack = 3.0f;       // log2 a score may pass the running maximu
 
 // What the attention kernel needs to know of a tile.
 struct TileMeta {
-    int k_exp;                       // k was multiplied by 2^k_exp (wild: by 2^k_row[u] row by row)
-    int v_exp;                       // v is its operands times 2^v_exp (wild: 2^v_row[u])
-    int flags;
-    int pad;
+    int k_exp, k_flags;              // k was multiplied by 2^k_exp (wild: by 2^k_row[u] row by row)
+    int v_exp, v_flags;              // v is its operands times 2^v_exp (wild: 2^v_row[u])
     int k_row[kTileKeys];
     int v_row[kTileKeys];
 };
@@ -67,7 +64,7 @@ struct TileHead {
 __device__ __forceinline__ TileHead head_of(const TileMeta *m)
 {
     const i4 x = *(const __attribute__((address_space(4))) i4 *)(uintptr_t)m;
-    return {x.x, x.y, x.z};
+    return {x.x, x.z, x.y | x.w};
 }
 enum { kWildK = 1, kWildV = 2, kOddV = 4 };      // kOddV: v holds values that are not finite (0 in the operands)
 constexpr int kNoExp = -100000;      // of a row of zeros
@@ -113,131 +110,129 @@ __device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo)
 }
 
 // ---------------------------------------------------------------- prepare
-// One workgroup per (tile, key/value head); 8 threads share a row of D values.
+// One workgroup per (tile, key/value head, k or v); 8 threads share a row of D
+// values. All latency at short prompts, 5.3 KiB in and out per row at long ones.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float x)
+{
+    return fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true)));
+}
+
 template <int D>
 __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__restrict__ tiles, TileMeta *__restrict__ metas)
 {
     constexpr int E = D / 8;                     // values a thread holds of its row
-    __shared__ float vt[kTileKeys][D + 1];
-    __shared__ float red[4][4];
-    __shared__ int v_factor[kTileKeys];
+    __shared__ float rows[kTileKeys][D + 1];
+    __shared__ float red[4][2];
+    __shared__ int factor[kTileKeys], any_odd;
     const int slot = blockIdx.x, head = blockIdx.y, tid = threadIdx.x;
+    const bool values = blockIdx.z != 0;
     const int b = seq_of_slot(a.cu, (int)a.T, a.B, kTileKeys, slot);
     const SeqRange r = seq_range(a.cu, (int)a.T, b);
     const int len = r.end - r.begin, tile = slot - first_slot(r.begin, b, kTileKeys);
     if (tile < 0 || tile * kTileKeys >= len) return;
     const int row = tid >> 3, seg = tid & 7, key = tile * kTileKeys + row;
-    const bool live = key < len;
-    float k[E], v[E];
-    float kmax = 0.0f, vmax = 0.0f;
-    int odd = 0;                                 // v not finite
-    const float *ks = a.k + (int64_t)(r.begin + key) * a.k_stride + head * D + seg * E;
-    const float *vs = a.v + (int64_t)(r.begin + key) * a.v_stride + head * D + seg * E;
+    const float *src = (values ? a.v + (int64_t)(r.begin + key) * a.v_stride : a.k + (int64_t)(r.begin + key) * a.k_stride) +
+                       head * D + seg * E;
+    float x[E], top = 0.0f;
+    bool odd = false;                            // not finite
+    if (tid == 0) any_odd = 0;
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
-        f4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-        if (live) {
-            x = reinterpret_cast<const f4 *>(ks)[i];
-            y = reinterpret_cast<const f4 *>(vs)[i];
-        }
+        f4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (key < len) y = reinterpret_cast<const f4 *>(src)[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            k[4 * i + j] = x[j];
-            v[4 * i + j] = y[j];
-            kmax = fmaxf(kmax, finite_abs(x[j]));
-            vmax = fmaxf(vmax, finite_abs(y[j]));
+            x[4 * i + j] = y[j];
+            top = fmaxf(top, finite_abs(y[j]));
             odd |= !(fabsf(y[j]) <= kBig);
         }
     }
+    top = max_dpp<0xB1>(top);                    // the row's 8 lanes: quad_perm 1 0 3 2, 2 3 0 1, row_half_mirror
+    top = max_dpp<0x4E>(top);
+    top = max_dpp<0x141>(top);
+    // the tile's largest row and smallest one that is not zero
+    float most = top, least = top > 0.0f ? -top : -kBig;
+    most = max_dpp<0x128>(most);                 // row_ror:8
+    least = max_dpp<0x128>(least);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {            // the row's maxima
-        kmax = fmaxf(kmax, __shfl_xor(kmax, o));
-        vmax = fmaxf(vmax, __shfl_xor(vmax, o));
-    }
-    // tile maxima and smallest rows that are not zero
-    float kt = kmax, vt_max = vmax, kl = kmax > 0.0f ? kmax : kBig, vl = vmax > 0.0f ? vmax : kBig;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        kt = fmaxf(kt, __shfl_xor(kt, o));
-        vt_max = fmaxf(vt_max, __shfl_xor(vt_max, o));
-        kl = fminf(kl, __shfl_xor(kl, o));
-        vl = fminf(vl, __shfl_xor(vl, o));
-        odd |= __shfl_xor(odd, o);
+    for (int o = 16; o < 64; o <<= 1) {
+        most = fmaxf(most, __shfl_xor(most, o));
+        least = fmaxf(least, __shfl_xor(least, o));
     }
     if ((tid & 63) == 0) {
-        float *w = red[tid >> 6];
-        w[0] = kt;
-        w[1] = odd ? -vt_max - 1e-45f : vt_max;  // a sign marks data that is not finite
-        w[2] = kl;
-        w[3] = vl;
+        red[tid >> 6][0] = most;
+        red[tid >> 6][1] = least;
     }
+    if (values) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) vt[row][seg * E + i] = v[i];
+        for (int i = 0; i < E; ++i) rows[row][seg * E + i] = x[i];
+    }
     __syncthreads();
-    odd = 0;
-    kt = vt_max = 0.0f;
-    kl = vl = kBig;
+    if (odd) any_odd = 1;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        kt = fmaxf(kt, red[w][0]);
-        odd |= red[w][1] < 0.0f;
-        vt_max = fmaxf(vt_max, fabsf(red[w][1]));
-        kl = fminf(kl, red[w][2]);
-        vl = fminf(vl, red[w][3]);
+        most = fmaxf(most, red[w][0]);
+        least = fmaxf(least, red[w][1]);
     }
-    const int ke = normaliser(kt, 15), ve = normaliser(vt_max, 15);
-    const bool wild_k = kt > 0.0f && normaliser(kl, 15) - ke > kWildBits;
-    const bool wild_v = vt_max > 0.0f && normaliser(vl, 15) - ve > kWildBits;
-    const int kr = wild_k ? normaliser(kmax, 15) : ke;
+    const int e = normaliser(most, 15);
+    const bool wild = most > 0.0f && normaliser(-least, 15) - e > kWildBits;
+    const int er = wild ? normaliser(top, 15) : e;
     const int64_t at = (int64_t)slot * a.kv_heads + head;
     TileMeta *m = metas + at;
-    if (tid == 0) {
-        m->k_exp = ke;
-        m->v_exp = -ve;
-        m->flags = (wild_k ? kWildK : 0) | (wild_v ? kWildV : 0) | (odd ? kOddV : 0);
+    _Float16 *dst = tiles + at * tile_halves(D);
+    if (!values) {
+        if (tid == 0) {
+            m->k_exp = e;
+            m->k_flags = wild ? kWildK : 0;
+        }
+        if (seg == 0) m->k_row[row] = er;
+        // fragment f covers values 16 f .. 16 f + 15; lane (key, half) holds 8 of them
+#pragma unroll
+        for (int c = 0; c < E / 8; ++c) {
+            const int d0 = seg * E + 8 * c, f = d0 >> 4, half = (d0 >> 3) & 1;
+            h8 hi, lo;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                _Float16 y, z;
+                split(ldexpf(x[8 * c + j], er), y, z);
+                hi[j] = y;
+                lo[j] = z;
+            }
+            const int o = f * 512 + (half * 32 + row) * 8;
+            *reinterpret_cast<h8 *>(dst + o) = hi;
+            *reinterpret_cast<h8 *>(dst + D * kTileKeys + o) = lo;
+        }
+        return;
     }
-    const int vr = wild_v ? normaliser(vmax, 15) : ve;
     if (seg == 0) {
-        m->k_row[row] = kr;
-        m->v_row[row] = vmax > 0.0f ? -vr : kNoExp;
-        v_factor[row] = vr;
+        m->v_row[row] = top > 0.0f ? -er : kNoExp;
+        factor[row] = er;
     }
     __syncthreads();
-    _Float16 *dst = tiles + at * tile_halves(D);
-    // k: fragment f covers values 16 f .. 16 f + 15; lane (key, half) holds 8 of them
-#pragma unroll
-    for (int c = 0; c < E / 8; ++c) {
-        const int d0 = seg * E + 8 * c, f = d0 >> 4, half = (d0 >> 3) & 1;
-        h8 hi, lo;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            _Float16 x, y;
-            split(ldexpf(k[8 * c + j], kr), x, y);
-            hi[j] = x;
-            lo[j] = y;
-        }
-        const int o = f * 512 + (half * 32 + row) * 8;
-        *reinterpret_cast<h8 *>(dst + o) = hi;
-        *reinterpret_cast<h8 *>(dst + D * kTileKeys + o) = lo;
+    if (tid == 0) {
+        m->v_exp = -e;
+        m->v_flags = (wild ? kWildV : 0) | (any_odd ? kOddV : 0);
     }
-    // v': fragment (db, s) covers values 32 db .. + 31 and 16 keys; lane (d, half)
-    // holds the keys that the scores' lane of that half holds: 16 s + 8 (e / 4) + 4 half + e % 4
+    // fragment (db, s) covers values 32 db .. + 31 and 16 keys; lane (d, half) holds the keys that the scores' lane
+    // of that half holds: 16 s + 8 (e / 4) + 4 half + e % 4
+    dst += 2 * D * kTileKeys;
 #pragma unroll
     for (int i = 0; i < D * kTileKeys / 8 / 256; ++i) {
         const int c = tid + 256 * i, lane = c & 63, f = c >> 6;
         const int d = (f >> 1) * 32 + (lane & 31), k0 = (f & 1) * 16 + 4 * (lane >> 5);
         h8 hi, lo;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int u = k0 + 8 * (e >> 2) + (e & 3);
-            const float y = vt[u][d];
-            _Float16 x, z;
-            split(fabsf(y) <= kBig ? ldexpf(y, v_factor[u]) : 0.0f, x, z);
-            hi[e] = x;
-            lo[e] = z;
+        for (int j = 0; j < 8; ++j) {
+            const int u = k0 + 8 * (j >> 2) + (j & 3);
+            const float y = rows[u][d];
+            _Float16 p, z;
+            split(fabsf(y) <= kBig ? ldexpf(y, factor[u]) : 0.0f, p, z);
+            hi[j] = p;
+            lo[j] = z;
         }
-        *reinterpret_cast<h8 *>(dst + 2 * D * kTileKeys + c * 8) = hi;
-        *reinterpret_cast<h8 *>(dst + 3 * D * kTileKeys + c * 8) = lo;
+        *reinterpret_cast<h8 *>(dst + c * 8) = hi;
+        *reinterpret_cast<h8 *>(dst + D * kTileKeys + c * 8) = lo;
     }
 }
 
@@ -593,7 +588,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
     }
     if (odd)                                     // (apart from the loop, whose registers it would take)
         for (int t = 0; t <= mine; ++t)
-            if (metas[at0 + t * step].flags & kOddV)
+            if (metas[at0 + t * step].v_flags & kOddV)
                 odd_values<D>(s, t == mine, t * kTileKeys - pos,
                               a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
                               len - t * kTileKeys, lane);
@@ -685,7 +680,7 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
     }
     if (odd)                                     // (apart from the loop, whose registers it would take)
         for (int t = wave; t <= last; t += kShare)
-            if (metas[at0 + t * step].flags & kOddV)
+            if (metas[at0 + t * step].v_flags & kOddV)
                 odd_values<D>(s, t == last, t * kTileKeys - pos,
                               a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
                               len - t * kTileKeys, lane);
@@ -725,6 +720,14 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
 inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((uint64_t)slots * kv_heads * sizeof(TileMeta)); }
 
+// Up to so many workgroups of 128 rows, prompts run on the kernel whose wavefronts
+// share 32 rows. Measured, both kernels (us, shared / other): 16 heads of 128,
+// one prompt of 1024 (144 groups) 35 / 67, 2048 (272) 95 / 124, 4096 (528)
+// 284 / 277; 8 prompts of 256 (384) 41 / 40; 64 heads, 512 tokens (320) 41 / 43;
+// 16 heads of 64, 4096 tokens (528) 154 / 179, 6000 (752) 290 / 300, 8 prompts
+// of 1024 (1152) 114 / 101.
+constexpr int64_t few_groups(int D) { return D == 128 ? 352 : 768; }
+
 template <int D>
 hipError_t launch(const PromptArgs &a, hipStream_t stream)
 {
@@ -732,17 +735,18 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     const int64_t slots = tile_slots(a.T, a.B, kTileKeys);
     TileMeta *metas = reinterpret_cast<TileMeta *>(a.ws);
     _Float16 *tiles = reinterpret_cast<_Float16 *>((char *)a.ws + meta_bytes(slots, a.kv_heads));
-    prepare_kernel<D><<<dim3((unsigned)slots, (unsigned)a.kv_heads), 256, 0, stream>>>(a, tiles, metas);
+    prepare_kernel<D><<<dim3((unsigned)slots, (unsigned)a.kv_heads, 2), 256, 0, stream>>>(a, tiles, metas);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
-    if (getenv("WQSHARE") && atoi(getenv("WQSHARE"))) {
+    const int64_t rows = tile_slots(a.T, a.B, 32 * W);
+    if (rows * a.heads <= few_groups(D)) {
         const int64_t blocks = tile_slots(a.T, a.B, 32);
-        attend_shared_kernel<D><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c), c_exp - 1, (int)blocks);
+        attend_shared_kernel<D><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c),
+                                                                                          c_exp - 1, (int)blocks);
         return hipGetLastError();
     }
-    const int64_t rows = tile_slots(a.T, a.B, 32 * W);
     attend_kernel<D, W><<<(unsigned)(rows * a.heads), 64 * W, 0, stream>>>(a, tiles, metas, (float)(2.0 * c), c_exp - 1, (int)rows);
     return hipGetLastError();
 }
