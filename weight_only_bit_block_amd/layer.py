@@ -21,6 +21,7 @@ KV_PAGE = 64
 _WS_ALIGN = 256
 _F32, _I32, _I16, _U8 = torch.float32, torch.int32, torch.int16, torch.uint8
 _Tensor = torch.Tensor
+_CONTIGUOUS = torch.contiguous_format
 
 
 class KVCache(NamedTuple):
@@ -56,9 +57,10 @@ class KVCache(NamedTuple):
     def head_dim(self) -> int:
         return self.kq.shape[3] * 2
 
-    def _struct(self, device) -> WqKVCache:
+    def _struct(self, at: int) -> WqKVCache:
+        """The library's view of the cache, whose arrays must lie on device `at`."""
         kq, ks, vq, vs = self
-        if not (isinstance(kq, _Tensor) and kq.is_cuda and kq.dim() == 4):
+        if not (isinstance(kq, _Tensor) and kq.dim() == 4):
             raise ValueError("cache.kq must be a 4-D device tensor")
         shape = kq.shape
         n, h, page, half = shape
@@ -66,18 +68,19 @@ class KVCache(NamedTuple):
         scales = (n, h, page, half // 16)
         for t, dt, want, name in ((kq, _U8, shape, "kq"), (vq, _U8, shape, "vq"), (ks, _I16, scales, "ks"),
                                   (vs, _I16, scales, "vs")):
-            if not (t.dtype == dt and t.shape == want and t.is_contiguous() and t.device == device):
-                raise ValueError(f"cache.{name} must be a contiguous {dt} tensor {list(want)} on {device}")
+            if not (t.dtype is dt and t.shape == want and t.get_device() == at and t.is_contiguous()):
+                raise ValueError(f"cache.{name} must be a contiguous {dt} tensor {list(want)} on device {at}")
         return WqKVCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), n, h, 2 * half)
 
 
-def _heads(t, name, device=None):
-    """[tokens, heads, head_dim] fp32 with heads and values contiguous; returns
-    (tokens, heads, head_dim, floats between tokens)."""
-    if not (isinstance(t, _Tensor) and t.is_cuda and t.dtype == _F32 and t.dim() == 3):
+def _heads(t, name, at=None):
+    """[tokens, heads, head_dim] fp32 with heads and values contiguous, on
+    device `at` where given; returns (tokens, heads, head_dim, floats between
+    tokens)."""
+    if not (isinstance(t, _Tensor) and t.dtype is _F32 and t.dim() == 3 and t.is_cuda):
         raise ValueError(f"{name} must be a float32 device tensor [tokens, heads, head_dim]")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if at is not None and t.get_device() != at:
+        raise ValueError(f"{name} must be on device {at}")
     n, h, d = t.shape
     row, head, value = t.stride()
     if (value != 1 and d > 1) or (head != d and h > 1):
@@ -86,42 +89,51 @@ def _heads(t, name, device=None):
     return n, h, d, row if n > 1 else -(-h * d // 4) * 4
 
 
-def _index(t, shape, name, device):
-    if not (isinstance(t, _Tensor) and t.dtype == _I32 and t.device == device and t.is_contiguous() and t.shape == shape):
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+def _index(t, shape, name, at):
+    if not (isinstance(t, _Tensor) and t.dtype is _I32 and t.shape == shape and t.get_device() == at and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on device {at}")
     return t.data_ptr()
 
 
-def _cu(cu, device):
+def _cu(cu, at):
     """Address and number of sequences of cu."""
     if cu is None:
         return None, 1
     _need(isinstance(cu, _Tensor) and cu.dim() == 1 and cu.shape[0] >= 1, "cu must be [sequences + 1]")
-    return _index(cu, cu.shape, "cu", device), cu.shape[0] - 1
+    return _index(cu, cu.shape, "cu", at), cu.shape[0] - 1
 
 
-def _table(table, B, device):
+def _table(table, B, at):
     _need(isinstance(table, _Tensor) and table.dim() == 2, "table must be [sequences, max_pages]")
     W = table.shape[1]
-    return _index(table, (B, W), "table", device), W
+    return _index(table, (B, W), "table", at), W
+
+
+class _Here:
+    """The usual case: the current device and its current stream."""
+
+    def __init__(self, at):
+        self.at = at
+
+    def __enter__(self):
+        return _stream(None, self.at)
+
+    def __exit__(self, *exc):
+        return False
 
 
 class _On:
-    """The tensors' device made current, and allocations taken from `stream`."""
+    """A device made current, and allocations taken from `stream`."""
 
-    def __init__(self, device, stream):
-        _need(stream is None or stream.device == device, "stream belongs to another device")
-        self.device, self.stream = device, stream
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
+    def __init__(self, at, stream):
+        _need(stream is None or stream.device.index == at, "stream belongs to another device")
+        self.at, self.stream = at, stream
+        self.guards = [torch.cuda.device(at)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return _stream(self.stream, self.device.index)
+        return _stream(self.stream, self.at)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -129,20 +141,24 @@ class _On:
         return False
 
 
-def _workspace(nbytes, device):
+def _on(at, stream):
+    return _Here(at) if stream is None and at == torch.cuda.current_device() else _On(at, stream)
+
+
+def _workspace(nbytes, like):
     """A workspace of nbytes, 256-byte aligned: (tensor to keep, address)."""
     if nbytes == 0:
         return None, None
-    t = torch.empty(nbytes + _WS_ALIGN, dtype=_U8, device=device)
+    t = torch.empty(nbytes + _WS_ALIGN, dtype=_U8, device=like.device)
     p = t.data_ptr()
     return t, p + (-p) % _WS_ALIGN
 
 
-def _out_heads(out, shape, device):
-    """`out` of a given shape, made here if None, and the floats between its tokens."""
+def _out_heads(out, q, shape, at):
+    """`out` of q's shape, made here if None, and the floats between its tokens."""
     if out is None:
-        return torch.empty(shape, dtype=_F32, device=device), shape[1] * shape[2]
-    n, h, d, stride = _heads(out, "out", device)
+        return torch.empty_like(q, memory_format=_CONTIGUOUS), shape[1] * shape[2]
+    n, h, d, stride = _heads(out, "out", at)
     if (n, h, d) != shape:
         raise ValueError("out must have q's shape")
     return out, stride
@@ -155,17 +171,17 @@ def attn_prefill(q, k, v, cu: Optional[torch.Tensor] = None, scale: Optional[flo
     device (None: one prompt). scale defaults to head_dim ** -0.5. Returns out
     [T, heads, head_dim]; rows of no sequence are not written."""
     T, H, D, qs = _heads(q, "q")
-    dev = q.device
-    Tk, Hk, Dk, ks = _heads(k, "k", dev)
-    Tv, Hv, Dv, vs = _heads(v, "v", dev)
+    at = q.get_device()
+    Tk, Hk, Dk, ks = _heads(k, "k", at)
+    Tv, Hv, Dv, vs = _heads(v, "v", at)
     if not (Tk == T and Tv == T and Dk == D and Dv == D and Hv == Hk):
         raise ValueError("k and v must be [T, kv_heads, head_dim] for q's T and head_dim")
-    pcu, B = _cu(cu, dev)
+    pcu, B = _cu(cu, at)
     lib = load()
-    with _On(dev, stream) as s:
-        out, os_ = _out_heads(out, (T, H, D), dev)
+    with _on(at, stream) as s:
+        out, os_ = _out_heads(out, q, (T, H, D), at)
         nb = lib.wq_attn_prefill_ws(T, B, H, Hk, D)
-        keep, ws = _workspace(nb, dev)
+        keep, ws = _workspace(nb, q)
         st = lib.wq_attn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, pcu, B, H, Hk, D,
                                  D ** -0.5 if scale is None else scale, out.data_ptr(), os_, ws, nb, s)
     if st:
@@ -181,15 +197,15 @@ def kv_append(cache: KVCache, k, v, table, cu: Optional[torch.Tensor] = None, st
     [sequences + 1] (None: one sequence), start int32 [sequences]. Rows without
     a page in the cache are dropped."""
     T, H, D, ks = _heads(k, "k")
-    dev = k.device
-    Tv, Hv, Dv, vs = _heads(v, "v", dev)
-    c = cache._struct(dev)
+    at = k.get_device()
+    Tv, Hv, Dv, vs = _heads(v, "v", at)
+    c = cache._struct(at)
     if not (Tv == T and Hv == H and Dv == D and H == c.kv_heads and D == c.head_dim):
         raise ValueError("k and v must be [T, kv_heads, head_dim] of the cache")
-    pcu, B = _cu(cu, dev)
-    pt, W = _table(table, B, dev)
-    pst = None if start is None else _index(start, (B,), "start", dev)
-    with _On(dev, stream) as s:
+    pcu, B = _cu(cu, at)
+    pt, W = _table(table, B, at)
+    pst = None if start is None else _index(start, (B,), "start", at)
+    with _on(at, stream) as s:
         st = load().wq_kv_append(c, k.data_ptr(), ks, v.data_ptr(), vs, T, pcu, pst, B, pt, W, s)
     if st:
         raise WqError(st, "wq_kv_append")
@@ -202,16 +218,16 @@ def attn_decode(q, cache: KVCache, table, lens, scale: Optional[float] = None, o
     head_dim ** -0.5. Returns out like q: zeros where lens is 0, NaN where a
     length or page lies outside the table or the cache."""
     B, H, D, qs = _heads(q, "q")
-    dev = q.device
-    c = cache._struct(dev)
+    at = q.get_device()
+    c = cache._struct(at)
     _need(D == c.head_dim, "q must have the cache's head_dim")
-    pt, W = _table(table, B, dev)
-    pl = _index(lens, (B,), "lens", dev)
+    pt, W = _table(table, B, at)
+    pl = _index(lens, (B,), "lens", at)
     lib = load()
-    with _On(dev, stream) as s:
-        out, os_ = _out_heads(out, (B, H, D), dev)
+    with _on(at, stream) as s:
+        out, os_ = _out_heads(out, q, (B, H, D), at)
         nb = lib.wq_attn_decode_ws(B, H, c.kv_heads, D, W)
-        keep, ws = _workspace(nb, dev)
+        keep, ws = _workspace(nb, q)
         st = lib.wq_attn_decode(c, q.data_ptr(), qs, H, pl, B, pt, W, D ** -0.5 if scale is None else scale,
                                 out.data_ptr(), os_, ws, nb, s)
     if st:
@@ -219,12 +235,12 @@ def attn_decode(q, cache: KVCache, table, lens, scale: Optional[float] = None, o
     return out
 
 
-def _rows(t, shape, name, device):
+def _rows(t, shape, name, at):
     """Address of a contiguous fp32 tensor, None for none."""
     if t is None:
         return None
-    if not (isinstance(t, _Tensor) and t.dtype == _F32 and t.device == device and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on {device}")
+    if not (isinstance(t, _Tensor) and t.dtype is _F32 and t.shape == shape and t.get_device() == at and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on device {at}")
     return t.data_ptr()
 
 
@@ -238,28 +254,28 @@ def residual_norm(h, y=None, post_weight=None, gate=None, alpha: float = 1.0, pr
     h_out is given). x_out is computed where pre_weight or x_out is given, or
     where norm is True (weight 1). Returns (h_out, x_out), None for what was
     not computed. h_out may be h."""
-    if not (isinstance(h, _Tensor) and h.is_cuda and h.dtype == _F32 and h.dim() == 2 and h.is_contiguous()):
+    if not (isinstance(h, _Tensor) and h.dtype is _F32 and h.dim() == 2 and h.is_cuda and h.is_contiguous()):
         raise ValueError("h must be a contiguous float32 device tensor [M, N]")
-    dev, shape = h.device, h.shape
+    at, shape = h.get_device(), h.shape
     M, N = shape
-    py = _rows(y, shape, "y", dev)
-    pp = _rows(post_weight, (N,), "post_weight", dev)
-    pw = _rows(pre_weight, (N,), "pre_weight", dev)
+    py = _rows(y, shape, "y", at)
+    pp = _rows(post_weight, (N,), "post_weight", at)
+    pw = _rows(pre_weight, (N,), "pre_weight", at)
     pg, gs = None, 0
     if gate is not None:
         one = isinstance(gate, _Tensor) and gate.dim() == 1
-        pg, gs = _rows(gate, (N,) if one else shape, "gate", dev), 0 if one else N
+        pg, gs = _rows(gate, (N,) if one else shape, "gate", at), 0 if one else N
     want_x = (pre_weight is not None or x_out is not None) if norm is None else norm
     _need(want_x or (pre_weight is None and x_out is None), "norm=False with a pre_weight or x_out")
     _need(y is not None or (post_weight is None and gate is None), "post_weight and gate need y")
     _need(want_x or y is not None, "nothing to compute: neither a block output nor a norm")
-    with _On(dev, stream) as s:
+    with _on(at, stream) as s:
         if h_out is None and y is not None:
-            h_out = torch.empty(shape, dtype=_F32, device=dev)
+            h_out = torch.empty_like(h)
         if x_out is None and want_x:
-            x_out = torch.empty(shape, dtype=_F32, device=dev)
-        st = load().wq_residual_norm(h.data_ptr(), py, pp, pg, gs, alpha, pw, eps, M, N, _rows(h_out, shape, "h_out", dev),
-                                     _rows(x_out, shape, "x_out", dev), s)
+            x_out = torch.empty_like(h)
+        st = load().wq_residual_norm(h.data_ptr(), py, pp, pg, gs, alpha, pw, eps, M, N, _rows(h_out, shape, "h_out", at),
+                                     _rows(x_out, shape, "x_out", at), s)
     if st:
         raise WqError(st, "wq_residual_norm")
     return h_out, x_out

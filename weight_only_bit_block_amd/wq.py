@@ -250,9 +250,9 @@ def embed(ids, q, scales, K: int, bits: int, out=None, stream=None):
     """Tied token embedding: out[i] = dequantized row ids[i] of the packed table
     (q, scales) in fp32; ids outside [0, N) give rows of NaN."""
     torch = _torch()
-    _dev_tensor(ids, torch.int32, "ids")
-    _dev_tensor(q, torch.uint8, "q")
-    _dev_tensor(scales, torch.int16, "scales")
+    for t, dt, name in ((ids, torch.int32, "ids"), (q, torch.uint8, "q"), (scales, torch.int16, "scales")):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dt and t.is_contiguous()):
+            _dev_tensor(t, dt, name)                # raises with the reason
     _need(ids.dim() == 1, "ids must be 1-D")
     N = q.shape[0]
     _need(q.shape[1] == q_row_bytes(K, bits), "q has the wrong row length for K and bits")
