@@ -214,16 +214,21 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
 
 // ---- how the work is cut
 // kFill workgroups in all, 2 on each of 256 compute units; for every kv head and
-// group of query heads equally many. Finding its place makes every workgroup look at all
-// lengths, so many sequences (they fill the card by themselves) are not cut,
-// one workgroup each, and neither are tables without room for two steps.
+// group of query heads equally many. Finding its place makes every workgroup look
+// at all lengths, and the pieces cost a second kernel, so many sequences (they
+// fill the card by themselves) are not cut, one workgroup each, and neither are
+// short ones: tables of up to 16 pages, or 32 where there are kFill / 2
+// workgroups without (us, uncut / cut, 8 kv heads of 128, 2 query heads each:
+// 1 x 500 tokens 7.9 / 10.5, 1 x 1024 11.0 / 10.7 but 12 / 17 with the launches, 1 x 2048
+// 17.2 / 11.2, 32 x 777 12.8 / 17.2, 32 x 2048 20.7 / 24.7).
 constexpr int kFill = 512;
 constexpr int kCutMaxSeqs = 512;
+constexpr int kShortPages = 16;
 
 __host__ __device__ inline int head_groups(int heads, int kv_heads) { return (heads / kv_heads + kMaxGroup - 1) / kMaxGroup; }
-__host__ __device__ inline bool cut_sequences(int64_t B, int64_t max_pages)
+__host__ __device__ inline bool cut_sequences(int64_t B, int per_step, int64_t max_pages)
 {
-    return B <= kCutMaxSeqs && max_pages > kDecodeWaves;
+    return B <= kCutMaxSeqs && max_pages > (B * per_step >= kFill / 2 ? 2 * kShortPages : kShortPages);
 }
 __host__ __device__ inline int runs_per_head(int per_step) { return per_step < kFill ? kFill / per_step : 1; }
 
@@ -692,8 +697,8 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream)
 
 uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages)
 {
-    if (!cut_sequences(B, max_pages)) return 0;
     const int per_step = (int)kv_heads * head_groups((int)heads, (int)kv_heads);
+    if (!cut_sequences(B, per_step, max_pages)) return 0;
     return kCutMaxSeqs * sizeof(Pieces) +
            (uint64_t)per_step * runs_per_head(per_step) * kSlots * kMaxGroup * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
@@ -701,7 +706,7 @@ uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t hea
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
 {
     const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv), per_step = kv * groups;
-    const bool cut = cut_sequences(a.B, a.max_pages);
+    const bool cut = cut_sequences(a.B, per_step, a.max_pages);
     const unsigned grid = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : a.B));
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
