@@ -43,11 +43,15 @@ def test_prefill_refusals(lib):
 
 def test_prefill_workspace(lib):
     need = lib.wq_attn_prefill_ws(8, 2, 16, 8, 128)
+    assert need > 0 and need % 256 == 0
     assert lib.wq_attn_prefill_ws(8, 2, 15, 8, 128) == 0 and lib.wq_attn_prefill_ws(0, 2, 16, 8, 128) == 0
-    if need:
-        assert _prefill(lib, ws=None) == NULL and _prefill(lib, ws=MIS) == ALIGN and _prefill(lib, wsb=need - 1) == SHAPE
-    # the size holds the call's tiles wherever the sequences begin, and grows with T and B
-    assert lib.wq_attn_prefill_ws(4096, 9, 16, 8, 128) >= lib.wq_attn_prefill_ws(4096, 1, 16, 8, 128) >= need * 0
+    assert _prefill(lib, ws=None) == NULL and _prefill(lib, ws=MIS) == ALIGN and _prefill(lib, wsb=need - 1) == SHAPE
+    # a tile of 32 keys is 4 binary16 operands; sequences may begin anywhere, so each adds one tile
+    tile = 4 * 128 * 32 * 2
+    for T, B in ((1, 1), (31, 1), (32, 1), (33, 3), (4096, 9)):
+        slots = T // 32 + B
+        got = lib.wq_attn_prefill_ws(T, B, 16, 8, 128)
+        assert slots * 8 * tile <= got <= slots * 8 * (tile + 512) + 256
 
 
 def _cache(**kw):
@@ -106,9 +110,10 @@ def test_decode_refusals(lib):
         assert _decode(lib, _cache(**{name: None})) == NULL
         assert _decode(lib, _cache(**{name: MIS})) == ALIGN
     need = lib.wq_attn_decode_ws(1, 16, 8, 128, 1 << 11)
-    assert lib.wq_attn_decode_ws(1, 12, 8, 128, 4) == 0 and lib.wq_attn_decode_ws(0, 16, 8, 128, 4) == 0
-    if need:
-        assert _decode(lib, B=1, W=1 << 11, ws=None) == NULL and _decode(lib, B=1, W=1 << 11, wsb=need - 1) == SHAPE
+    assert need > 0 and lib.wq_attn_decode_ws(1, 12, 8, 128, 4) == 0 and lib.wq_attn_decode_ws(0, 16, 8, 128, 4) == 0
+    assert lib.wq_attn_decode_ws(1, 16, 8, 128, 4) == 0 and lib.wq_attn_decode_ws(5000, 16, 8, 128, 1 << 11) == 0    # not cut
+    assert _decode(lib, B=1, W=1 << 11, ws=None) == NULL and _decode(lib, B=1, W=1 << 11, wsb=need - 1) == SHAPE
+    assert _decode(lib, B=1, W=1 << 11, ws=FAKE + 64) == ALIGN
 
 
 def test_norm_refusals(lib):
