@@ -130,12 +130,13 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 //   scores   A = q, 16 rows (part, head of H, block of BC), zero outside the
 //     row's block, B = k codes (one block x 16 tokens): a chain of BC products
 //     gives BC blocks' partial sums side by side. A lane holds one token and the
-//     BC blocks of H / 2 heads, scales and adds them, and exchanges the part
-//     with the lane 32 away: a score per lane, none computed twice over.
+//     BC blocks of H / 2 heads, one part of each; it scales and adds them, and
+//     one exchange with the lane 32 away leaves it with the whole scores of
+//     two of its four tokens.
 //   output   A = weights p_u s_u, rows as above (each block of the row's BC has
-//     its own scale), 32 tokens; B = v codes. Every lane makes its token's 4 rows
-//     and they change sides through 2 KiB of LDS (ds_read_b64_tr_b16). Only the
-//     columns of a row's own block are used at the end.
+//     its own scale), 32 tokens; B = v codes. Every lane makes both parts of its
+//     two tokens' rows, and they change sides through 2 KiB of LDS
+//     (ds_read_b64_tr_b16). Only the columns of a row's own block are used at the end.
 // BC H = 8: few heads put blocks side by side, so that a lane has more to do per
 // token; more heads take that room.
 //
@@ -175,11 +176,10 @@ constexpr int kMinScaleExp = -24;                      // 2^-24 is binary16's sm
 
 __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// x plus the value 32 lanes away.
-__device__ __forceinline__ float add_halves(float x)
+// Sums over the two lanes 32 apart: of x for the lower one, of y for the upper.
+__device__ __forceinline__ float add_halves(float x, float y)
 {
-    const uint32_t v = __builtin_bit_cast(uint32_t, x);
-    const auto both = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto both = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y), false, false);
     const uint32_t lo = both[0], hi = both[1];       // (a bit cast of a vector's element takes element 0)
     return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
 }
@@ -415,7 +415,8 @@ next_sequence:
         }
     }
 
-    // From here on a lane is token 16 u + c of a tile, and the 4 rows 4 g + i: part g / 2, heads (g % 2) HL + i / BC
+    // From here on a lane is tokens 16 u + c of a tile, and the 4 rows 4 g + i: part g / 2, heads (g % 2) HL + i / BC.
+    // Of the whole scores it holds those of u = 2 (g / 2) + j, j < 2.
     f4 acc[D / 16];
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) acc[n] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -426,12 +427,11 @@ next_sequence:
         l[i] = 0.0f;
     }
     int v_exp = kMinScaleExp;
-    const uint16_t second = g >> 1 ? 0xFFFF : 0;                 // this lane keeps the second part of a weight
     // Tokens of the output's operands: element e of product x is token 16 (2 x + e / 4) + 4 g + e % 4. The
     // codes' transposed read puts row c of the lanes into nibble c % 8 of dword c / 8, nibble_of(e) = c % 8.
     const int vn = c & 7, ve = vn < 4 ? 2 * vn : 2 * (vn - 4) + 1;
     const int vt = 16 * (2 * (c >> 3) + (ve >> 2)) + 4 * g + (ve & 3);
-    uint8_t *const pw = pbuf + c * 32 + g * 8;                                    // weights are written by token
+    uint8_t *const pw = pbuf + (g >> 1) * 1024 + c * 32 + (g & 1) * 8;             // weights are written by token
     uint8_t *const pr = pbuf + (4 * g + (c >> 2)) * 32 + (c & 3) * 8;             // and read by row
 
     for (int tile = tile0; tile < tile_end; tile += kDecodeWaves) {
@@ -442,7 +442,7 @@ next_sequence:
         __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): the tile has arrived
         asm volatile("" ::: "memory");
         uint32_t kc[4][NB];                                      // codes of the lane's tokens, 8 of each block
-        hb ks[4], w[4];                                          // scales of the lane's tokens
+        hb ks[4], w[2];                                          // scales of the lane's tokens
         i2 vc[D / 16];                                           // codes of 16 tokens, one value each
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -451,8 +451,9 @@ next_sequence:
             for (int i = 0; i < NB; ++i)
                 kc[u][i] = *(const uint32_t *)(kbuf + t * (D / 2) + (i ^ ((t >> (D == 128 ? 2 : 3)) & (NB - 1))) * 16 + g * 4);
             ks[u] = *(const hb *)(kbuf + kCodeBytes + t * NB * 2);
-            w[u] = *(const hb *)(vbuf + kCodeBytes + t * NB * 2);
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[j] = *(const hb *)(vbuf + kCodeBytes + (16 * (2 * (g >> 1) + j) + c) * NB * 2);
 #pragma unroll
         for (int n = 0; n < D / 16; ++n)
             vc[n] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i2 *)(
@@ -464,33 +465,34 @@ next_sequence:
             copy(a.cache.vq, a.cache.vs, next, vbuf, true);
         }
         const int left = (int)(len - (int64_t)tile * kTile);     // tokens of the tile that count
-        float x[HL][4];
+        float s[4][HL], x[HL][2];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            float s[HL];
 #pragma unroll
-            for (int i = 0; i < HL; ++i) s[i] = 0.0f;
+            for (int i = 0; i < HL; ++i) s[u][i] = 0.0f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 f4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < BC; ++i) z = mfma16(q[r * BC + i], codes8(kc[u][r * BC + i]), z);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i / BC] = fmaf(z[i], (float)ks[u][r * BC + i % BC], s[i / BC]);
+                for (int i = 0; i < 4; ++i) s[u][i / BC] = fmaf(z[i], (float)ks[u][r * BC + i % BC], s[u][i / BC]);
             }
-#pragma unroll
-            for (int i = 0; i < HL; ++i) x[i][u] = add_halves(s[i]);      // the other part is 32 lanes away
         }
+#pragma unroll
+        for (int i = 0; i < HL; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) x[i][j] = add_halves(s[j][i], s[2 + j][i]);
         if (left < kTile) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (16 * u + c >= left) {
-                    w[u] = hb{};
+            for (int j = 0; j < 2; ++j)
+                if (16 * (2 * (g >> 1) + j) + c >= left) {
+                    w[j] = hb{};
 #pragma unroll
-                    for (int i = 0; i < HL; ++i) x[i][u] = -__builtin_inff();
+                    for (int i = 0; i < HL; ++i) x[i][j] = -__builtin_inff();
                 }
         }
-        hb wmax = __builtin_elementwise_max(__builtin_elementwise_max(w[0], w[1]), __builtin_elementwise_max(w[2], w[3]));
+        const hb wmax = __builtin_elementwise_max(w[0], w[1]);
         _Float16 vtop = wmax[0];
 #pragma unroll
         for (int i = 1; i < NB; ++i) vtop = __builtin_fmaxf16(vtop, wmax[i]);
@@ -498,18 +500,19 @@ next_sequence:
         bool raise = (float)vtop > ldexpf(1.0f, v_exp);
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
-            top[i] = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) * f[i];
+            top[i] = fmaxf(x[i][0], x[i][1]) * f[i];
             raise |= top[i] > m[i] + kSlack;
         }
         if (__any(raise)) {
             float vmax = (float)vtop;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, o));
+            for (int o = 1; o < 64; o <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, o));
             const int en = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
 #pragma unroll
             for (int i = 0; i < HL; ++i) {
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) top[i] = fmaxf(top[i], __shfl_xor(top[i], o));
+                for (int o = 1; o < 64; o <<= 1)
+                    if (o != 16) top[i] = fmaxf(top[i], __shfl_xor(top[i], o));
                 const float mn = fmaxf(m[i], top[i]);
                 const float by = ldexpf(__builtin_amdgcn_exp2f(m[i] - mn), v_exp - en);
                 l[i] *= by;
@@ -525,24 +528,25 @@ next_sequence:
         for (int i = 0; i < HL; ++i) {
             const float up = (float)(kWeightBits - v_exp) - m[i];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x[i][u] = __builtin_amdgcn_exp2f(fmaf(x[i][u], f[i], up));
-                l[i] += x[i][u];
+            for (int j = 0; j < 2; ++j) {
+                x[i][j] = __builtin_amdgcn_exp2f(fmaf(x[i][j], f[i], up));
+                l[i] += x[i][j];
             }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                h4 p;
+            for (int j = 0; j < 2; ++j) {
+                h4 p1, p2;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float xs = x[i / BC][u], ws = (float)w[u][r * BC + i % BC];
-                    // the first part, taken off for the lanes of the second (in bits, so that it is rounded once)
-                    const uint16_t hi = __builtin_bit_cast(uint16_t, (_Float16)(xs * ws)) & second;
-                    p[i] = (_Float16)fmaf(xs, ws, -(float)__builtin_bit_cast(_Float16, hi));
+                    float y = x[i / BC][j] * (float)w[j][r * BC + i % BC];
+                    asm("" : "+v"(y));                           // one rounding of y, whoever uses it
+                    p1[i] = (_Float16)y;
+                    p2[i] = (_Float16)(y - (float)p1[i]);
                 }
-                *(h4 *)(pw + u * 512) = p;
+                *(h4 *)(pw + j * 512) = p1;
+                *(h4 *)(pw + j * 512 + 16) = p2;
             }
             h4 w0, w1, w2, w3;
             read_rows(pr, w0, w1, w2, w3);
@@ -565,7 +569,8 @@ next_sequence:
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor(l[i], o);
+        for (int o = 1; o < 64; o <<= 1)
+            if (o != 16) l[i] += __shfl_xor(l[i], o);
         if (c == 0 && g < 2) {
             state[wave][g * HL + i][0] = m[i];
             state[wave][g * HL + i][1] = bad ? __builtin_nanf("") : ldexpf(l[i], v_exp - kWeightBits);
@@ -616,8 +621,8 @@ next_sequence:
 
 // Joins the pieces of a head in order; writes the rows of empty sequences and
 // of lengths out of range. kJoinParts lanes share a value's pieces: everything a
-// lane needs of 8 pieces is asked for at once, since the kernel is all latency.
-constexpr int kJoinParts = 8;
+// lane needs of 16 pieces is asked for at once, since the kernel is all latency.
+constexpr int kJoinParts = 4, kJoinAhead = 16;
 
 template <int D>
 __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int groups)
@@ -635,10 +640,10 @@ __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int 
     const int kv = a.cache.kv_heads, group = a.heads / kv, per_step = kv * groups, per = (group + groups - 1) / groups;
     const int kh = j / group, hg = j % group / per, hh = j % group % per;
     float m = -3.0e38f, l = 0.0f, o = 0.0f;
-    for (int i0 = part; i0 < at.count; i0 += 8 * kJoinParts) {
-        float pm[8], pl[8], po[8];
+    for (int i0 = part; i0 < at.count; i0 += kJoinAhead * kJoinParts) {
+        float pm[kJoinAhead], pl[kJoinAhead], po[kJoinAhead];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kJoinAhead; ++k) {
             const int i = i0 + k * kJoinParts;
             pm[k] = -3.0e38f;
             pl[k] = po[k] = 0.0f;
@@ -651,13 +656,13 @@ __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int 
         }
         float mn = m;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, pm[k]);
+        for (int k = 0; k < kJoinAhead; ++k) mn = fmaxf(mn, pm[k]);
         const float by = __builtin_amdgcn_exp2f(m - mn);
         l *= by;
         o *= by;
         m = mn;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kJoinAhead; ++k) {
             const float f = __builtin_amdgcn_exp2f(pm[k] - m);
             l = fmaf(f, pl[k], l);
             o = fmaf(f, po[k], o);
