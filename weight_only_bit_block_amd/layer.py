@@ -66,10 +66,12 @@ class KVCache(NamedTuple):
         n, h, page, half = shape
         _need(page == KV_PAGE, "cache pages hold 64 tokens")
         scales = (n, h, page, half // 16)
-        for t, dt, want, name in ((kq, _U8, shape, "kq"), (vq, _U8, shape, "vq"), (ks, _I16, scales, "ks"),
-                                  (vs, _I16, scales, "vs")):
-            if not (t.dtype is dt and t.shape == want and t.get_device() == at and t.is_contiguous()):
-                raise ValueError(f"cache.{name} must be a contiguous {dt} tensor {list(want)} on device {at}")
+        if not (kq.dtype is _U8 and vq.dtype is _U8 and ks.dtype is _I16 and vs.dtype is _I16 and vq.shape == shape
+                and ks.shape == scales and vs.shape == scales):
+            raise ValueError(f"the cache must be uint8 codes {list(shape)} and int16 scales {list(scales)}")
+        for t in self:
+            if not (t.get_device() == at and t.is_contiguous()):
+                raise ValueError(f"the cache's arrays must be contiguous and on device {at}")
         return WqKVCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), n, h, 2 * half)
 
 
@@ -109,31 +111,16 @@ def _table(table, B, at):
     return _index(table, (B, W), "table", at), W
 
 
-class _Here:
-    """The usual case: the current device and its current stream."""
-
-    def __init__(self, at):
-        self.at = at
-
-    def __enter__(self):
-        return _stream(None, self.at)
-
-    def __exit__(self, *exc):
-        return False
-
-
 class _On:
     """A device made current, and allocations taken from `stream`."""
 
     def __init__(self, at, stream):
         _need(stream is None or stream.device.index == at, "stream belongs to another device")
-        self.at, self.stream = at, stream
         self.guards = [torch.cuda.device(at)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return _stream(self.stream, self.at)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -141,8 +128,12 @@ class _On:
         return False
 
 
-def _on(at, stream):
-    return _Here(at) if stream is None and at == torch.cuda.current_device() else _On(at, stream)
+def _run(launch, at, stream):
+    """launch(raw stream) with device `at` current and allocations from the stream."""
+    if stream is None and at == torch.cuda.current_device():
+        return launch(_stream(None, at))
+    with _On(at, stream):
+        return launch(_stream(stream, at))
 
 
 def _workspace(nbytes, like):
@@ -178,15 +169,17 @@ def attn_prefill(q, k, v, cu: Optional[torch.Tensor] = None, scale: Optional[flo
         raise ValueError("k and v must be [T, kv_heads, head_dim] for q's T and head_dim")
     pcu, B = _cu(cu, at)
     lib = load()
-    with _on(at, stream) as s:
-        out, os_ = _out_heads(out, q, (T, H, D), at)
+
+    def launch(s):
+        y, ys = _out_heads(out, q, (T, H, D), at)
         nb = lib.wq_attn_prefill_ws(T, B, H, Hk, D)
         keep, ws = _workspace(nb, q)
         st = lib.wq_attn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, pcu, B, H, Hk, D,
-                                 D ** -0.5 if scale is None else scale, out.data_ptr(), os_, ws, nb, s)
-    if st:
-        raise WqError(st, "wq_attn_prefill")
-    return out
+                                 D ** -0.5 if scale is None else scale, y.data_ptr(), ys, ws, nb, s)
+        if st:
+            raise WqError(st, "wq_attn_prefill")
+        return y
+    return _run(launch, at, stream)
 
 
 def kv_append(cache: KVCache, k, v, table, cu: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
@@ -205,10 +198,12 @@ def kv_append(cache: KVCache, k, v, table, cu: Optional[torch.Tensor] = None, st
     pcu, B = _cu(cu, at)
     pt, W = _table(table, B, at)
     pst = None if start is None else _index(start, (B,), "start", at)
-    with _on(at, stream) as s:
+
+    def launch(s):
         st = load().wq_kv_append(c, k.data_ptr(), ks, v.data_ptr(), vs, T, pcu, pst, B, pt, W, s)
-    if st:
-        raise WqError(st, "wq_kv_append")
+        if st:
+            raise WqError(st, "wq_kv_append")
+    _run(launch, at, stream)
 
 
 def attn_decode(q, cache: KVCache, table, lens, scale: Optional[float] = None, out=None, stream=None):
@@ -224,15 +219,17 @@ def attn_decode(q, cache: KVCache, table, lens, scale: Optional[float] = None, o
     pt, W = _table(table, B, at)
     pl = _index(lens, (B,), "lens", at)
     lib = load()
-    with _on(at, stream) as s:
-        out, os_ = _out_heads(out, q, (B, H, D), at)
+
+    def launch(s):
+        y, ys = _out_heads(out, q, (B, H, D), at)
         nb = lib.wq_attn_decode_ws(B, H, c.kv_heads, D, W)
         keep, ws = _workspace(nb, q)
         st = lib.wq_attn_decode(c, q.data_ptr(), qs, H, pl, B, pt, W, D ** -0.5 if scale is None else scale,
-                                out.data_ptr(), os_, ws, nb, s)
-    if st:
-        raise WqError(st, "wq_attn_decode")
-    return out
+                                y.data_ptr(), ys, ws, nb, s)
+        if st:
+            raise WqError(st, "wq_attn_decode")
+        return y
+    return _run(launch, at, stream)
 
 
 def _rows(t, shape, name, at):
@@ -269,13 +266,15 @@ def residual_norm(h, y=None, post_weight=None, gate=None, alpha: float = 1.0, pr
     _need(want_x or (pre_weight is None and x_out is None), "norm=False with a pre_weight or x_out")
     _need(y is not None or (post_weight is None and gate is None), "post_weight and gate need y")
     _need(want_x or y is not None, "nothing to compute: neither a block output nor a norm")
-    with _on(at, stream) as s:
-        if h_out is None and y is not None:
-            h_out = torch.empty_like(h)
-        if x_out is None and want_x:
-            x_out = torch.empty_like(h)
-        st = load().wq_residual_norm(h.data_ptr(), py, pp, pg, gs, alpha, pw, eps, M, N, _rows(h_out, shape, "h_out", at),
-                                     _rows(x_out, shape, "x_out", at), s)
-    if st:
-        raise WqError(st, "wq_residual_norm")
-    return h_out, x_out
+    ph, px = _rows(h_out, shape, "h_out", at), _rows(x_out, shape, "x_out", at)
+
+    def launch(s):
+        ho = torch.empty_like(h) if h_out is None and y is not None else h_out
+        xo = torch.empty_like(h) if x_out is None and want_x else x_out
+        st = load().wq_residual_norm(h.data_ptr(), py, pp, pg, gs, alpha, pw, eps, M, N,
+                                     ho.data_ptr() if ph is None and ho is not None else ph,
+                                     xo.data_ptr() if px is None and xo is not None else px, s)
+        if st:
+            raise WqError(st, "wq_residual_norm")
+        return ho, xo
+    return _run(launch, at, stream)
