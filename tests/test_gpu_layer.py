@@ -518,6 +518,31 @@ def test_decode_non_finite_data():
         assert (np.abs(got - want[0])[~hit] <= lim[~hit]).all(), which
 
 
+def test_decode_value_scales_of_either_sign():
+    """A cache filled by other means: value scales below zero, far larger than the
+    others, and an infinite one, whose block alone is not finite."""
+    note("decode value scale signs")
+    torch = torch_cuda()
+    heads, kv, d, lens = 4, 2, 128, [700]
+    rng = rng_for(27)
+    table, pages = table_for(rng, lens)
+    q = rng.standard_normal((1, heads, d)).astype(np.float32)
+    host, _ = cache_arrays(rng, pages, kv, d)
+    host[3][:, :, ::3] *= -1
+    host[3][table[0, 2], :, 5, 1] = -20000.0
+    host[3][table[0, 9], :, 40, :] = -300.0
+    want, sums = ref.decode(q, ref.values(*host[:2]), ref.values(*host[2:]), np.abs(host[3]), table, lens, d ** -0.5)
+    lim = ref.bound(sums, 700, d)[0]
+    for inf in (False, True):
+        hit = np.zeros((heads, d), bool)
+        if inf:
+            host[3][table[0, 1], 1, 7, 2] = -np.inf
+            hit[2:, 64:96] = True
+        got = wqa.attn_decode(dev(q), cache_on(host), dev(table), dev(np.array(lens, np.int32))).cpu().numpy()[0]
+        assert not np.isfinite(got[hit]).any(), inf
+        assert (np.abs(got - want[0])[~hit] <= lim[~hit]).all(), inf
+
+
 # ------------------------------------------------------------------ norms
 def norm_bound(h, y, post, gate, alpha, pre, eps, want_h, size, want_x):
     """h_out: t carries the norm (mean of squares: one rounding a square, half

@@ -427,6 +427,7 @@ next_sequence:
         l[i] = 0.0f;
     }
     int v_exp = kMinScaleExp;
+    uint16_t v_limit = 1;                                        // 2^v_exp as binary16 bits
     // Tokens of the output's operands: element e of product x is token 16 (2 x + e / 4) + 4 g + e % 4. The
     // codes' transposed read puts row c of the lanes into nibble c % 8 of dword c / 8, nibble_of(e) = c % 8.
     const int vn = c & 7, ve = vn < 4 ? 2 * vn : 2 * (vn - 4) + 1;
@@ -492,19 +493,21 @@ next_sequence:
                     for (int i = 0; i < HL; ++i) x[i][j] = -__builtin_inff();
                 }
         }
-        const hb wmax = __builtin_elementwise_max(w[0], w[1]);
-        _Float16 vtop = wmax[0];
+        // largest magnitude of the value scales, as bits (what is not finite is larger than what is)
+        typedef uint16_t ub __attribute__((ext_vector_type(NB)));
+        const ub wmax = __builtin_elementwise_max(__builtin_bit_cast(ub, w[0]) & (uint16_t)0x7FFF, __builtin_bit_cast(ub, w[1]) & (uint16_t)0x7FFF);
+        uint16_t vtop = wmax[0];
 #pragma unroll
-        for (int i = 1; i < NB; ++i) vtop = __builtin_fmaxf16(vtop, wmax[i]);
+        for (int i = 1; i < NB; ++i) vtop = vtop > wmax[i] ? vtop : wmax[i];
         float top[HL];
-        bool raise = (float)vtop > ldexpf(1.0f, v_exp);
+        bool raise = vtop > v_limit;
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
             top[i] = fmaxf(x[i][0], x[i][1]) * f[i];
             raise |= top[i] > m[i] + kSlack;
         }
         if (__any(raise)) {
-            float vmax = (float)vtop;
+            float vmax = fminf((float)__builtin_bit_cast(_Float16, vtop), 65504.0f);
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, o));
             const int en = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
@@ -523,6 +526,7 @@ next_sequence:
                     for (int k = 0; k < BC; ++k) acc[n][i * BC + k] *= by;
             }
             v_exp = en;
+            v_limit = __builtin_bit_cast(uint16_t, (_Float16)ldexpf(1.0f, en));
         }
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
