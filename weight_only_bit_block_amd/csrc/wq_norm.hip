@@ -3,15 +3,18 @@
 //   t = y * rsqrt(mean(y^2) + eps) * post,  h' = h + alpha * gate * t,
 //   x = h' * rsqrt(mean(h'^2) + eps) * pre
 //
-// HBM-bound: 12 to 20 bytes a value, one pass. A row is held in registers (4
-// consecutive values a load) from its first read to its last write, by as many
-// threads as it has groups of 4 values up to 1024 threads, which hold up to 8
-// groups each (rows of 32768); longer rows are read once per sum. Many threads
-// with one group each beat few with many, both where rows are few (one row of
-// 1024: 2.6 us against 3.9 us for one wavefront) and where they fill the card
-// (4096 x 1024: 14 against 18 us, 4.7 TB/s). Loads and stores of 4 values ask for
-// 4-byte alignment only, so odd widths and offset storage take the same path;
-// the last values of an odd row go one by one.
+// HBM-bound: 12 to 20 bytes a value, one pass. A row is held in registers from
+// its first read to its last write: 2 groups of 4 consecutive values a thread
+// where 640 threads are enough (3 such workgroups fit a compute unit), then 4
+// (rows of 16384); longer rows are read once per sum (8 groups do not fit 128
+// registers a thread: 256 x 32768 72.7 us, read again 45.6). One group a thread
+// spends more on the barriers of its sums, four leave fewer wavefronts, in us
+// for 1 / 2 / 4 groups, gate and both norms: 1 x 1024 3.9 / 3.9 / 4.4, 4096 x 1024
+// 16.5 / 15.0 / 14.7 (5.7 TB/s), 1024 x 4096 18.1 / 15.7 / 14.6, 515 x 5003
+// - / 15.4 / 17.1, 512 x 8192 - / 19.3 / 15.0. A row of 1024 in one wavefront: 5.0,
+// 4096 of them 17.3. Loads and stores of 4 values ask for 4-byte alignment only,
+// so odd widths and offset storage take the same path; the last values of an odd
+// row go one by one.
 #include "wq_internal.h"
 #include "wq_device.h"
 
@@ -21,6 +24,8 @@ namespace {
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 
+constexpr int kMaxThreads = 1024, kPairThreads = 640;
+
 __device__ __forceinline__ float wave_sum(float v)
 {
 #pragma unroll
@@ -28,24 +33,24 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// Sum over a row's T threads; every thread gets it.
-template <int T>
+// Sum over a row's threads; every thread gets it.
+template <bool ONE>
 __device__ __forceinline__ float row_sum(float v, float *red)
 {
     v = wave_sum(v);
-    if constexpr (T > 64) {
+    if constexpr (!ONE) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
         v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < T / 64; ++w) v += red[w];
+        for (int w = 0; w < (int)blockDim.x / 64; ++w) v += red[w];
     }
     return v;
 }
 
 // 4 values from i on, zeros past the row's end.
-__device__ __forceinline__ f4 load4(const float *p, int64_t i, int64_t N)
+template <typename I>
+__device__ __forceinline__ f4 load4(const float *p, I i, I N)
 {
     if (i + 4 <= N) return *reinterpret_cast<const f4u *>(p + i);
     f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -55,7 +60,8 @@ __device__ __forceinline__ f4 load4(const float *p, int64_t i, int64_t N)
     return v;
 }
 
-__device__ __forceinline__ void store4(float *p, int64_t i, int64_t N, f4 v)
+template <typename I>
+__device__ __forceinline__ void store4(float *p, I i, I N, f4 v)
 {
     if (i + 4 <= N) {
         *reinterpret_cast<f4u *>(p + i) = v;
@@ -82,25 +88,25 @@ __device__ __forceinline__ f4 residual(const NormArgs &a, f4 h, f4 y, f4 post, f
     return r;
 }
 
-// T threads a row, V groups of 4 values a thread; workgroups of one row, or of
-// 4 where a row is a wavefront's.
-template <int T, int V>
-__global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a)
+// V groups of 4 values a thread; workgroups of one row, or, ONE, of 4 rows of a
+// wavefront each.
+template <bool ONE, int V>
+__global__ __launch_bounds__(ONE ? 256 : kMaxThreads) void norm_kernel(NormArgs a)
 {
-    constexpr int kRows = T == 64 ? 4 : 1;
-    __shared__ float red[T / 64];
-    const int tid = threadIdx.x % T;
+    constexpr int kRows = ONE ? 4 : 1;
+    __shared__ float red[kMaxThreads / 64];
+    const uint32_t T = ONE ? 64 : blockDim.x, tid = threadIdx.x % T, N = (uint32_t)a.N;       // (32-bit offsets: N is small)
     for (int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / T; m < a.M; m += (int64_t)gridDim.x * kRows) {
         const float *hp = a.h + m * a.N, *yp = a.y ? a.y + m * a.N : nullptr, *gp = a.gate ? a.gate + m * a.gate_stride : nullptr;
         f4 h[V], y[V], gate[V], post[V], pre[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t i = 4 * (tid + T * v);
-            h[v] = load4(hp, i, a.N);
-            if (yp) y[v] = load4(yp, i, a.N);
-            if (gp) gate[v] = load4(gp, i, a.N);
-            if (a.post) post[v] = load4(a.post, i, a.N);
-            if (a.pre && a.x_out) pre[v] = load4(a.pre, i, a.N);
+            const uint32_t i = 4 * (tid + T * v);
+            h[v] = load4(hp, i, N);
+            if (yp) y[v] = load4(yp, i, N);
+            if (gp) gate[v] = load4(gp, i, N);
+            if (a.post) post[v] = load4(a.post, i, N);
+            if (a.pre && a.x_out) pre[v] = load4(a.pre, i, N);
         }
         if (yp) {
             float ry = 1.0f;
@@ -108,25 +114,25 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a)
                 float s = 0.0f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) s += squares(y[v]);
-                ry = inverse_rms(row_sum<T>(s, red), a.N, a.eps);
+                ry = inverse_rms(row_sum<ONE>(s, red), a.N, a.eps);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = residual(a, h[v], y[v], post[v], gate[v], ry);
         }
         if (a.h_out) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) store4(a.h_out + m * a.N, 4 * (tid + T * v), a.N, h[v]);
+            for (int v = 0; v < V; ++v) store4(a.h_out + m * a.N, 4 * (tid + T * v), N, h[v]);
         }
         if (a.x_out) {
             float s = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) s += squares(h[v]);
-            const float rh = inverse_rms(row_sum<T>(s, red), a.N, a.eps);
+            const float rh = inverse_rms(row_sum<ONE>(s, red), a.N, a.eps);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 f4 x = h[v] * rh;
                 if (a.pre) x *= pre[v];
-                store4(a.x_out + m * a.N, 4 * (tid + T * v), a.N, x);
+                store4(a.x_out + m * a.N, 4 * (tid + T * v), N, x);
             }
         }
     }
@@ -181,12 +187,11 @@ __global__ __launch_bounds__(kLongThreads) void long_norm_kernel(NormArgs a)
     }
 }
 
-template <int T, int V>
-void run(const NormArgs &a, hipStream_t stream)
+template <bool ONE, int V>
+void run(const NormArgs &a, int threads, hipStream_t stream)
 {
-    constexpr int kRows = T == 64 ? 4 : 1;
-    const int64_t groups = (a.M + kRows - 1) / kRows, most = (int64_t)1 << 20;
-    norm_kernel<T, V><<<(unsigned)(groups < most ? groups : most), T == 64 ? 256 : T, 0, stream>>>(a);
+    const int64_t rows = ONE ? 4 : 1, groups = (a.M + rows - 1) / rows, most = (int64_t)1 << 20;
+    norm_kernel<ONE, V><<<(unsigned)(groups < most ? groups : most), threads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -194,15 +199,11 @@ void run(const NormArgs &a, hipStream_t stream)
 hipError_t launch_residual_norm(const NormArgs &a, hipStream_t stream)
 {
     const int64_t groups = (a.N + 3) / 4;                // of 4 values
-    if (groups <= 64) run<64, 1>(a, stream);
-    else if (groups <= 128) run<128, 1>(a, stream);
-    else if (groups <= 256) run<256, 1>(a, stream);
-    else if (groups <= 512) run<512, 1>(a, stream);
-    else if (groups <= 1024) run<1024, 1>(a, stream);
-    else if (groups <= 2048) run<1024, 2>(a, stream);
-    else if (groups <= 4096) run<1024, 4>(a, stream);
-    else if (groups <= 8192) run<1024, 8>(a, stream);
-    else long_norm_kernel<<<(unsigned)(a.M < 65536 ? a.M : 65536), kLongThreads, 0, stream>>>(a);
+    const auto threads = [&](int v) { return (int)((groups + 64 * v - 1) / (64 * v) * 64); };
+    if (groups > 4 * kMaxThreads) long_norm_kernel<<<(unsigned)(a.M < 65536 ? a.M : 65536), kLongThreads, 0, stream>>>(a);
+    else if (groups <= 64) run<true, 1>(a, 256, stream);
+    else if (threads(2) <= kPairThreads) run<false, 2>(a, threads(2), stream);
+    else run<false, 4>(a, threads(4), stream);
     return hipGetLastError();
 }
 
