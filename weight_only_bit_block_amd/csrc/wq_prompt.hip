@@ -258,25 +258,32 @@ struct Query {
     h8 q1[D / 16], q2[D / 16];
 };
 
-// The lane's half of a query, and the power of two that brings it below 2^14;
-// starts the rows' state.
-template <int D>
-__device__ __forceinline__ int load_query(Rows<D> &s, float (&x)[D / 16][8], const float *q, bool live, int c_exp, int half)
+// The lane's half of 16 F values of a query, and the largest of both halves.
+template <int F>
+__device__ __forceinline__ float load_query(float (&x)[F][8], const float *q, bool live, int half)
 {
     float top = 0.0f;
 #pragma unroll
-    for (int f = 0; f < D / 16; ++f)
+    for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
             if (live) v = *reinterpret_cast<const f4 *>(q + 16 * f + 8 * half + 4 * i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[f][4 * i + j] = v[j];
-                top = fmaxf(top, finite_abs(v[j]));
-            }
+            for (int j = 0; j < 4; ++j) x[f][4 * i + j] = v[j];
         }
-    top = fmaxf(top, other_half(top));
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(x[f][j]));
+    return fmaxf(top, other_half(top));
+}
+
+// Starts the rows' state; the power of two that brings the query, `top` its
+// largest value, below 2^14.
+template <int D>
+__device__ __forceinline__ int start_rows(Rows<D> &s, float top, int c_exp)
+{
     const int e = normaliser(top, 14);
     s.q_exp = c_exp - e;
 #pragma unroll
@@ -505,7 +512,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
     Query<D> q;
     {
         float x[D / 16][8];
-        const int e = load_query<D>(s, x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D, live, c_exp, half);
+        const int e = start_rows<D>(s, load_query(x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D, live, half), c_exp);
 #pragma unroll
         for (int f = 0; f < D / 16; ++f) split_query(x[f], e, c_man, q.q1[f], q.q2[f]);
     }
@@ -631,15 +638,21 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
     h8 k[F], v[F];
     TileHead now = head_at(wave);
     int odd = 0;
-    if (wave <= last) load(wave, 0, k);
     Rows<D> s;
     h8 *const qs = reinterpret_cast<h8 *>(res[0]) + lane;        // until the join
     {
-        float x[D / 16][8];
-        const int e = load_query<D>(s, x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D, pos < len, c_exp, half);
+        // each wavefront brings its share of every row's values, D / 4 side by side
+        constexpr int P = D / 16 / kShare;
+        float x[P][8];
+        float most = load_query<P>(x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D + wave * (D / kShare), pos < len, half);
+        if (wave <= last) load(wave, 0, k);
+        if (half == 0) top[wave][lane] = most;
+        __syncthreads();
 #pragma unroll
-        for (int f = 0; f < D / 16; ++f)
-            if (f % kShare == wave) split_query(x[f], e, c_man, qs[64 * f], qs[64 * (D / 16 + f)]);
+        for (int w = 0; w < kShare; ++w) most = fmaxf(most, top[w][lane & 31]);
+        const int e = start_rows<D>(s, most, c_exp);
+#pragma unroll
+        for (int f = 0; f < P; ++f) split_query(x[f], e, c_man, qs[64 * (wave * P + f)], qs[64 * (D / 16 + wave * P + f)]);
     }
     if (wave <= last) load(wave, 1, v);
     __syncthreads();
@@ -703,9 +716,9 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
             *reinterpret_cast<f4 *>(mine + 32 * db + 8 * g) = y;
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * D / 4; i += 64 * kShare) {
-        const int row = i / (D / 4), d = i % (D / 4) * 4;
-        if (row0 + row >= len) break;
+#pragma unroll
+    for (int n = 0; n < 32 * D / 4 / (64 * kShare); ++n) {
+        const int i = threadIdx.x + n * 64 * kShare, row = i / (D / 4), d = i % (D / 4) * 4;
         f4 y = *reinterpret_cast<const f4 *>(res[0] + row * kPitch + d);
         float total = sum[0][row];
 #pragma unroll
@@ -713,7 +726,8 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
             y += *reinterpret_cast<const f4 *>(res[w] + row * kPitch + d);
             total += sum[w][row];
         }
-        *reinterpret_cast<f4 *>(a.out + (int64_t)(r.begin + row0 + row) * a.out_stride + head * D + d) = y * (1.0f / total);
+        if (row0 + row < len)
+            *reinterpret_cast<f4 *>(a.out + (int64_t)(r.begin + row0 + row) * a.out_stride + head * D + d) = y * (1.0f / total);
     }
 }
 
