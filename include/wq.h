@@ -320,9 +320,11 @@ uint64_t wq_attn_prefill_ws(int64_t T, int64_t B, int64_t heads, int64_t kv_head
  * the fp16 matrix cores with every operand split into two binary16 parts (22
  * bits) after power-of-two normalisation of each query row and of every 32
  * consecutive keys or values of a head, partial sums, softmax maximum and sum
- * in fp32. Error: logits within (2^-20 + 2^-38 r) |scale| |q|_2 |k|_2, r the
- * largest magnitude of the 32 keys over the key's own norm; weights and sums add 2^-20 sum p |v| +
- * 2^-36 max |v| per output, the maximum over the visible values of the head.
+ * in fp32. Error, over n visible keys: a logit is within
+ * 2 (3 2^-22 + (3 head_dim / 16 + 4) 2^-24) |scale| |q|_2 |k|_2 (a weight moves
+ * with it, and the sum of weights too), weights and values add
+ * (5 2^-22 + (11 n / 16 + 8) 2^-24) sum p |v| + (2^-36 + n 2^-37) max |v|, the
+ * maximum over the visible values of the head.
  * Non-finite data stays with the rows that see it: a NaN or infinity in a
  * query makes its row NaN, in a key every row that sees the key, in element d of a
  * value element d of every row that sees the value; no other output changes.
@@ -379,7 +381,9 @@ uint64_t wq_attn_decode_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t h
  * inside the kernel (the token itself is appended first). The codes are exact
  * operands of the fp16 matrix cores; q, and the weights times the value
  * scales, are split into two binary16 parts after power-of-two normalisation;
- * sums, softmax maximum and sum in fp32. Long sequences are split over
+ * sums, softmax maximum and sum in fp32. Error: as wq_attn_prefill's for the
+ * dequantized rows, 16 times the head's largest value scale in place of
+ * max |v|. Long sequences are split over
  * workgroups and joined in a fixed order. lens[b] == 0 gives a row of zeros;
  * a non-finite query value makes its head NaN;
  * a length outside [0, 64 * max_pages], or a page outside [0, n_pages) among
@@ -404,7 +408,7 @@ int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, i
  * both); pre_weight null: weight 1. gate is [M][N] (gate_stride N) or one row
  * for all (gate_stride 0). h_out may be h itself; no other outputs alias an
  * input or each other. Rows are contiguous, N >= 1 of any size, and pointers need only
- * 4-byte alignment here. Sums in fp32 (rows above 32768: in fp64).
+ * 4-byte alignment here. Sums in fp32 (rows above 16384: in fp64).
  */
 int wq_residual_norm(const float *h, const float *y, const float *post_weight, const float *gate,
                      int64_t gate_stride, float alpha, const float *pre_weight, float eps,

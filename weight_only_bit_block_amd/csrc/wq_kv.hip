@@ -16,7 +16,8 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 // D values is D / 4 lanes, 4 values each: a wavefront reads 1 KiB of consecutive
 // floats, the maximum of a block goes over its 8 lanes by cross-lane moves.
 // Every thread takes kAppendRows rows, keys and values, and asks for all of
-// them before it looks up where they go (three dependent reads).
+// them before it looks up where they go (three dependent reads). 4096 tokens, 8
+// heads of 128: 12.1 us, 3.2 TB/s.
 //
 // The quotients of wq_pack's rule are correctly rounded; here they cost three
 // operations each instead of a division's ten: q0 = x r, q = q0 + r (x - q0 s)
@@ -160,6 +161,10 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 // workgroup takes an equal run of them, whatever sequences it meets. A sequence
 // that lies in one run is finished there; the pieces of others go to a workspace
 // and a second kernel joins them in order.
+//
+// 8 heads of 128: one sequence of 131072, 2 query heads each, 31 us (4.9 TB/s), joining
+// them 7.4; 64 sequences of 262139 in all, 4 query heads each, 74 us (4.1 TB/s, bound by the
+// vector instructions that make weights of scores and numbers of codes), joining 7.8.
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));

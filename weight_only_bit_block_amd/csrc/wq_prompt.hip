@@ -28,6 +28,11 @@
 // visible row) of v seen so far; tiles are walked first to last, so that its
 // precision never depends on values it does not see by more than the 2^14 of
 // one tile.
+//
+// Bound: the matrix cores in long prompts (8192 tokens, 16 heads of 128: 819 us,
+// 1006 TFLOP/s of binary16 products where a large library product reaches 1205), the
+// latency of both launches in short ones (128 tokens: 11.4 us), in between the L2's
+// k and v and the issue of matrix and vector instructions in turns (1024 tokens: 31 us).
 #include "wq_internal.h"
 #include "wq_device.h"
 #include "wq_seq.h"
