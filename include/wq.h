@@ -389,7 +389,7 @@ uint64_t wq_attn_decode_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t h
  * a length outside [0, 64 * max_pages], or a page outside [0, n_pages) among
  * those the length covers, gives rows of NaN for that sequence and reads
  * nothing outside the cache. Rows past lens[b] may hold anything.
- * B * heads is below 2^24, max_pages below 2^25.
+ * B * heads is below 2^23, max_pages below 2^25, B * max_pages below 2^32.
  */
 int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
                    const int32_t *lens, int64_t B, const int32_t *table, int64_t max_pages, float scale,

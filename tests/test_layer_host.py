@@ -102,6 +102,8 @@ def test_decode_refusals(lib):
     for bad in (dict(H=12), dict(H=0), dict(B=-1), dict(W=-1), dict(W=1 << 25), dict(qs=1024), dict(os=2046),
                 dict(B=1 << 16, H=256, qs=1 << 15, os=1 << 15), dict(B=1 << 20, H=16)):
         assert _decode(lib, **bad) == SHAPE, bad
+    for bad in (dict(B=1 << 13, H=1 << 10, qs=1 << 17, os=1 << 17), dict(B=1 << 8, W=1 << 24)):
+        assert _decode(lib, **bad) == SHAPE, bad
     for bad in (dict(q=None), dict(lens=None), dict(out=None), dict(table=None)):
         assert _decode(lib, **bad) == NULL, bad
     for bad in (dict(q=MIS), dict(lens=FAKE + 2), dict(out=MIS), dict(table=FAKE + 1)):

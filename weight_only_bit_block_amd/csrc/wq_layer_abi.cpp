@@ -65,7 +65,8 @@ int check_decode(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, i
     int st = check_heads(heads, kv_heads, head_dim);
     if (st) return st;
     if (B < 0 || B >= kMaxSeqs || max_pages < 0 || max_pages >= (int64_t)1 << 25) return WQ_ERR_SHAPE;
-    if (B * heads >= kMaxGroups) return WQ_ERR_SHAPE;
+    // the join's workgroups of up to 512 threads, below 2^32 threads in all; steps are counted in 31 bits
+    if (B * heads >= kMaxGroups / 2 || B * max_pages >= (int64_t)1 << 32) return WQ_ERR_SHAPE;
     return WQ_OK;
 }
 
