@@ -365,9 +365,11 @@ next_sequence:
         for (int i = 0; i < kCodeBytes / 1024; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(dst + i * 1024), 16,
                                                      values ? (D == 128 ? vat ^ i << 4 : vat) : kat, i * 1024, 0, kNonTemporal);
-        if (lane < kScaleBytes / 16)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)(dst + kCodeBytes), 16,
-                                                     lane * 16, 0, 0, kNonTemporal);
+        // (4 bytes a lane: with 16, half of the lanes would be left out and the compiler doubles what follows)
+#pragma unroll
+        for (int i = 0; i < kScaleBytes / 256; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)(dst + kCodeBytes + i * 256), 4,
+                                                     lane * 4, i * 256, 0, kNonTemporal);
     };
     uint8_t *kbuf = lds[wave], *vbuf = kbuf + kHalf, *pbuf = vbuf + kHalf;
     const bool any_page = a.cache.n_pages > 0;
