@@ -60,11 +60,13 @@ __device__ __forceinline__ f4 load4(const float *p, I i, I N)
     return v;
 }
 
+// (Stored non-temporally: lines still dirty in the L2 when the kernel ends delay
+// what follows, 2048 x 1024 10.0 -> 8.5 us, 512 x 8192 15.4 -> 13.7.)
 template <typename I>
 __device__ __forceinline__ void store4(float *p, I i, I N, f4 v)
 {
     if (i + 4 <= N) {
-        *reinterpret_cast<f4u *>(p + i) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<f4u *>(p + i));
     } else {
 #pragma unroll
         for (int j = 0; j < 3; ++j)

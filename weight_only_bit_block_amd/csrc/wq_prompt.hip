@@ -123,6 +123,16 @@ __device__ __forceinline__ float max_dpp(float x)
     return fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true)));
 }
 
+// Stores that leave the L2 at once: what is still dirty there when a kernel ends
+// delays the next one's start (1024 tokens: 32.4 us without, 30.8 with them). `at`
+// in values from the tile's k or v on.
+template <int D>
+__device__ __forceinline__ void store_through(_Float16 *dst, int at, h8 x)
+{
+    constexpr int kSc0Sc1 = 17;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), make_rsrc(dst, tile_halves(D)), at * 2, 0, kSc0Sc1);
+}
+
 template <int D>
 __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__restrict__ tiles, TileMeta *__restrict__ metas)
 {
@@ -205,8 +215,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__
                 lo[j] = z;
             }
             const int o = f * 512 + (half * 32 + row) * 8;
-            *reinterpret_cast<h8 *>(dst + o) = hi;
-            *reinterpret_cast<h8 *>(dst + D * kTileKeys + o) = lo;
+            store_through<D>(dst, o, hi);
+            store_through<D>(dst, D * kTileKeys + o, lo);
         }
         return;
     }
@@ -236,8 +246,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__
             hi[j] = p;
             lo[j] = z;
         }
-        *reinterpret_cast<h8 *>(dst + c * 8) = hi;
-        *reinterpret_cast<h8 *>(dst + D * kTileKeys + c * 8) = lo;
+        store_through<D>(dst, c * 8, hi);
+        store_through<D>(dst, D * kTileKeys + c * 8, lo);
     }
 }
 
