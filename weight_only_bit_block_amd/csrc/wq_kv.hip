@@ -291,7 +291,7 @@ __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
     return {0, 0, 0, 0};
 }
 
-constexpr int kPartialExtra = 2;             // a partial result: D values, then m and l
+constexpr int kPartialExtra = 4;             // a partial result: D values, then m and l, 16-byte aligned
 
 // Piece `slot` of a workgroup, head hh.
 template <int D>
@@ -631,38 +631,44 @@ next_sequence:
 }
 
 // Joins the pieces of a head in order; writes the rows of empty sequences and
-// of lengths out of range. kJoinParts lanes share a value's pieces: everything a
-// lane needs of 16 pieces is asked for at once, since the kernel is all latency.
-constexpr int kJoinParts = 4, kJoinAhead = 16;
+// of lengths out of range. A thread takes 4 values of every kJoinParts-th piece and
+// asks for all it needs of kJoinAhead pieces at once, since the kernel is all latency.
+constexpr int kJoinParts = 8, kJoinAhead = 8;
 
 template <int D>
-__global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int groups)
+__global__ __launch_bounds__(D / 4 * kJoinParts) void join_kernel(DecodeArgs a, int groups)
 {
-    __shared__ float red[kJoinParts][D], ml[kJoinParts][2];
-    const int b = blockIdx.x / a.heads, j = blockIdx.x % a.heads, d = threadIdx.x % D, part = threadIdx.x / D;
+    constexpr int V = D / 4;                     // threads of a part
+    __shared__ f4 red[kJoinParts][V];
+    __shared__ float ml[kJoinParts][2];
+    const int b = blockIdx.x / a.heads, j = blockIdx.x % a.heads, c = threadIdx.x % V, part = threadIdx.x / V;
     const Pieces at = ((const Pieces *)a.ws)[b];
     const int64_t len = a.lens[b];
-    float *out = a.out + (int64_t)b * a.out_stride + j * D + d;
+    f4 *out = (f4 *)(a.out + (int64_t)b * a.out_stride + j * D) + c;
     if (len <= 0 || len > a.max_pages * kTile) {
-        if (part == 0) *out = len == 0 ? 0.0f : __builtin_nanf("");
+        const float y = len == 0 ? 0.0f : __builtin_nanf("");
+        if (part == 0) *out = f4{y, y, y, y};
         return;
     }
     if (at.count == 1) return;                   // written already
     const int kv = a.cache.kv_heads, group = a.heads / kv, per_step = kv * groups, per = (group + groups - 1) / groups;
     const int kh = j / group, hg = j % group / per, hh = j % group % per;
-    float m = -3.0e38f, l = 0.0f, o = 0.0f;
+    float m = -3.0e38f, l = 0.0f;
+    f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int i0 = part; i0 < at.count; i0 += kJoinAhead * kJoinParts) {
-        float pm[kJoinAhead], pl[kJoinAhead], po[kJoinAhead];
+        float pm[kJoinAhead], pl[kJoinAhead];
+        f4 po[kJoinAhead];
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) {
             const int i = i0 + k * kJoinParts;
             pm[k] = -3.0e38f;
-            pl[k] = po[k] = 0.0f;
+            pl[k] = 0.0f;
+            po[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
             if (i < at.count) {
                 const float *p = partial<D>(a, (int64_t)(at.first + i) * per_step + hg * kv + kh, i == 0 ? at.slot : 0, hh);
                 pm[k] = p[D];
                 pl[k] = p[D + 1];
-                po[k] = p[d];
+                po[k] = ((const f4 *)p)[c];
             }
         }
         float mn = m;
@@ -676,11 +682,11 @@ __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int 
         for (int k = 0; k < kJoinAhead; ++k) {
             const float f = __builtin_amdgcn_exp2f(pm[k] - m);
             l = fmaf(f, pl[k], l);
-            o = fmaf(f, po[k], o);
+            o += f * po[k];
         }
     }
-    red[part][d] = o;
-    if (d == 0) {
+    red[part][c] = o;
+    if (c == 0) {
         ml[part][0] = m;
         ml[part][1] = l;
     }
@@ -689,12 +695,13 @@ __global__ __launch_bounds__(D * kJoinParts) void join_kernel(DecodeArgs a, int 
         float mn = ml[0][0];
 #pragma unroll
         for (int w = 1; w < kJoinParts; ++w) mn = fmaxf(mn, ml[w][0]);
-        float ll = 0.0f, oo = 0.0f;
+        float ll = 0.0f;
+        f4 oo = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kJoinParts; ++w) {
             const float f = __builtin_amdgcn_exp2f(ml[w][0] - mn);
             ll = fmaf(f, ml[w][1], ll);
-            oo = fmaf(f, red[w][d], oo);
+            oo += f * red[w][c];
         }
         *out = oo / ll;
     }
@@ -740,8 +747,8 @@ hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !cut) return e;
     const unsigned jobs = (unsigned)(a.B * a.heads);
-    if (a.cache.head_dim == 128) join_kernel<128><<<jobs, 128 * kJoinParts, 0, stream>>>(a, groups);
-    else join_kernel<64><<<jobs, 64 * kJoinParts, 0, stream>>>(a, groups);
+    if (a.cache.head_dim == 128) join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, groups);
+    else join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, groups);
     return hipGetLastError();
 }
 
