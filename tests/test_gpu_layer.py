@@ -70,7 +70,7 @@ def test_prompt_parity(heads, kv, d, lens):
     check_prompt(out, host, lens, d ** -0.5, what=str(lens))
 
 
-@pytest.mark.parametrize("T,heads", [(1, 16), (5, 16), (100, 16), (1023, 4), (2049, 4), (700, 60)])
+@pytest.mark.parametrize("T,heads", [(1, 16), (5, 16), (100, 16), (1023, 4), (2049, 4), (700, 60), (700, 80)])
 def test_prompt_single(T, heads):
     note(f"prompt single {T} {heads}")
     torch = torch_cuda()

@@ -163,8 +163,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 // and a second kernel joins them in order.
 //
 // 8 heads of 128: one sequence of 131072, 2 query heads each, 31 us (4.9 TB/s), joining
-// them 7.4; 64 sequences of 262139 in all, 4 query heads each, 74 us (4.1 TB/s, bound by the
-// vector instructions that make weights of scores and numbers of codes), joining 7.8.
+// them 5.9; 64 sequences of 262139 in all, 4 query heads each, 74 us (4.1 TB/s, bound by the
+// vector instructions that make weights of scores and numbers of codes), joining 4.8.
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -224,8 +224,8 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
 // fill the card by themselves) are not cut, one workgroup each, and neither are
 // short ones: tables of up to 16 pages, or 32 where there are kFill / 2
 // workgroups without (us, uncut / cut, 8 kv heads of 128, 2 query heads each:
-// 1 x 500 tokens 7.9 / 10.5, 1 x 1024 11.0 / 10.7 but 12 / 17 with the launches, 1 x 2048
-// 17.2 / 11.2, 32 x 777 12.8 / 17.2, 32 x 2048 20.7 / 24.7).
+// 1 x 500 tokens 8.1 / 10.8, 1 x 1000 10.9 / 10.9, 1 x 2040 17.0 / 11.1, 16 x 1500
+// 15.7 / 16.9, 32 x 777 12.7 / 17.6, 32 x 2040 20.4 / 23.7).
 constexpr int kFill = 512;
 constexpr int kCutMaxSeqs = 512;
 constexpr int kShortPages = 16;

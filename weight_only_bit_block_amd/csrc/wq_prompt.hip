@@ -751,11 +751,11 @@ inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((u
 
 // Up to so many workgroups of 128 rows, prompts run on the kernel whose wavefronts
 // share 32 rows. Measured, both kernels (us, shared / other): 16 heads of 128,
-// one prompt of 1024 (144 groups) 35 / 67, 2048 (272) 95 / 124, 4096 (528)
-// 284 / 277; 8 prompts of 256 (384) 41 / 40; 64 heads, 512 tokens (320) 41 / 43;
-// 16 heads of 64, 4096 tokens (528) 154 / 179, 6000 (752) 290 / 300, 8 prompts
-// of 1024 (1152) 114 / 101.
-constexpr int64_t few_groups(int D) { return D == 128 ? 352 : 768; }
+// one prompt of 1024 (144 groups) 32 / 64, 2048 (272) 85 / 117, 3000 (384)
+// 154 / 173, 4096 (528) 264 / 266; 8 prompts of 256 (384) 33 / 36, 6 of 512 (480)
+// 54 / 52; 64 heads, 700 tokens (384) 50 / 51, 1024 (576) 85 / 78; 16 heads of 64,
+// 4096 tokens (528) 143 / 170, 16 prompts of 256 (768) 32 / 32, 8 of 1024 (1152) 97 / 96.
+constexpr int64_t few_groups(int D) { return D == 128 ? 448 : 768; }
 
 template <int D>
 hipError_t launch(const PromptArgs &a, hipStream_t stream)
