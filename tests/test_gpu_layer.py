@@ -102,7 +102,7 @@ def test_prompt_strides():
     assert torch.isnan(wide[:, :16]).all() and torch.isnan(wide[:, 16 + 6 * 64:]).all()
 
 
-@pytest.mark.parametrize("heads", [4, 120])
+@pytest.mark.parametrize("heads", [4, 120, 2])
 @pytest.mark.parametrize("what", ["outlier_keys", "peaked", "tiny", "huge", "value_spread", "key_spread", "equal", "one_channel"])
 def test_prompt_range(what, heads):
     """Magnitudes the normalisation has to carry: single rows far above the
@@ -110,7 +110,7 @@ def test_prompt_range(what, heads):
     span 2^60 between rows."""
     note(f"prompt range {what} {heads}")
     torch = torch_cuda()
-    kv, d, lens = 2, 128, [200, 77]
+    kv, d, lens = 2, 128, [70, 45] if heads == 2 else [200, 77]          # 2: short enough for one kernel
     T = sum(lens)
     rng = rng_for(5, len(what))
     y = rng.standard_normal((T, (heads + 2 * kv) * d)).astype(np.float32)

@@ -42,13 +42,16 @@ def test_prefill_refusals(lib):
 
 
 def test_prefill_workspace(lib):
-    need = lib.wq_attn_prefill_ws(8, 2, 16, 8, 128)
+    need = lib.wq_attn_prefill_ws(800, 2, 16, 8, 128)
     assert need > 0 and need % 256 == 0
-    assert lib.wq_attn_prefill_ws(8, 2, 15, 8, 128) == 0 and lib.wq_attn_prefill_ws(0, 2, 16, 8, 128) == 0
-    assert _prefill(lib, ws=None) == NULL and _prefill(lib, ws=MIS) == ALIGN and _prefill(lib, wsb=need - 1) == SHAPE
+    assert lib.wq_attn_prefill_ws(800, 2, 15, 8, 128) == 0 and lib.wq_attn_prefill_ws(0, 2, 16, 8, 128) == 0
+    assert _prefill(lib, T=800, ws=None) == NULL and _prefill(lib, T=800, ws=MIS) == ALIGN
+    assert _prefill(lib, T=800, wsb=need - 1) == SHAPE
+    # the shortest prompts take none
+    assert lib.wq_attn_prefill_ws(8, 2, 16, 8, 128) == 0 and lib.wq_attn_prefill_ws(8, 2000, 16, 8, 128) > 0
     # a tile of 32 keys is 4 binary16 operands; sequences may begin anywhere, so each adds one tile
     tile = 4 * 128 * 32 * 2
-    for T, B in ((1, 1), (31, 1), (32, 1), (33, 3), (4096, 9)):
+    for T, B in ((129, 1), (191, 1), (192, 1), (193, 3), (4096, 9)):
         slots = T // 32 + B
         got = lib.wq_attn_prefill_ws(T, B, 16, 8, 128)
         assert slots * 8 * tile <= got <= slots * 8 * (tile + 512) + 256

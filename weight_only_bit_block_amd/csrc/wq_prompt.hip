@@ -8,7 +8,7 @@
 // product is three matrix products, x1 y1 + x1 y2 + x2 y1. That is a third of
 // the fp16 rate, 2.6 times the rate of the fp32 matrix instructions.
 //
-// Two kernels:
+// Two kernels, and one for very short prompts that does without the first (attend_direct_kernel):
 //   prepare_kernel  splits k and v once per call into a workspace, in tiles of
 //     32 keys per key/value head that begin at the sequence's first token, in
 //     the order the matrix instructions take their operands (a fragment is
@@ -445,6 +445,23 @@ __device__ __forceinline__ void accumulate(Rows<D> &s, const h8 *v1, int t, h8 p
     }
 }
 
+// The same from v in registers (v1 then v2), all 32 keys.
+template <int D>
+__device__ __forceinline__ void accumulate_held(Rows<D> &s, const h8 (&v)[D / 8], const f16v &x)
+{
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        h8 p1, p2;
+        split8(x, t, p1, p2);
+#pragma unroll
+        for (int db = 0; db < D / 32; ++db) {
+            s.o[db] = mfma(v[D / 16 + 2 * db + t], p1, s.o[db]);
+            s.o[db] = mfma(v[2 * db + t], p2, s.o[db]);
+            s.o[db] = mfma(v[2 * db + t], p1, s.o[db]);
+        }
+    }
+}
+
 // Weights of a tile with wild v, whose rows have a factor each.
 template <int D>
 __device__ __forceinline__ void weigh_rows(const Rows<D> &s, f16v &x, const TileMeta *meta, int half)
@@ -620,107 +637,72 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
 
 // Few rows: the 4 wavefronts of a workgroup share 32 rows and take every fourth
 // tile each, so that short prompts fill the card and no wavefront walks far; what
-// they found is joined through LDS. k and v come from L2 straight into
-// registers, a tile ahead; the queries, the same for all, stay in LDS.
+// they found is joined through LDS, where the queries, the same for all, stay
+// until then.
 constexpr int kShare = 4;
 
-template <int D>
-__global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArgs a, const _Float16 *__restrict__ tiles,
-                                                                      const TileMeta *__restrict__ metas, float c_man,
-                                                                      int c_exp, int slots)
+constexpr int result_pitch(int D) { return D + 4; }             // floats between rows of results
+struct RowSums {
+    float top[kShare][32], sum[kShare][32];
+};
+
+// Where a workgroup's rows are.
+struct Block {
+    int head, kvh, b, last;                      // last: block of 32 rows within sequence b, and its last tile
+    SeqRange r;
+    int len, row0;
+};
+
+__device__ __forceinline__ Block find_block(const PromptArgs &a, int slots)
 {
-    constexpr int F = D / 8, kPitch = D + 4;     // operands of k or v (both parts); floats between rows of LDS
-    __shared__ __attribute__((aligned(16))) float res[kShare][32 * kPitch];
-    __shared__ float top[kShare][32], sum[kShare][32];
-    const int id = blockIdx.x, group = a.heads / a.kv_heads;
-    const int hp = id % a.heads, kvh = hp % a.kv_heads, head = kvh * group + hp / a.kv_heads;
+    Block x;
+    const int id = blockIdx.x, group = a.heads / a.kv_heads, hp = id % a.heads;
+    x.kvh = hp % a.kv_heads;
+    x.head = x.kvh * group + hp / a.kv_heads;
     // long blocks first, then short ones: a compute unit that begins with a long one gets a short one beside it
     const int rank = id / a.heads, slot = rank < (slots + 1) / 2 ? slots - 1 - rank : rank - (slots + 1) / 2;
-    const int b = seq_of_slot(a.cu, (int)a.T, a.B, 32, slot);
-    const SeqRange r = seq_range(a.cu, (int)a.T, b);
-    const int len = r.end - r.begin, last = __builtin_amdgcn_readfirstlane(slot - first_slot(r.begin, b, 32)), row0 = last * 32;
-    if (row0 < 0 || row0 >= len) return;
-    const int lane = threadIdx.x & 63, half = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int pos = row0 + (lane & 31);
-    const int step = a.kv_heads, at0 = __builtin_amdgcn_readfirstlane(first_slot(r.begin, b, kTileKeys) * step + kvh);
-    auto load = [&](int tile, int values, h8 (&x)[F]) {
-        const h8 *src = reinterpret_cast<const h8 *>(tiles + (int64_t)(at0 + tile * step) * tile_halves(D)) + values * (2 * D * kTileKeys / 8);
-#pragma unroll
-        for (int f = 0; f < F; ++f) x[f] = (src + 64 * f)[lane];
-    };
-    const auto head_at = [&](int t) { return head_of(metas + at0 + (t <= last ? t : last) * step); };
-    h8 k[F], v[F];
-    TileHead now = head_at(wave);
-    int odd = 0;
-    Rows<D> s;
-    h8 *const qs = reinterpret_cast<h8 *>(res[0]) + lane;        // until the join
-    {
-        // each wavefront brings its share of every row's values, D / 4 side by side
-        constexpr int P = D / 16 / kShare;
-        float x[P][8];
-        float most = load_query<P>(x, a.q + (int64_t)(r.begin + pos) * a.q_stride + head * D + wave * (D / kShare), pos < len, half);
-        if (wave <= last) load(wave, 0, k);
-        if (half == 0) top[wave][lane] = most;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kShare; ++w) most = fmaxf(most, top[w][lane & 31]);
-        const int e = start_rows<D>(s, most, c_exp);
-#pragma unroll
-        for (int f = 0; f < P; ++f) split_query(x[f], e, c_man, qs[64 * (wave * P + f)], qs[64 * (D / 16 + wave * P + f)]);
-    }
-    if (wave <= last) load(wave, 1, v);
+    x.b = seq_of_slot(a.cu, (int)a.T, a.B, 32, slot);
+    x.r = seq_range(a.cu, (int)a.T, x.b);
+    x.len = x.r.end - x.r.begin;
+    x.last = __builtin_amdgcn_readfirstlane(slot - first_slot(x.r.begin, x.b, 32));
+    x.row0 = x.last * 32;
+    return x;
+}
+
+// Each wavefront brings its share of every row's values, D / 4 side by side, into
+// LDS (q1 then q2; qs: this lane's part); `between` runs while they are under way. The caller lets all waves meet.
+template <int D, typename F>
+__device__ __forceinline__ void share_queries(Rows<D> &s, h8 *qs, RowSums &sh, const float *q, bool live, float c_man, int c_exp,
+                                              int lane, int wave, F between)
+{
+    constexpr int P = D / 16 / kShare;
+    const int half = lane >> 5;
+    float x[P][8];
+    float most = load_query<P>(x, q + wave * (D / kShare), live, half);
+    between();
+    if (half == 0) sh.top[wave][lane] = most;
     __syncthreads();
-    for (int t = wave; t <= last; t += kShare) {
-        const TileMeta *meta = metas + at0 + t * step;
-        const TileHead next = head_at(t + kShare);
-        const bool edge = t == last;
-        const int first = t * kTileKeys - pos;
-        __builtin_amdgcn_sched_barrier(0);
-        f16v x = scores<D>(qs, k);
-        // two reads of queries ahead, not all of them: registers are what is short
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
-        for (int f = 0; f < D / 16; ++f) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);       // (moved up, the loads would need registers of their own)
-        if (t + kShare <= last) load(t + kShare, 0, k);
-        settle<D>(s, x, now, meta, edge, first, half);
-        weigh<D>(s, x);
-        if (now.flags & kWildV) weigh_rows<D>(s, x, meta, half);
+    for (int w = 0; w < kShare; ++w) most = fmaxf(most, sh.top[w][lane & 31]);
+    const int e = start_rows<D>(s, most, c_exp);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            h8 p1, p2;
-            split8(x, h, p1, p2);
-#pragma unroll
-            for (int db = 0; db < D / 32; ++db) {
-                s.o[db] = mfma(v[F / 2 + 2 * db + h], p1, s.o[db]);
-                s.o[db] = mfma(v[2 * db + h], p2, s.o[db]);
-                s.o[db] = mfma(v[2 * db + h], p1, s.o[db]);
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (t + kShare <= last) load(t + kShare, 1, v);
-        odd |= now.flags & kOddV;
-        now = next;
-    }
-    if (odd)                                     // (apart from the loop, whose registers it would take)
-        for (int t = wave; t <= last; t += kShare)
-            if (metas[at0 + t * step].v_flags & kOddV)
-                odd_values<D>(s, t == last, t * kTileKeys - pos,
-                              a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
-                              len - t * kTileKeys, lane);
-    // join: results in units of the largest maximum (the queries have been read when all meet)
-    if (half == 0) top[wave][lane] = s.m;
+    for (int f = 0; f < P; ++f) split_query(x[f], e, c_man, qs[64 * (wave * P + f)], qs[64 * (D / 16 + wave * P + f)]);
+}
+
+// Results in units of the largest maximum (the queries have been read when all meet).
+template <int D>
+__device__ __forceinline__ void join_rows(const PromptArgs &a, const Block &x, const Rows<D> &s, float *res, RowSums &sh, int lane, int wave)
+{
+    constexpr int kPitch = result_pitch(D);
+    const int half = lane >> 5;
+    if (half == 0) sh.top[wave][lane] = s.m;
     __syncthreads();
-    float m = top[0][lane & 31];
+    float m = sh.top[0][lane & 31];
 #pragma unroll
-    for (int w = 1; w < kShare; ++w) m = fmaxf(m, top[w][lane & 31]);
+    for (int w = 1; w < kShare; ++w) m = fmaxf(m, sh.top[w][lane & 31]);
     const float by = __builtin_amdgcn_exp2f(s.m - m), l = (s.l + other_half(s.l)) * by;
-    if (half == 0) sum[wave][lane] = l;
-    float *mine = res[wave] + (lane & 31) * kPitch + 4 * half;
+    if (half == 0) sh.sum[wave][lane] = l;
+    float *mine = res + (wave * 32 + (lane & 31)) * kPitch + 4 * half;
 #pragma unroll
     for (int db = 0; db < D / 32; ++db)
 #pragma unroll
@@ -734,16 +716,289 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
 #pragma unroll
     for (int n = 0; n < 32 * D / 4 / (64 * kShare); ++n) {
         const int i = threadIdx.x + n * 64 * kShare, row = i / (D / 4), d = i % (D / 4) * 4;
-        f4 y = *reinterpret_cast<const f4 *>(res[0] + row * kPitch + d);
-        float total = sum[0][row];
+        f4 y = *reinterpret_cast<const f4 *>(res + row * kPitch + d);
+        float total = sh.sum[0][row];
 #pragma unroll
         for (int w = 1; w < kShare; ++w) {
-            y += *reinterpret_cast<const f4 *>(res[w] + row * kPitch + d);
-            total += sum[w][row];
+            y += *reinterpret_cast<const f4 *>(res + (w * 32 + row) * kPitch + d);
+            total += sh.sum[w][row];
         }
-        if (row0 + row < len)
-            *reinterpret_cast<f4 *>(a.out + (int64_t)(r.begin + row0 + row) * a.out_stride + head * D + d) = y * (1.0f / total);
+        if (x.row0 + row < x.len)
+            *reinterpret_cast<f4 *>(a.out + (int64_t)(x.r.begin + x.row0 + row) * a.out_stride + x.head * D + d) = y * (1.0f / total);
     }
+}
+
+// Prepared k and v come from L2 straight into registers, a tile ahead.
+template <int D>
+__global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArgs a, const _Float16 *__restrict__ tiles,
+                                                                      const TileMeta *__restrict__ metas, float c_man,
+                                                                      int c_exp, int slots)
+{
+    constexpr int F = D / 8;                     // operands of k or v (both parts)
+    __shared__ __attribute__((aligned(16))) float res[kShare * 32 * result_pitch(D)];           // until the join: queries
+    __shared__ RowSums sh;
+    const Block x = find_block(a, slots);
+    if (x.row0 < 0 || x.row0 >= x.len) return;
+    const int lane = threadIdx.x & 63, half = lane >> 5, last = x.last;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int pos = x.row0 + (lane & 31);
+    const int step = a.kv_heads, at0 = __builtin_amdgcn_readfirstlane(first_slot(x.r.begin, x.b, kTileKeys) * step + x.kvh);
+    auto load = [&](int tile, int values, h8 (&y)[F]) {
+        const h8 *src = reinterpret_cast<const h8 *>(tiles + (int64_t)(at0 + tile * step) * tile_halves(D)) + values * (2 * D * kTileKeys / 8);
+#pragma unroll
+        for (int f = 0; f < F; ++f) y[f] = (src + 64 * f)[lane];
+    };
+    const auto head_at = [&](int t) { return head_of(metas + at0 + (t <= last ? t : last) * step); };
+    h8 k[F], v[F];
+    TileHead now = head_at(wave);
+    int odd = 0;
+    Rows<D> s;
+    h8 *const qs = reinterpret_cast<h8 *>(res) + lane;
+    share_queries<D>(s, qs, sh, a.q + (int64_t)(x.r.begin + pos) * a.q_stride + x.head * D, pos < x.len, c_man, c_exp, lane, wave,
+                     [&]() { if (wave <= last) load(wave, 0, k); });
+    if (wave <= last) load(wave, 1, v);
+    __syncthreads();
+    for (int t = wave; t <= last; t += kShare) {
+        const TileMeta *meta = metas + at0 + t * step;
+        const TileHead next = head_at(t + kShare);
+        const bool edge = t == last;
+        const int first = t * kTileKeys - pos;
+        __builtin_amdgcn_sched_barrier(0);
+        f16v y = scores<D>(qs, k);
+        // two reads of queries ahead, not all of them: registers are what is short
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int f = 0; f < D / 16; ++f) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);       // (moved up, the loads would need registers of their own)
+        if (t + kShare <= last) load(t + kShare, 0, k);
+        settle<D>(s, y, now, meta, edge, first, half);
+        weigh<D>(s, y);
+        if (now.flags & kWildV) weigh_rows<D>(s, y, meta, half);
+        accumulate_held<D>(s, v, y);
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + kShare <= last) load(t + kShare, 1, v);
+        odd |= now.flags & kOddV;
+        now = next;
+    }
+    if (odd)                                     // (apart from the loop, whose registers it would take)
+        for (int t = wave; t <= last; t += kShare)
+            if (metas[at0 + t * step].v_flags & kOddV)
+                odd_values<D>(s, t == last, t * kTileKeys - pos,
+                              a.v + (int64_t)(x.r.begin + t * kTileKeys) * a.v_stride + x.kvh * D, a.v_stride,
+                              x.len - t * kTileKeys, lane);
+    join_rows<D>(a, x, s, res, sh, lane, wave);
+}
+
+// ---------------------------------------------------------------- attend, without prepare
+// Very few rows: a launch costs more than splitting k and v where they are used.
+// As attend_shared_kernel, but every wavefront copies its own tiles as they are
+// into LDS and splits them on the way to the operands: rows for k and for the
+// maxima of v, columns for v. 16-byte pieces of a row are swizzled by row.
+__device__ __forceinline__ float wave_max(float x)             // over 32 lanes; both halves hold the same
+{
+    x = max_dpp<0xB1>(x);                        // quad_perm 1 0 3 2, 2 3 0 1, row_half_mirror, row_ror:8
+    x = max_dpp<0x4E>(x);
+    x = max_dpp<0x141>(x);
+    x = max_dpp<0x128>(x);
+    return fmaxf(x, __shfl_xor(x, 16));
+}
+
+// Largest magnitude of a row, half of it per lane, what is not finite left out; `odd`: there was some.
+template <int D>
+__device__ __forceinline__ float row_top(const float (&x)[D / 16][8], bool &odd)
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = __builtin_elementwise_maximum(top, fabsf(x[f][j]));       // (a NaN stays)
+    odd = !(top <= kBig);
+    if (__any(odd)) {
+        top = 0.0f;
+#pragma unroll
+        for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(x[f][j]));
+    }
+    return fmaxf(top, other_half(top));
+}
+
+// Values times a power of two that is no number by itself; by: 1 from then on.
+template <int F>
+__device__ __forceinline__ void scale_row(float (&x)[F][8], int e, float &by)
+{
+    by = 1.0f;
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[f][j] = ldexpf(x[f][j], e);
+}
+
+__device__ __forceinline__ void split_by(const float (&x)[8], float by, h8 &y1, h8 &y2)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        _Float16 hi, lo;
+        split(x[j] * by, hi, lo);
+        y1[j] = hi;
+        y2[j] = lo;
+    }
+}
+
+struct Factors {
+    int tile, row;                               // powers of two of the tile, and of this lane's row
+    bool wild;
+};
+
+__device__ __forceinline__ Factors factors(float top)
+{
+    const float most = wave_max(top), least = wave_max(top > 0.0f ? -top : -kBig);
+    Factors f;
+    f.tile = __builtin_amdgcn_readfirstlane(normaliser(most, 15));
+    f.wild = most > 0.0f && __builtin_amdgcn_readfirstlane(normaliser(-least, 15)) - f.tile > kWildBits;
+    f.row = f.wild ? normaliser(top, 15) : f.tile;
+    return f;
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArgs a, float c_man, int c_exp, int slots)
+{
+    constexpr int C = D / 4, kTileFloats = kTileKeys * D;        // pieces of a row
+    static_assert(2 * kTileFloats >= 32 * result_pitch(D), "the results fit the buffers");
+    __shared__ __attribute__((aligned(16))) float buf[kShare][2][kTileFloats];      // k and v; after the last tile: results
+    __shared__ __attribute__((aligned(16))) h8 queries[D / 8 * 64];
+    __shared__ RowSums sh;
+    __shared__ TileMeta metas[kShare];
+    const Block x = find_block(a, slots);
+    if (x.row0 < 0 || x.row0 >= x.len) return;
+    const int lane = threadIdx.x & 63, half = lane >> 5, last = x.last;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int pos = x.row0 + (lane & 31);
+    TileMeta *const meta = &metas[wave];
+    const float *const ks = a.k + (int64_t)x.r.begin * a.k_stride + x.kvh * D, *const vs = a.v + (int64_t)x.r.begin * a.v_stride + x.kvh * D;
+    // (keys past the end: the last one's values, whose weights are 0)
+    auto copy = [&](const float *p, int64_t stride, int tile, float *dst) {
+        const float *const end = p + (x.len - 1) * stride, *at = p + (int64_t)(tile * kTileKeys + lane / C) * stride;
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            const int piece = (lane % C ^ ((i * (64 / C) + lane / C) & (C - 1))) * 4;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((at < end ? at : end) + piece),
+                                             (__attribute__((address_space(3))) void *)(dst + i * 256), 16, 0, 0);
+            at += 64 / C * stride;
+        }
+    };
+    auto load = [&](int tile) {
+        copy(ks, a.k_stride, tile, buf[wave][0]);
+        copy(vs, a.v_stride, tile, buf[wave][1]);
+    };
+    // half of row lane % 32, 8 values in turns
+    auto read_row = [&](const float *src, float (&y)[D / 16][8]) {
+        const int row = lane & 31;
+#pragma unroll
+        for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f4 z = *reinterpret_cast<const f4 *>(src + row * D + ((4 * f + 2 * half + i) ^ (row & (C - 1))) * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[f][4 * i + j] = z[j];
+            }
+    };
+    // as prepare_kernel's fragment f: values 32 (f / 2) + lane % 32 of keys 16 (f % 2) + 8 (j / 4) + 4 half + j % 4
+    auto read_column = [&](const float *src, int f, float (&y)[8]) {
+        const int piece = ((lane & 31) >> 2) ^ (half << 2);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int u = 16 * (f & 1) + 8 * (j >> 2) + (j & 3);               // and 4 half
+            y[j] = src[(u + 4 * half) * D + (piece ^ (j & 3)) * 4 + (lane & 3) + ((8 * (f >> 1)) ^ (u & (C - 8))) * 4];
+        }
+    };
+    bool any_odd = false;
+    Rows<D> s;
+    h8 *const qs = queries + lane;
+    share_queries<D>(s, qs, sh, a.q + (int64_t)(x.r.begin + pos) * a.q_stride + x.head * D, pos < x.len, c_man, c_exp, lane, wave,
+                     [&]() { if (wave <= last) load(wave); });
+    __syncthreads();
+    for (int t = wave; t <= last; t += kShare) {
+        const bool edge = t == last;
+        const int first = t * kTileKeys - pos;
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): the tile has arrived
+        asm volatile("" ::: "memory");
+        float x8[D / 16][8];                     // k's rows, then v's
+        bool odd;
+        read_row(buf[wave][0], x8);
+        const Factors fk = factors(row_top<D>(x8, odd));
+        if (half == 0) meta->k_row[lane] = fk.row;
+        f16v y = {};
+        {
+            float by = ldexpf(1.0f, fk.row);
+            if (__any(fk.row > 127 || fk.row < -126)) scale_row(x8, fk.row, by);
+#pragma unroll
+            for (int f = 0; f < D / 16; ++f) {
+                h8 k1, k2;
+                split_by(x8[f], by, k1, k2);
+                const h8 q1 = qs[64 * f], q2 = qs[64 * (D / 16 + f)];
+                y = mfma(k2, q1, y);
+                y = mfma(k1, q2, y);
+                y = mfma(k1, q1, y);
+            }
+        }
+        read_row(buf[wave][1], x8);
+        const float top = row_top<D>(x8, odd);
+        odd = __any(odd);
+        any_odd |= odd;
+        const Factors fv = factors(top);
+        if (half == 0) meta->v_row[lane] = top > 0.0f ? -fv.row : kNoExp;
+        float by = ldexpf(1.0f, fv.tile);
+        if (odd || fv.wild || fv.tile > 127 || fv.tile < -126) {
+            // v is made what its operands are split of, in place
+#pragma unroll
+            for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f4 z;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float w = x8[f][4 * i + j];
+                        z[j] = fabsf(w) <= kBig ? ldexpf(w, fv.row) : 0.0f;
+                    }
+                    *reinterpret_cast<f4 *>(buf[wave][1] + (lane & 31) * D + ((4 * f + 2 * half + i) ^ (lane & (C - 1))) * 4) = z;
+                }
+            by = 1.0f;
+        }
+        asm volatile("" ::: "memory");
+        const TileHead now = {fk.tile, -fv.tile, (fk.wild ? kWildK : 0) | (fv.wild ? kWildV : 0)};
+        settle<D>(s, y, now, meta, edge, first, half);
+        weigh<D>(s, y);
+        if (now.flags & kWildV) weigh_rows<D>(s, y, meta, half);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            h8 p1, p2;
+            split8(y, h, p1, p2);
+#pragma unroll
+            for (int db = 0; db < D / 32; ++db) {
+                float z[8];
+                h8 v1, v2;
+                read_column(buf[wave][1], 2 * db + h, z);
+                split_by(z, by, v1, v2);
+                s.o[db] = mfma(v2, p1, s.o[db]);
+                s.o[db] = mfma(v1, p2, s.o[db]);
+                s.o[db] = mfma(v1, p1, s.o[db]);
+            }
+        }
+        if (t + kShare <= last) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): read, the buffers may be filled again
+            load(t + kShare);
+        }
+    }
+    if (any_odd)
+        for (int t = wave; t <= last; t += kShare)
+            odd_values<D>(s, t == last, t * kTileKeys - pos, vs + (int64_t)(t * kTileKeys) * a.v_stride, a.v_stride,
+                          x.len - t * kTileKeys, lane);
+    join_rows<D>(a, x, s, buf[0][0], sh, lane, wave);
 }
 
 inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
@@ -757,18 +1012,33 @@ inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((u
 // 4096 tokens (528) 143 / 170, 16 prompts of 256 (768) 32 / 32, 8 of 1024 (1152) 97 / 96.
 constexpr int64_t few_groups(int D) { return D == 128 ? 448 : 768; }
 
+// Prompts so short are not prepared: no wavefront has more than one tile of 128 values (two of
+// 64), and the workgroups, whose k and v fill a compute unit's LDS (half of it), run at
+// once. Measured (us on the device, without / with; from the host a call costs 9 / 14 at least): 16
+// heads of 128, 128 tokens (80 workgroups) 10.9 / 11.4, 192 (112) 15.9 / 13.1, 4 x 32 (128)
+// 10.6 / 11.4; 64 heads, 128 tokens (320) 11.5 / 11.7; 14 heads of 64, 128 tokens (70)
+// 7.4 / 8.6, 256 (126) 10.3 / 9.9; 16 heads of 128, 16 x 32 (512) 20 / 13.
+inline bool direct(int64_t T, int64_t B, int64_t heads, int64_t head_dim)
+{
+    return T * head_dim <= 16384 && tile_slots(T, B, 32) * heads * head_dim <= 40960;
+}
+
 template <int D>
 hipError_t launch(const PromptArgs &a, hipStream_t stream)
 {
     constexpr int W = 4;
+    int c_exp = 0;
+    const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
     const int64_t slots = tile_slots(a.T, a.B, kTileKeys);
+    if (direct(a.T, a.B, a.heads, D)) {
+        attend_direct_kernel<D><<<(unsigned)(slots * a.heads), 64 * kShare, 0, stream>>>(a, (float)(2.0 * c), c_exp - 1, (int)slots);
+        return hipGetLastError();
+    }
     TileMeta *metas = reinterpret_cast<TileMeta *>(a.ws);
     _Float16 *tiles = reinterpret_cast<_Float16 *>((char *)a.ws + meta_bytes(slots, a.kv_heads));
     prepare_kernel<D><<<dim3((unsigned)slots, (unsigned)a.kv_heads, 2), 256, 0, stream>>>(a, tiles, metas);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    int c_exp = 0;
-    const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
     const int64_t rows = tile_slots(a.T, a.B, 32 * W);
     if (rows * a.heads <= few_groups(D)) {
         const int64_t blocks = tile_slots(a.T, a.B, 32);
@@ -782,8 +1052,9 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
 
 }  // namespace
 
-uint64_t prompt_ws_bytes(int64_t T, int64_t B, int64_t, int64_t kv_heads, int64_t head_dim)
+uint64_t prompt_ws_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim)
 {
+    if (direct(T, B, heads, head_dim)) return 0;
     const int64_t slots = tile_slots(T, B, kTileKeys);
     return meta_bytes(slots, kv_heads) + (uint64_t)slots * kv_heads * tile_halves((int)head_dim) * 2;
 }
