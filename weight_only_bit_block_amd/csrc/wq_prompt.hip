@@ -29,10 +29,10 @@
 // precision never depends on values it does not see by more than the 2^14 of
 // one tile.
 //
-// Bound: the matrix cores in long prompts (8192 tokens, 16 heads of 128: 819 us,
-// 1006 TFLOP/s of binary16 products where a large library product reaches 1205), the
-// latency of both launches in short ones (128 tokens: 11.4 us), in between the L2's
-// k and v and the issue of matrix and vector instructions in turns (1024 tokens: 31 us).
+// Bound: the matrix cores in long prompts (8192 tokens, 16 heads of 128: 812 us,
+// 1014 TFLOP/s of binary16 products where a large library product reaches 1205), the
+// latency of a launch or two in short ones (128 tokens: 10.6 us), in between the L2's
+// k and v and the issue of matrix and vector instructions in turns (1024 tokens: 30 us).
 #include "wq_internal.h"
 #include "wq_device.h"
 #include "wq_seq.h"
