@@ -22,6 +22,7 @@ _WS_ALIGN = 256
 _F32, _I32, _I16, _U8 = torch.float32, torch.int32, torch.int16, torch.uint8
 _Tensor = torch.Tensor
 _CONTIGUOUS = torch.contiguous_format
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class KVCache(NamedTuple):
@@ -130,7 +131,7 @@ class _On:
 
 def _run(launch, at, stream):
     """launch(raw stream) with device `at` current and allocations from the stream."""
-    if stream is None and at == torch.cuda.current_device():
+    if stream is None and at == _current_device():
         return launch(_stream(None, at))
     with _On(at, stream):
         return launch(_stream(stream, at))

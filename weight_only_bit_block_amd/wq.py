@@ -126,9 +126,15 @@ def _check(status: int, where: str) -> None:
 
 
 # ------------------------------------------------------------------ helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 _raw_stream = None
@@ -139,12 +145,11 @@ def _stream(stream=None, device=None) -> int:
     global _raw_stream
     if stream is not None:
         return int(stream.cuda_stream)
-    torch = _torch()
     if _raw_stream is None:
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
+        _raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream", False)
     if _raw_stream and device is not None:
-        return int(_raw_stream(device))
-    return int(torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(device)
+    return int(_torch().cuda.current_stream().cuda_stream)
 
 
 def _ptr(t) -> int:
@@ -251,20 +256,24 @@ def embed(ids, q, scales, K: int, bits: int, out=None, stream=None):
     (q, scales) in fp32; ids outside [0, N) give rows of NaN."""
     torch = _torch()
     for t, dt, name in ((ids, torch.int32, "ids"), (q, torch.uint8, "q"), (scales, torch.int16, "scales")):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dt and t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dt and t.is_contiguous()):
             _dev_tensor(t, dt, name)                # raises with the reason
-    _need(ids.dim() == 1, "ids must be 1-D")
-    N = q.shape[0]
-    _need(q.shape[1] == q_row_bytes(K, bits), "q has the wrong row length for K and bits")
-    _need(tuple(scales.shape) == (N, K // BLOCK), "scales must be [N, K/32]")
-    n = ids.shape[0]
+    if ids.dim() != 1:
+        raise ValueError("ids must be 1-D")
+    n, N, row = ids.shape[0], q.shape[0], q.shape[1]
+    if row != q_row_bytes(K, bits):
+        raise ValueError("q has the wrong row length for K and bits")
+    if scales.shape != (N, K // BLOCK):
+        raise ValueError("scales must be [N, K/32]")
     if out is None:
         out = torch.empty((n, K), dtype=torch.float32, device=ids.device)
     else:
         _dev_tensor(out, torch.float32, "out")
         _need(tuple(out.shape) == (n, K), "out must be [len(ids), K]")
-    _check(load().wq_embed(_ptr(ids), n, K, N, bits, _ptr(q), _ptr(scales), _ptr(out),
-                           _stream(stream, ids.get_device())), "wq_embed")
+    st = load().wq_embed(ids.data_ptr(), n, K, N, bits, q.data_ptr(), scales.data_ptr(), out.data_ptr(),
+                         _stream(stream, ids.get_device()))
+    if st:
+        raise WqError(st, "wq_embed")
     return out
 
 
