@@ -158,12 +158,15 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
 //
 // Lengths are device data, so the split is made on the device: the sequences'
 // steps of 256 tokens (4 tiles, one per wavefront) are laid end to end and every
-// workgroup takes an equal run of them, whatever sequences it meets. A sequence
+// workgroup takes an equal run of them, whatever sequences it meets. Going from
+// one sequence to the next costs a workgroup as much as 3 steps (its length, its pages and
+// the first tile one after another, the join before: 6 us), so so many stand between
+// sequences (64 of 262139 in all, 4 heads each: 85 us without, 74 with). A sequence
 // that lies in one run is finished there; the pieces of others go to a workspace
 // and a second kernel joins them in order.
 //
 // 8 heads of 128: one sequence of 131072, 2 query heads each, 31 us (4.9 TB/s), joining
-// them 5.9; 64 sequences of 262139 in all, 4 query heads each, 74 us (4.1 TB/s, bound by the
+// them 5.9; 64 sequences of 262139 in all, 4 query heads each, 63 us (4.8 TB/s, bound by the
 // vector instructions that make weights of scores and numbers of codes), joining 4.8.
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
@@ -229,6 +232,7 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
 constexpr int kFill = 512;
 constexpr int kCutMaxSeqs = 512;
 constexpr int kShortPages = 16;
+constexpr int kChangeSteps = 3;              // 2 and 4 measure the same
 
 __host__ __device__ inline int head_groups(int heads, int kv_heads) { return (heads / kv_heads + kMaxGroup - 1) / kMaxGroup; }
 __host__ __device__ inline bool cut_sequences(int64_t B, int per_step, int64_t max_pages)
@@ -250,7 +254,8 @@ __device__ __forceinline__ int steps_of(const DecodeArgs &a, int b)
     return len < 0 || len > a.max_pages * kTile ? 0 : (int)((len + kDecodeStep - 1) / kDecodeStep);
 }
 
-// A run of steps: sequence b from its step `skip` on, `left` steps in all.
+// A run: sequence b from its step `skip` on, `left` steps in all, those that stand
+// for the changes between sequences among them.
 struct Run {
     int b, skip, left;
     int span;                                // of a run
@@ -260,17 +265,22 @@ struct Run {
 __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
 {
     const int lane = threadIdx.x & 63;
+    const auto cost = [&](int b) {
+        const int n = b < a.B ? steps_of(a, b) : 0;
+        return n > 0 ? n + kChangeSteps : 0;
+    };
     int64_t total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
-        int n = b0 + lane < a.B ? steps_of(a, b0 + lane) : 0;
+        int n = cost(b0 + lane);
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
         total += n;
     }
-    const int64_t span = (total + runs - 1) / runs, from = run * span;
+    // (no change before the first sequence)
+    const int64_t span = (total - kChangeSteps + runs - 1) / runs, from = kChangeSteps + run * span;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.B && from < total; b0 += 64) {
-        const int n = b0 + lane < a.B ? steps_of(a, b0 + lane) : 0;
+        const int n = cost(b0 + lane);
         int upto = n;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -281,9 +291,9 @@ __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
         const uint64_t who = __ballot(from >= first && from < first + n);
         if (who) {
             const int l = __ffsll((unsigned long long)who) - 1;
-            const int skip = __shfl((int)(from - first), l);
-            return {__builtin_amdgcn_readfirstlane(b0 + l), __builtin_amdgcn_readfirstlane(skip),
-                    __builtin_amdgcn_readfirstlane((int)(total - from < span ? total - from : span)),
+            const int at = __builtin_amdgcn_readfirstlane(__shfl((int)(from - first), l)) - kChangeSteps;      // < 0: in the change
+            const int left = __builtin_amdgcn_readfirstlane((int)(total - from < span ? total - from : span));
+            return {__builtin_amdgcn_readfirstlane(b0 + l), at < 0 ? 0 : at, at < 0 ? left + at : left,
                     __builtin_amdgcn_readfirstlane((int)span)};
         }
         before += __shfl(upto, 63);
@@ -327,20 +337,34 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
             a.out[(int64_t)run * a.out_stride + head0 * D + i] = a.lens[run] == 0 ? 0.0f : __builtin_nanf("");
         return;
     }
+    // (constant address space: scalar loads, which wait for nothing else)
+    typedef __attribute__((address_space(4))) int32_t const_i32;
+    const const_i32 *lens = (const const_i32 *)(uintptr_t)a.lens;
     int done = 0;                                                // steps of the run that are finished
 next_sequence:
     // (one value for the whole wavefront: said so, for the compiler's loops and descriptors)
     const int b = __builtin_amdgcn_readfirstlane(at.b);
-    const int64_t len = __builtin_amdgcn_readfirstlane(a.lens[b]);
+    const int c = lane & 15, g = lane >> 4;
+    // the query, asked for before anything that waits: row n = c of the operand is part c / 8 of head
+    // (c / 4 % 2) HL + c % 4 / BC, and of blocks r BC + c % BC
+    const int part = c >> 3, bc = c & (BC - 1);
+    float x[R][8];
+    {
+        const int h = ((c >> 2) & 1) * HL + (c & 3) / BC;
+        const bool live = h < heads;
+        const float *src = a.q + (int64_t)b * a.q_stride + (head0 + (live ? h : 0)) * D;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[r][e] = live ? src[32 * (r * BC + bc) + 8 * g + nibble_of(e)] : 0.0f;
+    }
+    const int64_t len = __builtin_amdgcn_readfirstlane(lens[b]);
     const int all = (int)((len + kDecodeStep - 1) / kDecodeStep);      // steps of the sequence
     const int mine = __builtin_amdgcn_readfirstlane(all - at.skip < at.left - done ? all - at.skip : at.left - done);
     const bool whole = mine == all;
     const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane(at.skip) * kDecodeStep, end = len < t0 + (int64_t)mine * kDecodeStep ? len : t0 + (int64_t)mine * kDecodeStep;
     const int tile0 = (int)(t0 / kTile) + wave, tile_end = (int)((end + kTile - 1) / kTile);
-    // (constant address space: scalar loads, which wait for nothing else)
-    const __attribute__((address_space(4))) int32_t *pages =
-        (const __attribute__((address_space(4))) int32_t *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
-    const int c = lane & 15, g = lane >> 4;
+    const const_i32 *pages = (const const_i32 *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
 
     // copies of a tile: 16-byte pieces (a block of a token each), swizzled by token so that the reads below
     // take 64 banks
@@ -383,20 +407,14 @@ next_sequence:
         }
     }
 
-    // the query: row n = c of the operand is part c / 8 of head (c / 4 % 2) HL + c % 4 / BC, and of blocks
-    // r BC + c % BC
     h8 q[NB];
     float f[HL];                                                 // scores in powers of two = sums times this
     {
-        const int part = c >> 3, bc = c & (BC - 1), h = ((c >> 2) & 1) * HL + (c & 3) / BC;
-        const bool live = h < heads;
-        const float *src = a.q + (int64_t)b * a.q_stride + (head0 + (live ? h : 0)) * D;
-        float x[R][8], top = 0.0f;
+        float top = 0.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[r][e] = live ? src[32 * (r * BC + bc) + 8 * g + nibble_of(e)] : 0.0f;
                 const float y = fabsf(x[r][e]);
                 if (y <= 3.4028235e38f) top = fmaxf(top, y);
             }
@@ -619,12 +637,12 @@ next_sequence:
         Pieces *p = (Pieces *)a.ws + b;
         *p = Pieces{run, 1 + (rest + at.span - 1) / at.span, done != 0, 0};
     }
-    done += mine;
+    done += mine + kChangeSteps;
     if (done >= at.left) return;
     do {
         ++at.b;
         if (at.b >= a.B) return;                                 // (not reached: `left` steps are there)
-    } while (a.lens[at.b] <= 0 || a.lens[at.b] > cap);
+    } while (lens[at.b] <= 0 || lens[at.b] > cap);
     at.skip = 0;
     __syncthreads();                                             // the results have been read
     goto next_sequence;
