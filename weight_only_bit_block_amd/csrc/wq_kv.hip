@@ -269,8 +269,17 @@ __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
         const int n = b < a.B ? steps_of(a, b) : 0;
         return n > 0 ? n + kChangeSteps : 0;
     };
-    int64_t total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const auto scan = [&](int n) {           // sum of the lanes up to this one
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(n, o);
+            if (lane >= o) n += x;
+        }
+        return n;
+    };
+    const int head = cost(lane), head_upto = scan(head);         // the first 64 sequences, often all
+    int64_t total = __shfl(head_upto, 63);
+    for (int b0 = 64; b0 < a.B; b0 += 64) {
         int n = cost(b0 + lane);
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
@@ -280,13 +289,7 @@ __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
     const int64_t span = (total - kChangeSteps + runs - 1) / runs, from = kChangeSteps + run * span;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.B && from < total; b0 += 64) {
-        const int n = cost(b0 + lane);
-        int upto = n;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int x = __shfl_up(upto, o);
-            if (lane >= o) upto += x;
-        }
+        const int n = b0 ? cost(b0 + lane) : head, upto = b0 ? scan(n) : head_upto;
         const int64_t first = before + upto - n;
         const uint64_t who = __ballot(from >= first && from < first + n);
         if (who) {
@@ -358,13 +361,18 @@ next_sequence:
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[r][e] = live ? src[32 * (r * BC + bc) + 8 * g + nibble_of(e)] : 0.0f;
     }
+    // its length and its first two pages at once (a page number that is not needed may be any of the row's)
+    const const_i32 *pages = (const const_i32 *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
+    const int tile0 = __builtin_amdgcn_readfirstlane(at.skip) * kDecodeWaves + wave, tile1 = tile0 + kDecodeWaves;
+    const int last_page = (int)a.max_pages - 1;
+    const int page1 = pages[tile0 < last_page ? tile0 : last_page];
+    int page2 = pages[tile1 < last_page ? tile1 : last_page];    // page of the tile after the next
     const int64_t len = __builtin_amdgcn_readfirstlane(lens[b]);
     const int all = (int)((len + kDecodeStep - 1) / kDecodeStep);      // steps of the sequence
     const int mine = __builtin_amdgcn_readfirstlane(all - at.skip < at.left - done ? all - at.skip : at.left - done);
     const bool whole = mine == all;
     const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane(at.skip) * kDecodeStep, end = len < t0 + (int64_t)mine * kDecodeStep ? len : t0 + (int64_t)mine * kDecodeStep;
-    const int tile0 = (int)(t0 / kTile) + wave, tile_end = (int)((end + kTile - 1) / kTile);
-    const const_i32 *pages = (const const_i32 *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
+    const int tile_end = (int)((end + kTile - 1) / kTile);
 
     // copies of a tile: 16-byte pieces (a block of a token each), swizzled by token so that the reads below
     // take 64 banks
@@ -397,10 +405,8 @@ next_sequence:
     };
     uint8_t *kbuf = lds[wave], *vbuf = kbuf + kHalf, *pbuf = vbuf + kHalf;
     const bool any_page = a.cache.n_pages > 0;
-    int page2 = 0;                                               // page of the tile after the next
     if (tile0 < tile_end) {
-        const int64_t row = row_of(pages[tile0]);
-        if (tile0 + kDecodeWaves < tile_end) page2 = pages[tile0 + kDecodeWaves];
+        const int64_t row = row_of(page1);
         if (any_page) {
             copy(a.cache.kq, a.cache.ks, row, kbuf, false);
             copy(a.cache.vq, a.cache.vs, row, vbuf, true);
