@@ -17,7 +17,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 // floats, the maximum of a block goes over its 8 lanes by cross-lane moves.
 // Every thread takes kAppendRows rows, keys and values, and asks for all of
 // them before it looks up where they go (three dependent reads). 4096 tokens, 8
-// heads of 128: 10.6 us, 3.6 TB/s (rows read with cached loads: 11.1).
+// heads of 128: 10.3 us, 3.7 TB/s (rows read with cached loads: 10.9); 16384: 33.0, 4.6.
 //
 // The quotients of wq_pack's rule are correctly rounded; here they cost three
 // operations each instead of a division's ten: q0 = x r, q = q0 + r (x - q0 s)
@@ -57,21 +57,24 @@ __device__ __forceinline__ void quantize4(f4 x, uint16_t &codes, uint16_t &scale
     const _Float16 s16 = (_Float16)quotient(amax, 7.0f, 1.0f / 7.0f);
     const float sf = (float)s16, r = 1.0f / sf;
     scale = __builtin_bit_cast(uint16_t, s16);
-    uint32_t c = 0;
-    if (!(amax <= 3.4028235e38f) || !(sf <= 65504.0f)) {
-        scale = 0x7E00;
-    } else if (sf != 0.0f) {
+    // rounded by adding 1.5 2^23, which leaves the code in the lowest bits
+    uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float q = fminf(fmaxf(rintf(quotient(x[j], sf, r)), -8.0f), 7.0f);
-            c |= ((uint32_t)(int)q & 0xFu) << (4 * j);
-        }
+    for (int j = 0; j < 4; ++j) {
+        const float q = __builtin_amdgcn_fmed3f(quotient(x[j], sf, r), -8.0f, 7.0f) + 12582912.0f;
+        c[j] = __builtin_bit_cast(uint32_t, q);
     }
-    codes = (uint16_t)c;
+    const uint32_t lo = (c[0] & 0xFu) | (c[1] << 4 & ~0xFu), hi = (c[2] & 0xFu) | (c[3] << 4 & ~0xFu);
+    const bool bad = !(amax <= 3.4028235e38f) || !(sf <= 65504.0f);
+    codes = bad || sf == 0.0f ? 0 : (uint16_t)((lo & 0xFFu) | (hi << 8 & ~0xFFu));
+    if (bad) scale = 0x7E00;
 }
 
+// by_heads, shift: a row number below 2^27 divided by the heads is the upper half of its
+// product with by_heads = ceil(2^(32 + shift) / heads), shifted (heads <= 2^(shift + 1) keeps by_heads
+// within 32 bits and what it is too large by below 2^(shift + 5)).
 template <int D>
-__global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t by_heads, int shift)
 {
     constexpr int kLanes = D / 4, kRows = 256 / kLanes;  // lanes of a row, rows of a workgroup at a time
     const uint32_t H = a.cache.kv_heads, rows = (uint32_t)(a.T * H);
@@ -80,7 +83,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
     int64_t dst[kAppendRows];                            // cache row
 #pragma unroll
     for (int i = 0; i < kAppendRows; ++i) {
-        const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = row / H, h = row % H;
+        const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = by_heads ? __umulhi(row, by_heads) >> shift : row, h = row - t * H;
         k[i] = v[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         if (row < rows) {
             k[i] = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(a.k + t * a.k_stride + h * D + c * 4));
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a)
     }
 #pragma unroll
     for (int i = 0; i < kAppendRows; ++i) {
-        const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = row / H, h = row % H;
+        const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = by_heads ? __umulhi(row, by_heads) >> shift : row, h = row - t * H;
         dst[i] = -1;
         if (row < rows) {
             const int b = seq_of_token(a.cu, a.B, (int)t);
@@ -737,8 +740,13 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream)
 {
     const int64_t rows = a.T * a.cache.kv_heads, each = kAppendRows * 256 / (a.cache.head_dim / 4);
     const unsigned grid = (unsigned)((rows + each - 1) / each);
-    if (a.cache.head_dim == 128) append_kernel<128><<<grid, 256, 0, stream>>>(a);
-    else append_kernel<64><<<grid, 256, 0, stream>>>(a);
+    int shift = 0;
+    while ((2 << shift) < a.cache.kv_heads) ++shift;
+    const uint64_t H = a.cache.kv_heads, by = (((uint64_t)1 << (32 + shift)) + H - 1) / H;
+    // one head: 2^32 does not fit, the quotient is the row
+    const uint32_t by_heads = H == 1 ? 0 : (uint32_t)by;
+    if (a.cache.head_dim == 128) append_kernel<128><<<grid, 256, 0, stream>>>(a, by_heads, shift);
+    else append_kernel<64><<<grid, 256, 0, stream>>>(a, by_heads, shift);
     return hipGetLastError();
 }
 
