@@ -339,16 +339,18 @@ def test_decode_long(lens):
     check_decode(out, q, host, table, lens, 0.3)
 
 
-def test_decode_many_sequences():
-    """More sequences than are looked at for a cut, some empty, some past a step."""
-    note("decode many")
+@pytest.mark.parametrize("count,longest", [(600, 1300), (600, 2500), (2100, 2500)])
+def test_decode_many_sequences(count, longest):
+    """More sequences than a workgroup looks at together, some empty, some past a
+    step: not cut for short tables, cut, and too many to be cut."""
+    note(f"decode many {count} {longest}")
     torch = torch_cuda()
     rng = rng_for(27)
-    lens = [int(n) for n in rng.integers(0, 80, 600)]
-    lens[7], lens[599] = 1300, 600
+    lens = [int(n) for n in rng.integers(0, 80, count)]
+    lens[7], lens[-1] = longest, 600
     table, pages = table_for(rng, lens)
     host, cache = cache_arrays(rng, pages, 1, 64)
-    q = rng.standard_normal((600, 2, 64)).astype(np.float32)
+    q = rng.standard_normal((count, 2, 64)).astype(np.float32)
     out = torch.full(q.shape, NAN, device="cuda")
     wqa.attn_decode(dev(q), cache, dev(table), dev(np.array(lens, np.int32)), out=out)
     check_decode(out, q, host, table, lens, 0.125)

@@ -226,14 +226,15 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
 // ---- how the work is cut
 // kFill workgroups in all, 2 on each of 256 compute units; for every kv head and
 // group of query heads equally many. Finding its place makes every workgroup look
-// at all lengths, and the pieces cost a second kernel, so many sequences (they
-// fill the card by themselves) are not cut, one workgroup each, and neither are
-// short ones: tables of up to 16 pages, or 32 where there are kFill / 2
-// workgroups without (us, uncut / cut, 8 kv heads of 128, 2 query heads each:
-// 1 x 500 tokens 8.1 / 10.8, 1 x 1000 10.9 / 10.9, 1 x 2040 17.0 / 11.1, 16 x 1500
-// 15.7 / 16.9, 32 x 777 12.7 / 17.6, 32 x 2040 20.4 / 23.7).
+// at all lengths, and the pieces cost a second kernel, so thousands of sequences
+// are not cut, one workgroup each, and neither are short ones: tables of up to 16 pages, or 32
+// where there are kFill / 2 workgroups without (us, uncut / cut, 8 kv heads of 128, 2 query
+// heads each: 1 x 500 tokens 8.1 / 10.8, 1 x 1000 10.9 / 10.9, 1 x 2040 17.0 / 11.1, 16 x 1500
+// 15.7 / 16.9, 32 x 777 12.7 / 17.6, 32 x 2040 20.4 / 23.7; 520 x 300 and one of 65536
+// 365 / 107, 1024 x 2560 497 / 526, 2048 ragged of 500 in the mean 359 / 350, 4096 of 300
+// 527 / 555).
 constexpr int kFill = 512;
-constexpr int kCutMaxSeqs = 512;
+constexpr int kCutMaxSeqs = 2048;
 constexpr int kShortPages = 16;
 constexpr int kChangeSteps = 3;              // 2 and 4 measure the same
 
