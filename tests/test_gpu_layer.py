@@ -10,7 +10,7 @@ from tests.gpu_util import note, torch_cuda
 pytestmark = pytest.mark.gpu
 
 LAYOUTS = [(16, 8, 128), (4, 4, 64), (14, 2, 64), (12, 1, 128)]
-WIDE = [(120, 2, 128), (260, 2, 64)]       # so many heads that short prompts fill the card: the other prompt kernel
+WIDE = [(160, 2, 128), (420, 2, 64)]       # so many heads that short prompts fill the card: the other prompt kernel
 NAN = float("nan")
 
 
@@ -70,7 +70,7 @@ def test_prompt_parity(heads, kv, d, lens):
     check_prompt(out, host, lens, d ** -0.5, what=str(lens))
 
 
-@pytest.mark.parametrize("T,heads", [(1, 16), (5, 16), (100, 16), (1023, 4), (2049, 4), (700, 60), (700, 80)])
+@pytest.mark.parametrize("T,heads", [(1, 16), (5, 16), (100, 16), (1023, 4), (2049, 4), (700, 60), (700, 100)])
 def test_prompt_single(T, heads):
     note(f"prompt single {T} {heads}")
     torch = torch_cuda()
@@ -102,7 +102,7 @@ def test_prompt_strides():
     assert torch.isnan(wide[:, :16]).all() and torch.isnan(wide[:, 16 + 6 * 64:]).all()
 
 
-@pytest.mark.parametrize("heads", [4, 120, 2])
+@pytest.mark.parametrize("heads", [4, 160, 2])
 @pytest.mark.parametrize("what", ["outlier_keys", "peaked", "tiny", "huge", "value_spread", "key_spread", "equal", "one_channel"])
 def test_prompt_range(what, heads):
     """Magnitudes the normalisation has to carry: single rows far above the
@@ -146,7 +146,7 @@ def test_prompt_range(what, heads):
     check_prompt(out, host, lens, scale, what=what)
 
 
-@pytest.mark.parametrize("heads", [4, 160])
+@pytest.mark.parametrize("heads", [4, 160, 420])
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf"), NAN])
 @pytest.mark.parametrize("at", [0, 31, 70, 150])
 def test_prompt_non_finite_stays_with_the_rows_that_see_it(bad, at, heads):

@@ -1005,12 +1005,15 @@ inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((uint64_t)slots * kv_heads * sizeof(TileMeta)); }
 
 // Up to so many workgroups of 128 rows, prompts run on the kernel whose wavefronts
-// share 32 rows. Measured, both kernels (us, shared / other): 16 heads of 128,
-// one prompt of 1024 (144 groups) 32 / 64, 2048 (272) 85 / 117, 3000 (384)
-// 154 / 173, 4096 (528) 264 / 266; 8 prompts of 256 (384) 33 / 36, 6 of 512 (480)
-// 54 / 52; 64 heads, 700 tokens (384) 50 / 51, 1024 (576) 85 / 78; 16 heads of 64,
-// 4096 tokens (528) 143 / 170, 16 prompts of 256 (768) 32 / 32, 8 of 1024 (1152) 97 / 96.
-constexpr int64_t few_groups(int D) { return D == 128 ? 448 : 768; }
+// share 32 rows; of several prompts, whose lengths will differ, more, since a long one's
+// last rows would be walked by few wavefronts. Measured, both kernels (us, shared / other): 16
+// heads of 128, one prompt of 1024 (144 groups) 32 / 64, 2048 (272) 85 / 117, 3000 (384)
+// 154 / 173, 4096 (528) 264 / 266; 64 heads, 1024 tokens (576) 85 / 78; 8 prompts of 256 (384)
+// 33 / 36, 12 (576) 44 / 43; of different lengths, 4 of 4094 in all (560) 139 / 156, 13 of
+// 4997 (832) 102 / 105, 24 of 4085 (880) 68 / 80, 24 of 7990 (1376) 134 / 125; 12 heads, 8 of
+// 3998 (468) 70 / 101. Heads of 64: one prompt of 4096 (528) 141 / 170, 8 of 1024 (1152) 97 / 96, 16
+// of 7991 (1248) 85 / 106, 24 of 7989 (1204) 64 / 67, 8 of 15995 (2112) 1012 / 932.
+inline int64_t few_groups(int D, int64_t B) { return D == 64 ? 1200 : B >= 4 ? 880 : 528; }
 
 // Prompts so short are not prepared: no wavefront has more than one tile of 128 values (two of
 // 64), and the workgroups, whose k and v fill a compute unit's LDS (half of it), run at
@@ -1040,7 +1043,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t rows = tile_slots(a.T, a.B, 32 * W);
-    if (rows * a.heads <= few_groups(D)) {
+    if (rows * a.heads <= few_groups(D, a.B)) {
         const int64_t blocks = tile_slots(a.T, a.B, 32);
         attend_shared_kernel<D><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c),
                                                                                           c_exp - 1, (int)blocks);
