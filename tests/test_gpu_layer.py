@@ -248,6 +248,33 @@ def test_append_is_bit_exact(kv, d, lens, starts):
         assert np.array_equal(t.cpu().numpy(), exp), j
 
 
+def test_append_ties():
+    """Blocks whose scale lies exactly midway between two binary16 numbers, and
+    values midway between two codes, or a step of fp32 off: the fp32 quotients
+    decide."""
+    note("append ties")
+    torch_cuda()
+    rng = rng_for(30)
+    half = np.arange(0x0400, 0x7000, 5, dtype=np.uint16)
+    low, high = half.view(np.float16).astype(np.float32), (half + 1).astype(np.uint16).view(np.float16).astype(np.float32)
+    amax = np.float32(7) * ((low + high) / np.float32(2))                         # exact: 15 bits
+    assert ((amax / np.float32(7)).astype(np.float64) * 7 == amax).all()
+    s = (amax / np.float32(7)).astype(np.float16).astype(np.float32)[:, None]
+    x = (rng.integers(-6, 6, (len(amax), 32)) + 0.5).astype(np.float32) * s      # exact: the middle of two codes
+    x = np.nextafter(x, x * rng.integers(0, 3, x.shape).astype(np.float32))       # a step down, none, a step up
+    x = np.clip(x, -amax[:, None], amax[:, None])
+    x[:, 0] = amax
+    T = len(amax) // 4
+    x = x[:T * 4].reshape(T, 1, 128)
+    pages = -(-T // ref.PAGE)
+    cache = wqa.KVCache.empty(pages, 1, 128)
+    wqa.kv_append(cache, dev(x), dev(-x), dev(np.arange(pages, dtype=np.int32)[None]))
+    for y, codes, scales in ((x, cache.kq, cache.ks), (-x, cache.vq, cache.vs)):
+        c, sc = ref.quantize(y[:, 0])
+        assert np.array_equal(scales.cpu().numpy().reshape(-1, 4)[:T], sc.view(np.int16))
+        assert np.array_equal(codes.cpu().numpy().reshape(-1, 64)[:T], ref.nibbles(c))
+
+
 def test_append_values_and_bad_blocks():
     """Ties, zeros, tiny and huge blocks as the packing rule has them; blocks
     that are not finite read back as NaN and change no other block."""

@@ -54,7 +54,9 @@ __device__ __forceinline__ void quantize4(f4 x, uint16_t &codes, uint16_t &scale
     top = max_dpp<0x4E>(top);                            // quad_perm 2 3 0 1
     top = max_dpp<0x141>(top);                           // row_half_mirror: the other quad of 8
     const float amax = __builtin_bit_cast(float, top);
-    const _Float16 s16 = (_Float16)quotient(amax, 7.0f, 1.0f / 7.0f);
+    float s32 = quotient(amax, 7.0f, 1.0f / 7.0f);
+    asm("" : "+v"(s32));                                 // rounded to fp32 first, not at once to binary16
+    const _Float16 s16 = (_Float16)s32;
     const float sf = (float)s16, r = 1.0f / sf;
     scale = __builtin_bit_cast(uint16_t, s16);
     // rounded by adding 1.5 2^23, which leaves the code in the lowest bits
