@@ -65,14 +65,15 @@ class KVCache(NamedTuple):
             raise ValueError("cache.kq must be a 4-D device tensor")
         shape = kq.shape
         n, h, page, half = shape
-        _need(page == KV_PAGE, "cache pages hold 64 tokens")
+        if page != KV_PAGE:
+            raise ValueError("cache pages hold 64 tokens")
         scales = (n, h, page, half // 16)
         if not (kq.dtype is _U8 and vq.dtype is _U8 and ks.dtype is _I16 and vs.dtype is _I16 and vq.shape == shape
                 and ks.shape == scales and vs.shape == scales):
             raise ValueError(f"the cache must be uint8 codes {list(shape)} and int16 scales {list(scales)}")
-        for t in self:
-            if not (t.get_device() == at and t.is_contiguous()):
-                raise ValueError(f"the cache's arrays must be contiguous and on device {at}")
+        if not (kq.get_device() == at and ks.get_device() == at and vq.get_device() == at and vs.get_device() == at
+                and kq.is_contiguous() and ks.is_contiguous() and vq.is_contiguous() and vs.is_contiguous()):
+            raise ValueError(f"the cache's arrays must be contiguous and on device {at}")
         return WqKVCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), n, h, 2 * half)
 
 
@@ -85,6 +86,8 @@ def _heads(t, name, at=None):
     if at is not None and t.get_device() != at:
         raise ValueError(f"{name} must be on device {at}")
     n, h, d = t.shape
+    if t.is_contiguous() and d % 4 == 0:
+        return n, h, d, h * d
     row, head, value = t.stride()
     if (value != 1 and d > 1) or (head != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -102,12 +105,15 @@ def _cu(cu, at):
     """Address and number of sequences of cu."""
     if cu is None:
         return None, 1
-    _need(isinstance(cu, _Tensor) and cu.dim() == 1 and cu.shape[0] >= 1, "cu must be [sequences + 1]")
-    return _index(cu, cu.shape, "cu", at), cu.shape[0] - 1
+    if not (isinstance(cu, _Tensor) and cu.dim() == 1 and cu.shape[0] >= 1):
+        raise ValueError("cu must be [sequences + 1]")
+    shape = cu.shape
+    return _index(cu, shape, "cu", at), shape[0] - 1
 
 
 def _table(table, B, at):
-    _need(isinstance(table, _Tensor) and table.dim() == 2, "table must be [sequences, max_pages]")
+    if not (isinstance(table, _Tensor) and table.dim() == 2):
+        raise ValueError("table must be [sequences, max_pages]")
     W = table.shape[1]
     return _index(table, (B, W), "table", at), W
 
