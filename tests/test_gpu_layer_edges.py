@@ -1,0 +1,52 @@
+"""Operators between the projections on data that strains what the kernels keep
+beside the values: the units of a tile, the power of two of the scores, the
+largest value scale. Against the plain 64-bit forms of tests/layer_ref.py, within
+the bounds derived there."""
+import numpy as np
+import pytest
+
+import weight_only_bit_block_amd as wqa
+from tests import layer_ref as ref
+from tests.gpu_util import note, torch_cuda
+from tests.test_gpu_layer import NAN, cache_arrays, cache_on, check_decode, cu_of, dev, qkv, rng_for, table_for
+
+pytestmark = pytest.mark.gpu
+
+# heads, kv heads, head size, tokens of one prompt, for each prompt kernel: it splits k and v itself (one and two
+# tiles a wavefront), wavefronts share 32 rows, wavefronts of 32 rows each
+KERNELS = [(16, 8, 128, 128), (14, 2, 64, 256), (4, 2, 128, 530), (4, 2, 64, 530), (288, 2, 128, 200), (602, 2, 64, 200)]
+
+
+def prompt_of(host, cu=None, scale=None):
+    torch = torch_cuda()
+    out = torch.full(host[0].shape, NAN, device="cuda")
+    wqa.attn_prefill(*(dev(x) for x in host), cu=cu, scale=scale, out=out)
+    return out.cpu().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------------ tiles of zeros
+@pytest.mark.parametrize("heads,kv,d,T", KERNELS)
+@pytest.mark.parametrize("where", ["first", "middle", "last", "first_two", "all", "not_finite"])
+def test_prompt_tile_of_zero_values(heads, kv, d, T, where):
+    """32 keys whose values are all zero (padding, silence) have no largest value
+    and must not set the units of the others; neither must 32 keys none of whose
+    values is finite. Values of any size around them: the output is
+    proportional, exactly so for powers of two."""
+    note(f"prompt zero tile {heads} {kv} {d} {T} {where}")
+    host, _ = qkv(rng_for(50, heads, d), T, heads, kv, d)
+    last = (T - 1) // 32
+    tiles = {"first": [0], "middle": [3], "last": [last], "first_two": [0, 1], "all": range(last + 1), "not_finite": [2]}[where]
+    for t in tiles:
+        host[2][32 * t:32 * t + 32] = 0
+    want, sums = ref.prompt(*host, [T], d ** -0.5)
+    lim = ref.bound(sums, T, d)
+    for size in (2.0 ** 60, 1.0, 2.0 ** -10, 2.0 ** -20, 2.0 ** -30, 2.0 ** -100):
+        v = host[2] * np.float32(size)
+        seen = np.ones(want.shape, bool)
+        if where == "not_finite":
+            v[64:96] = np.inf
+            seen[64:] = False
+        got = prompt_of([host[0], host[1], v])
+        err, most = np.abs(got - want * size), (lim - 1e-44) * size + 1e-44
+        assert (err[seen] <= most[seen]).all(), f"values {size}: worst error / bound {np.nanmax((err / most)[seen]):.3g}"
+        assert np.isnan(got[~seen]).all()

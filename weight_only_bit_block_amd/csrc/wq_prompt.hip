@@ -25,9 +25,9 @@
 // smaller than the largest; a "wild" tile (rows further apart) takes a factor
 // per row: on the scores for k, on the weights for v. Sums, maxima and weights
 // are fp32. The output of a query is kept in units of the largest tile (wild:
-// visible row) of v seen so far; tiles are walked first to last, so that its
-// precision never depends on values it does not see by more than the 2^14 of
-// one tile.
+// visible row) of v seen so far, which values of zero leave alone; tiles are
+// walked first to last, so that its precision never depends on values it does
+// not see by more than the 2^14 of one tile.
 //
 // Bound: the matrix cores in long prompts (8192 tokens, 16 heads of 128: 812 us,
 // 1014 TFLOP/s of binary16 products where a large library product reaches 1205), the
@@ -56,7 +56,7 @@ constexpr float kSlack = 3.0f;       // log2 a score may pass the running maximu
 // What the attention kernel needs to know of a tile.
 struct TileMeta {
     int k_exp, k_flags;              // k was multiplied by 2^k_exp (wild: by 2^k_row[u] row by row)
-    int v_exp, v_flags;              // v is its operands times 2^v_exp (wild: 2^v_row[u])
+    int v_exp, v_flags;              // v is its operands times 2^v_exp (wild: 2^v_row[u]; kNoExp: all are zero)
     int k_row[kTileKeys];
     int v_row[kTileKeys];
 };
@@ -72,7 +72,7 @@ __device__ __forceinline__ TileHead head_of(const TileMeta *m)
     return {x.x, x.z, x.y | x.w};
 }
 enum { kWildK = 1, kWildV = 2, kOddV = 4 };      // kOddV: v holds values that are not finite (0 in the operands)
-constexpr int kNoExp = -100000;      // of a row of zeros
+constexpr int kNoExp = -100000;      // of zeros: below every other, so that they never set the units of the output
 
 __host__ __device__ inline int64_t tile_slots(int64_t T, int64_t B, int rows) { return T / rows + B; }
 constexpr int tile_halves(int D) { return 4 * D * kTileKeys; }      // binary16 values of a tile: k1 k2 v1 v2
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__
     }
     __syncthreads();
     if (tid == 0) {
-        m->v_exp = -e;
+        m->v_exp = most > 0.0f ? -e : kNoExp;
         m->v_flags = (wild ? kWildV : 0) | (any_odd ? kOddV : 0);
     }
     // fragment (db, s) covers values 32 db .. + 31 and 16 keys; lane (d, half) holds the keys that the scores' lane
@@ -400,8 +400,9 @@ __device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const Ti
         s.m = m;
         s.v_exp = vn;
     }
-    // weights in units of 2^-(kWeightBits + d), d <= 0 the distance of this tile's values below the largest
-    const int d = (flags & kWildV) ? 0 : ve - s.v_exp < -60 ? -60 : ve - s.v_exp;
+    // weights in units of 2^-(kWeightBits + d), d <= 0 the distance of this tile's values below the largest (none for
+    // values of zero, whose weights only count in the sum)
+    const int d = (flags & kWildV) || ve == kNoExp ? 0 : ve - s.v_exp < -60 ? -60 : ve - s.v_exp;
     s.f = f;
     s.up = (float)(kWeightBits + d) - s.m;
     s.unit = ldexpf(1.0f, -kWeightBits - d);
@@ -850,7 +851,7 @@ __device__ __forceinline__ void split_by(const float (&x)[8], float by, h8 &y1, 
 
 struct Factors {
     int tile, row;                               // powers of two of the tile, and of this lane's row
-    bool wild;
+    bool wild, zero;                             // zero: the whole tile
 };
 
 __device__ __forceinline__ Factors factors(float top)
@@ -858,6 +859,7 @@ __device__ __forceinline__ Factors factors(float top)
     const float most = wave_max(top), least = wave_max(top > 0.0f ? -top : -kBig);
     Factors f;
     f.tile = __builtin_amdgcn_readfirstlane(normaliser(most, 15));
+    f.zero = !__builtin_amdgcn_readfirstlane(most > 0.0f);
     f.wild = most > 0.0f && __builtin_amdgcn_readfirstlane(normaliser(-least, 15)) - f.tile > kWildBits;
     f.row = f.wild ? normaliser(top, 15) : f.tile;
     return f;
@@ -969,7 +971,7 @@ __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArg
             by = 1.0f;
         }
         asm volatile("" ::: "memory");
-        const TileHead now = {fk.tile, -fv.tile, (fk.wild ? kWildK : 0) | (fv.wild ? kWildV : 0)};
+        const TileHead now = {fk.tile, fv.zero ? kNoExp : -fv.tile, (fk.wild ? kWildK : 0) | (fv.wild ? kWildV : 0)};
         settle<D>(s, y, now, meta, edge, first, half);
         weigh<D>(s, y);
         if (now.flags & kWildV) weigh_rows<D>(s, y, meta, half);
