@@ -50,3 +50,21 @@ def test_prompt_tile_of_zero_values(heads, kv, d, T, where):
         err, most = np.abs(got - want * size), (lim - 1e-44) * size + 1e-44
         assert (err[seen] <= most[seen]).all(), f"values {size}: worst error / bound {np.nanmax((err / most)[seen]):.3g}"
         assert np.isnan(got[~seen]).all()
+
+
+# ------------------------------------------------------------------ scores below fp32
+@pytest.mark.parametrize("heads,kv,d,T", KERNELS)
+@pytest.mark.parametrize("qs,ks,scale", [(1e-20, 1e-17, None), (1e-37, 1.0, None), (1.0, 1e-41, 1e-3), (1e-25, 1e-25, -0.1),
+                                         (1.0, 1.0, 1e-44), (1.0, 1.0, 0.0)])
+def test_prompt_scores_below_the_range(heads, kv, d, T, qs, ks, scale):
+    """Products whose powers of two are below fp32's: the weights are equal, and
+    keys that a query does not see still have none."""
+    note(f"prompt tiny scores {heads} {kv} {d} {T} {qs} {ks} {scale}")
+    T = T - 9
+    host, _ = qkv(rng_for(51, heads, d), T, heads, kv, d)
+    host[0], host[1] = (host[0] * qs).astype(np.float32), (host[1] * ks).astype(np.float32)
+    used = d ** -0.5 if scale is None else float(np.float32(scale))
+    want, sums = ref.prompt(*host, [T], used)
+    got = prompt_of(host, scale=scale)
+    assert np.isfinite(got).all(), f"{np.isnan(got).sum()} NaN"
+    assert (np.abs(got - want) <= ref.bound(sums, T, d)).all()

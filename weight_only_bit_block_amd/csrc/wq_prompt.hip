@@ -372,7 +372,8 @@ __device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const Ti
         for (int i = 0; i < 16; ++i)
             if (first + 8 * (i >> 2) + 4 * half + (i & 3) > 0) x[i] = -__builtin_inff();
     }
-    const float f = ldexpf(1.0f, e > 127 ? 127 : e);
+    // (never 0: times a masked key's -inf that is no number. Products are below 2^38, so such scores are as good as equal)
+    const float f = ldexpf(1.0f, e > 127 ? 127 : e < -126 ? -126 : e);
     float top = fmaxf(x[0], x[1]);
 #pragma unroll
     for (int i = 2; i < 16; ++i) top = fmaxf(top, x[i]);
