@@ -68,3 +68,19 @@ def test_prompt_scores_below_the_range(heads, kv, d, T, qs, ks, scale):
     got = prompt_of(host, scale=scale)
     assert np.isfinite(got).all(), f"{np.isnan(got).sum()} NaN"
     assert (np.abs(got - want) <= ref.bound(sums, T, d)).all()
+
+
+@pytest.mark.parametrize("heads,kv,d", [(4, 2, 128), (8, 2, 128), (16, 2, 128), (4, 2, 64), (16, 2, 64)])
+@pytest.mark.parametrize("lens", [[70, 1, 333], [1100, 0, 2000, 3]])
+@pytest.mark.parametrize("qs,scale", [(1e-41, None), (1e-36, 1e-8), (1.0, 1e-44), (1e-38, -1e-3), (1.0, 0.0)])
+def test_decode_scores_below_the_range(heads, kv, d, lens, qs, scale):
+    """The same over the cache, whose last pages end inside a tile."""
+    note(f"decode tiny scores {heads} {kv} {d} {lens} {qs} {scale}")
+    torch = torch_cuda()
+    rng = rng_for(52, heads, d, len(lens))
+    table, pages = table_for(rng, lens)
+    host, cache = cache_arrays(rng, pages, kv, d)
+    q = (rng.standard_normal((len(lens), heads, d)) * qs).astype(np.float32)
+    out = torch.full(q.shape, NAN, device="cuda")
+    wqa.attn_decode(dev(q), cache, dev(table), dev(np.array(lens, np.int32)), scale=scale, out=out)
+    check_decode(out, q, host, table, lens, d ** -0.5 if scale is None else float(np.float32(scale)))

@@ -434,7 +434,8 @@ next_sequence:
         for (int o = 1; o < 64; o <<= 1)
             if (o < BC || o >= 16) top = fmaxf(top, __shfl_xor(top, o));
         const int e2 = top > 0.0f ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-        const float fe = ldexpf(1.0f, c_exp - e2 > 127 ? 127 : c_exp - e2);
+        // (never 0: times a masked token's -inf that is no number. Sums are below 2^42, so such scores are as good as equal)
+        const float fe = ldexpf(1.0f, c_exp - e2 > 127 ? 127 : c_exp - e2 < -126 ? -126 : c_exp - e2);
 #pragma unroll
         for (int i = 0; i < HL; ++i) f[i] = __shfl(fe, 4 * (g & 1) + i * BC);
 #pragma unroll
