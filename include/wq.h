@@ -382,10 +382,13 @@ uint64_t wq_attn_decode_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t h
  * operands of the fp16 matrix cores; q, and the weights times the value
  * scales, are split into two binary16 parts after power-of-two normalisation;
  * sums, softmax maximum and sum in fp32. Error: as wq_attn_prefill's for the
- * dequantized rows, 16 times the head's largest value scale in place of
- * max |v|. Long sequences are split over
+ * dequantized rows, 16 times the largest finite value scale of the head's first
+ * lens[b] tokens in place of max |v|. Long sequences are split over
  * workgroups and joined in a fixed order. lens[b] == 0 gives a row of zeros;
- * a non-finite query value makes its head NaN;
+ * a non-finite query value makes its head NaN, a NaN key scale the heads that
+ * read it; a value scale that is not finite makes its block's elements of those heads
+ * non-finite, and no others. (An infinite key scale, which wq_kv_append never
+ * stores, makes the heads that read it NaN or counts as a weight of 0.)
  * a length outside [0, 64 * max_pages], or a page outside [0, n_pages) among
  * those the length covers, gives rows of NaN for that sequence and reads
  * nothing outside the cache. Rows past lens[b] may hold anything.

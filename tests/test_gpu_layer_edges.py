@@ -84,3 +84,60 @@ def test_decode_scores_below_the_range(heads, kv, d, lens, qs, scale):
     out = torch.full(q.shape, NAN, device="cuda")
     wqa.attn_decode(dev(q), cache, dev(table), dev(np.array(lens, np.int32)), scale=scale, out=out)
     check_decode(out, q, host, table, lens, d ** -0.5 if scale is None else float(np.float32(scale)))
+
+
+# ------------------------------------------------------------------ scales that are not finite
+@pytest.mark.parametrize("heads,kv,d", [(4, 2, 128), (8, 2, 128), (16, 2, 128), (4, 2, 64), (16, 2, 64)])
+@pytest.mark.parametrize("lens", [[900], [2000, 1100]])
+@pytest.mark.parametrize("bad", [NAN, float("inf"), -float("inf")])
+def test_decode_value_scale_that_is_not_finite(heads, kv, d, lens, bad):
+    """One value block that is not finite makes its own elements so; all others keep
+    the precision that the finite scales give them."""
+    note(f"decode bad value scale {heads} {kv} {d} {lens} {bad}")
+    torch = torch_cuda()
+    rng = rng_for(53, heads, d, len(lens))
+    table, pages = table_for(rng, lens)
+    host, _ = cache_arrays(rng, pages, kv, d)
+    host[3] = (host[3].astype(np.float32) * 2.0 ** -7).astype(np.float16)        # about 1e-3
+    q = rng.standard_normal((len(lens), heads, d)).astype(np.float32)
+    want, sums = ref.decode(q, ref.values(*host[:2]), ref.values(*host[2:]), host[3], table, lens, d ** -0.5)
+    lim = ref.bound(sums, max(lens), d)
+    host[3][table[0, 0], 1, 9, 1] = bad
+    host[2][table[0, 0], 1, 9, 32:64] = 3
+    hit = np.zeros(q.shape, bool)
+    hit[0, heads // 2:, 32:64] = True
+    out = torch.zeros(q.shape, device="cuda")
+    wqa.attn_decode(dev(q), cache_on(host), dev(table), dev(np.array(lens, np.int32)), out=out)
+    got = out.cpu().numpy().astype(np.float64)
+    assert not np.isfinite(got[hit]).any()
+    err = np.abs(got - want)
+    assert (err[~hit] <= lim[~hit]).all(), f"worst error / bound {np.nanmax((err / lim)[~hit]):.3g}"
+
+
+def test_decode_after_a_token_that_is_not_finite():
+    """The same through the append: a token with a NaN among its values costs the
+    others nothing."""
+    note("decode after a NaN token")
+    torch_cuda()
+    heads, kv, d, n = 8, 2, 128, 960
+    rng = rng_for(54)
+    table, pages = table_for(rng, [n])
+    k = rng.standard_normal((n, kv, d)).astype(np.float32)
+    v = (rng.standard_normal((n, kv, d)) * 2.0 ** -12).astype(np.float32)
+    clean = [np.zeros((pages, kv, ref.PAGE, w), t) for w, t in ((d, np.int8), (d // 32, np.float16)) * 2]
+    for j, x in ((0, k), (2, v)):
+        codes, scales = ref.quantize(x)
+        at = table[0, np.arange(n) // ref.PAGE], np.arange(n) % ref.PAGE
+        clean[j][at[0], :, at[1]], clean[j + 1][at[0], :, at[1]] = codes, scales
+    clean[2][table[0, 0], 0, 5, 96:], clean[3][table[0, 0], 0, 5, 3] = 0, 0
+    v[5, 0, 100] = np.nan
+    cache = wqa.KVCache.empty(pages, kv, d)
+    wqa.kv_append(cache, dev(k), dev(v), dev(table))
+    q = rng.standard_normal((1, heads, d)).astype(np.float32)
+    got = wqa.attn_decode(dev(q), cache, dev(table), dev(np.array([n], np.int32))).cpu().numpy()
+    want, sums = ref.decode(q, ref.values(*clean[:2]), ref.values(*clean[2:]), clean[3], table, [n], d ** -0.5)
+    lim = ref.bound(sums, n, d)
+    hit = np.zeros(q.shape, bool)
+    hit[0, :4, 96:] = True
+    assert np.isnan(got[hit]).all()
+    assert (np.abs(got - want)[~hit] <= lim[~hit]).all()

@@ -212,6 +212,14 @@ __device__ __forceinline__ void read_rows(const uint8_t *p, h4 &a, h4 &b, h4 &c,
 // 8 codes of a dword, in the order of nibbles 0 4 1 5 2 6 3 7.
 __device__ __forceinline__ int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
 
+// Binary16 bits in the order of their magnitudes, the sign shifted out; infinities and NaNs wrap round to below zero.
+constexpr uint32_t kRankZero = 0x800;
+template <typename V>
+__device__ __forceinline__ V scale_rank(V bits)
+{
+    return bits * (uint16_t)2 + (uint16_t)kRankZero;
+}
+
 // The codes of a dword as exact binary16 values.
 __device__ __forceinline__ h8 codes8(uint32_t x)
 {
@@ -465,7 +473,7 @@ next_sequence:
         l[i] = 0.0f;
     }
     int v_exp = kMinScaleExp;
-    uint16_t v_limit = 1;                                        // 2^v_exp as binary16 bits
+    uint32_t v_limit = kRankZero + 2;                            // scale_rank of 2^v_exp (past 16 bits for 2^16: never passed)
     // Tokens of the output's operands: element e of product x is token 16 (2 x + e / 4) + 4 g + e % 4. The
     // codes' transposed read puts row c of the lanes into nibble c % 8 of dword c / 8, nibble_of(e) = c % 8.
     const int vn = c & 7, ve = vn < 4 ? 2 * vn : 2 * (vn - 4) + 1;
@@ -531,9 +539,10 @@ next_sequence:
                     for (int i = 0; i < HL; ++i) x[i][j] = -__builtin_inff();
                 }
         }
-        // largest magnitude of the value scales, as bits (what is not finite is larger than what is)
+        // largest magnitude of the value scales, in the order of scale_rank (those that are not finite spoil their own
+        // blocks only: the others are held against the finite ones)
         typedef uint16_t ub __attribute__((ext_vector_type(NB)));
-        const ub wmax = __builtin_elementwise_max(__builtin_bit_cast(ub, w[0]) & (uint16_t)0x7FFF, __builtin_bit_cast(ub, w[1]) & (uint16_t)0x7FFF);
+        const ub wmax = __builtin_elementwise_max(scale_rank(__builtin_bit_cast(ub, w[0])), scale_rank(__builtin_bit_cast(ub, w[1])));
         uint16_t vtop = wmax[0];
 #pragma unroll
         for (int i = 1; i < NB; ++i) vtop = vtop > wmax[i] ? vtop : wmax[i];
@@ -545,7 +554,7 @@ next_sequence:
             raise |= top[i] > m[i] + kSlack;
         }
         if (__any(raise)) {
-            float vmax = fminf((float)__builtin_bit_cast(_Float16, vtop), 65504.0f);
+            float vmax = vtop > kRankZero ? (float)__builtin_bit_cast(_Float16, (uint16_t)((vtop - kRankZero) >> 1)) : 0.0f;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, o));
             const int en = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
@@ -564,7 +573,7 @@ next_sequence:
                     for (int k = 0; k < BC; ++k) acc[n][i * BC + k] *= by;
             }
             v_exp = en;
-            v_limit = __builtin_bit_cast(uint16_t, (_Float16)ldexpf(1.0f, en));
+            v_limit = kRankZero + 2 * (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(1.0f, en));
         }
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
