@@ -324,7 +324,10 @@ uint64_t wq_attn_prefill_ws(int64_t T, int64_t B, int64_t heads, int64_t kv_head
  * 2 (3 2^-22 + (3 head_dim / 16 + 4) 2^-24) |scale| |q|_2 |k|_2 (a weight moves
  * with it, and the sum of weights too), weights and values add
  * (5 2^-22 + (11 n / 16 + 8) 2^-24) sum p |v| + (2^-36 + n 2^-37) max |v|, the
- * maximum over the visible values of the head.
+ * maximum over the visible values of the head. Where the query's own 32 keys
+ * (counted from the sequence's first) hold later values more than 8 times
+ * larger, add 2^-24 of the sum over its visible keys of p max |v_u|, each row's
+ * own largest value.
  * Non-finite data stays with the rows that see it: a NaN or infinity in a
  * query makes its row NaN, in a key every row that sees the key, in element d of a
  * value element d of every row that sees the value; no other output changes.

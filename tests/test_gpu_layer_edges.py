@@ -141,3 +141,30 @@ def test_decode_after_a_token_that_is_not_finite():
     hit[0, :4, 96:] = True
     assert np.isnan(got[hit]).all()
     assert (np.abs(got - want)[~hit] <= lim[~hit]).all()
+
+
+# ------------------------------------------------------------------ larger values that a query does not see
+@pytest.mark.parametrize("heads,kv,d,T", KERNELS)
+@pytest.mark.parametrize("bits", [3, 8, 13, 14])
+def test_prompt_larger_values_behind_a_query(heads, kv, d, T, bits):
+    """The last keys of every 32 have values 2^bits above the others, and set the
+    units of the tile also for queries that do not see them. A tile's operands
+    are off by 2^-25 at most where its largest value has become 2^14 or more,
+    that is by 2^-39 of it: within the bound's 2^-36 up to 8 times larger ones.
+    Rows keep a common factor up to 2^15 between them, so it is never more
+    than 2^-24 of the row's own largest value."""
+    note(f"prompt larger values behind {heads} {kv} {d} {T} {bits}")
+    host, _ = qkv(rng_for(55, heads, d), T, heads, kv, d)
+    v = host[2]
+    v[:, :, 1::2] *= np.float32(2.0 ** -11)              # elements far below their row's largest
+    late = np.arange(T) % 32 >= 30
+    v[late] *= np.float32(2.0 ** bits)
+    want, sums = ref.prompt(*host, [T], d ** -0.5)
+    lim = ref.bound(sums, T, d)
+    rows = np.abs(v).max(2)                              # [T, kv]
+    if bits > 3:
+        extra = ref.prompt(host[0], host[1], np.repeat(rows[:, :, None], d, 2), [T], d ** -0.5)[0]
+        lim = lim + 2.0 ** -24 * extra
+    got = prompt_of(host)
+    err = np.abs(got - want)
+    assert (err <= lim).all(), f"worst error / bound {np.nanmax(err / lim):.3g}"
