@@ -168,3 +168,69 @@ def test_prompt_larger_values_behind_a_query(heads, kv, d, T, bits):
     got = prompt_of(host)
     err = np.abs(got - want)
     assert (err <= lim).all(), f"worst error / bound {np.nanmax(err / lim):.3g}"
+
+
+# ------------------------------------------------------------------ walks that nothing else takes
+@pytest.mark.parametrize("heads,kv,d,lens", [(24, 8, 128, [2900]), (8, 2, 128, [6000, 3000, 31]), (40, 8, 64, [4000]), (16, 2, 64, [33, 7000, 3300, 0, 64])])
+def test_prompt_long_walk(heads, kv, d, lens):
+    """Hundreds of tiles through the double buffer of the kernel for long prompts,
+    some rows checked against the 64-bit form of their own."""
+    note(f"prompt long walk {heads} {kv} {d} {lens}")
+    T = sum(lens)
+    rng = rng_for(56, heads, d)
+    host, _ = qkv(rng, T, heads, kv, d)
+    got = prompt_of(host, cu=cu_of(lens))
+    q, k, v = (x.astype(np.float64) for x in host)
+    at = 0
+    for n in lens:
+        rows = sorted({0, n // 2, n - 1, *rng.integers(0, n, 20).tolist()}) if n else []
+        for j in range(heads):
+            kk, vv = k[at:at + n, j // (heads // kv)], v[at:at + n, j // (heads // kv)]
+            if not rows:
+                continue
+            see = np.arange(n)[None, :] <= np.array(rows)[:, None]
+            o, pv, first = ref._attend(q[at:at + n][rows, j], kk, vv, d ** -0.5, see)
+            top = np.maximum.accumulate(np.abs(vv).max(1))[rows][:, None] * np.ones((1, d))
+            lim = ref.bound(np.stack([pv, first, top]), n, d)
+            assert (np.abs(got[at:at + n][rows, j] - o) <= lim).all(), (n, j)
+        at += n
+    assert np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("heads,kv,d,lens,width", [(300, 300, 64, [2300, 0, 5, 400], 0), (600, 600, 128, [2200], 0),
+                                                   (600, 300, 64, [70, 2100, 256], 0), (16, 8, 128, [1, 64, 65, 0, 300], 256),
+                                                   (16, 8, 128, [0, 0, 0], 64), (8, 8, 64, [16], 4096), (14, 2, 64, [40] * 9, 300)])
+def test_decode_cut_of_few_steps_and_many_heads(heads, kv, d, lens, width):
+    """So many heads that a run of steps is the whole batch, and tables of a fixed
+    width far beyond the lengths, where most workgroups find nothing to do."""
+    note(f"decode cut {heads} {kv} {d} {lens} {width}")
+    torch = torch_cuda()
+    rng = rng_for(57, heads, d, len(lens))
+    table, pages = table_for(rng, lens)
+    if width:
+        table = np.pad(table, ((0, 0), (0, width - table.shape[1])), constant_values=-1)
+    host, cache = cache_arrays(rng, pages, kv, d)
+    q = rng.standard_normal((len(lens), heads, d)).astype(np.float32)
+    out = torch.full(q.shape, NAN, device="cuda")
+    wqa.attn_decode(dev(q), cache, dev(table), dev(np.array(lens, np.int32)), out=out)
+    check_decode(out, q, host, table, lens, d ** -0.5)
+
+
+@pytest.mark.parametrize("lens", [[300, 5], [3000, 5, 0, 1500]])
+def test_decode_rows_of_wider_rows(lens):
+    """Queries and outputs inside wider rows, in groups of five and six heads; what lies between is left alone."""
+    note(f"decode strides {lens}")
+    torch = torch_cuda()
+    for heads, kv, d in ((11, 1, 128), (10, 2, 64)):
+        rng = rng_for(58, heads, d, len(lens))
+        table, pages = table_for(rng, lens)
+        host, cache = cache_arrays(rng, pages, kv, d)
+        q = rng.standard_normal((len(lens), heads, d)).astype(np.float32)
+        qw = torch.full((len(lens), heads * d + 20), NAN, device="cuda")
+        qs = qw[:, 8:8 + heads * d].unflatten(1, (heads, d))
+        qs.copy_(dev(q))
+        wide = torch.full((len(lens), heads * d + 52), NAN, device="cuda")
+        out = wide[:, 4:4 + heads * d].unflatten(1, (heads, d))
+        wqa.attn_decode(qs, cache, dev(table), dev(np.array(lens, np.int32)), out=out)
+        check_decode(out, q, host, table, lens, d ** -0.5)
+        assert torch.isnan(wide[:, :4]).all() and torch.isnan(wide[:, 4 + heads * d:]).all()
