@@ -395,7 +395,8 @@ uint64_t wq_attn_decode_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t h
  * a length outside [0, 64 * max_pages], or a page outside [0, n_pages) among
  * those the length covers, gives rows of NaN for that sequence and reads
  * nothing outside the cache. Rows past lens[b] may hold anything.
- * B * heads is below 2^23, max_pages below 2^25, B * max_pages below 2^32.
+ * out must not alias an input. B * heads is below 2^23, max_pages below 2^25,
+ * B * max_pages below 2^32.
  */
 int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
                    const int32_t *lens, int64_t B, const int32_t *table, int64_t max_pages, float scale,
@@ -414,7 +415,8 @@ int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, i
  * both); pre_weight null: weight 1. gate is [M][N] (gate_stride N) or one row
  * for all (gate_stride 0). h_out may be h itself; no other outputs alias an
  * input or each other. Rows are contiguous, N >= 1 of any size, and pointers need only
- * 4-byte alignment here. Sums in fp32 (rows above 16384: in fp64).
+ * 4-byte alignment here. Squares in fp32, sums in fp32 (rows above 16384: in
+ * fp64): a row whose squares pass fp32's range is normed to zeros.
  */
 int wq_residual_norm(const float *h, const float *y, const float *post_weight, const float *gate,
                      int64_t gate_stride, float alpha, const float *pre_weight, float eps,

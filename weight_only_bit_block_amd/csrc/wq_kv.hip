@@ -17,7 +17,8 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 // floats, the maximum of a block goes over its 8 lanes by cross-lane moves.
 // Every thread takes kAppendRows rows, keys and values, and asks for all of
 // them before it looks up where they go (three dependent reads). 4096 tokens, 8
-// heads of 128: 10.3 us, 3.7 TB/s (rows read with cached loads: 10.9); 16384: 33.0, 4.6.
+// heads of 128, calls back to back: 10.3 us, 3.7 TB/s (rows read with cached loads: 10.9;
+// inputs still in the last-level cache 8.9, six sets in turn 11.1); 16384: 31, 4.9.
 //
 // The quotients of wq_pack's rule are correctly rounded; here they cost three
 // operations each instead of a division's ten: q0 = x r, q = q0 + r (x - q0 s)
@@ -159,7 +160,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t by_h
 //
 // A tile goes from LDS to registers at once and the copies of the next tile
 // into the same LDS go out before anything is computed, so that copies are
-// under way all the time and 12 wavefronts of 11 KiB share a compute unit's LDS.
+// under way all the time with one buffer of 11 KiB a wavefront (heads of 128;
+// 8 wavefronts a compute unit, by their registers and by kFill).
 //
 // Lengths are device data, so the split is made on the device: the sequences'
 // steps of 256 tokens (4 tiles, one per wavefront) are laid end to end and every
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t by_h
 // that lies in one run is finished there; the pieces of others go to a workspace
 // and a second kernel joins them in order.
 //
-// 8 heads of 128: one sequence of 131072, 2 query heads each, 31 us (4.9 TB/s), joining
+// 8 heads of 128: one sequence of 131072, 2 query heads each, 30 us (5.0 TB/s), joining
 // them 5.9; 64 sequences of 262139 in all, 4 query heads each, 63 us (4.8 TB/s, bound by the
 // vector instructions that make weights of scores and numbers of codes), joining 4.8.
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -242,7 +244,11 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
 // heads each: 1 x 500 tokens 8.1 / 10.8, 1 x 1000 10.9 / 10.9, 1 x 2040 17.0 / 11.1, 16 x 1500
 // 15.7 / 16.9, 32 x 777 12.7 / 17.6, 32 x 2040 20.4 / 23.7; 520 x 300 and one of 65536
 // 365 / 107, 1024 x 2560 497 / 526, 2048 ragged of 500 in the mean 359 / 350, 4096 of 300
-// 527 / 555).
+// 527 / 555). The limits do not follow all of these: batches of 16 to 31 sequences of 17 to 32
+// pages are cut and would be faster without (16 x 1100 13.4 / 15.5, 16 x 1500 15.3 / 17.9, 31 x 2040
+// 19.3 / 24.1; 8 x 2040 18.1 / 15.6). It is the table's width that decides, since the lengths are on the
+// device: short sequences in a table made for long ones are cut (1 x 300 7.6 us, 10.4 in a
+// table of 256 pages; 32 x 777 12.4, 18.3; 64 x 1000 19.2, 20.5).
 constexpr int kFill = 512;
 constexpr int kCutMaxSeqs = 2048;
 constexpr int kShortPages = 16;

@@ -11,7 +11,9 @@
 // spends more on the barriers of its sums, four leave fewer wavefronts, in us
 // for 1 / 2 / 4 groups, gate and both norms: 1 x 1024 3.9 / 3.9 / 4.4, 4096 x 1024
 // 16.5 / 15.0 / 14.7 (5.7 TB/s), 1024 x 4096 18.1 / 15.7 / 14.6, 515 x 5003
-// - / 15.4 / 17.1, 512 x 8192 - / 19.3 / 15.0. A row of 1024 in one wavefront: 5.0,
+// - / 15.4 / 17.1, 512 x 8192 - / 19.3 / 15.0. (Between 2560 and 5120 values two groups are
+// the better choice for most numbers of rows: 64 x 4096 4.7 / 5.5, 4096 x 4096 60.0 / 62.3, 1024 x 5100
+// 23.7 / 24.6 for 2 / 4, though not for 1024 x 4096.) A row of 1024 in one wavefront: 5.0,
 // 4096 of them 17.3. Loads and stores of 4 values ask for 4-byte alignment only,
 // so odd widths and offset storage take the same path; the last values of an odd
 // row go one by one.

@@ -29,8 +29,8 @@
 // walked first to last, so that its precision never depends on values it does
 // not see by more than the 2^14 of one tile.
 //
-// Bound: the matrix cores in long prompts (8192 tokens, 16 heads of 128: 812 us,
-// 1014 TFLOP/s of binary16 products where a large library product reaches 1205), the
+// Bound: in long prompts the rate of binary16 products (8192 tokens, 16 heads of 128: 815 us,
+// 1012 TFLOP/s where a large library product reaches 1205 of nominal 2500), the
 // latency of a launch or two in short ones (128 tokens: 10.6 us), in between the L2's
 // k and v and the issue of matrix and vector instructions in turns (1024 tokens: 30 us).
 #include "wq_internal.h"
@@ -116,7 +116,8 @@ __device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo)
 
 // ---------------------------------------------------------------- prepare
 // One workgroup per (tile, key/value head, k or v); 8 threads share a row of D
-// values. All latency at short prompts, 5.3 KiB in and out per row at long ones.
+// values. All latency at short prompts; at long ones 4 D bytes in and as many out for a
+// row (8192 tokens, 8 heads of 128: 134 MB, 36 us).
 template <int CTRL>
 __device__ __forceinline__ float max_dpp(float x)
 {
@@ -1015,7 +1016,11 @@ inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((u
 // 33 / 36, 12 (576) 44 / 43; of different lengths, 4 of 4094 in all (560) 139 / 156, 13 of
 // 4997 (832) 102 / 105, 24 of 4085 (880) 68 / 80, 24 of 7990 (1376) 134 / 125; 12 heads, 8 of
 // 3998 (468) 70 / 101. Heads of 64: one prompt of 4096 (528) 141 / 170, 8 of 1024 (1152) 97 / 96, 16
-// of 7991 (1248) 85 / 106, 24 of 7989 (1204) 64 / 67, 8 of 15995 (2112) 1012 / 932.
+// of 7991 (1248) 85 / 106, 24 of 7989 (1204) 64 / 67, 8 of 15995 (2112) 1012 / 932. The limit of
+// 1200 lies between what many prompts and one would have: 24 of 7977 (1204) 60 / 68, 16 of 7982
+// (1248) 104 / 118, but one of 9700 (1216) 690 / 658, of 11300 (1246) 812 / 789. The number of
+// prompts stands for how their lengths differ, which only the device knows: one long prompt
+// beside empty ones counts as several.
 inline int64_t few_groups(int D, int64_t B) { return D == 64 ? 1200 : B >= 4 ? 880 : 528; }
 
 // Prompts so short are not prepared: no wavefront has more than one tile of 128 values (two of

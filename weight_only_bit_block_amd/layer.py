@@ -5,7 +5,8 @@ the residual norms.
 As in wq.py the binding marshals arguments only. Every tensor of a call lives
 on one device, which need not be the current one; work goes to `stream`, else
 to that device's current stream, and outputs and workspaces allocated here
-belong to that stream. Bad arguments raise ValueError (or WqError where the
+belong to that stream (tensors of another stream have to be ready for it and stay
+until it is done with them, as everywhere in torch). Bad arguments raise ValueError (or WqError where the
 library refuses them) before anything is launched.
 """
 from __future__ import annotations
@@ -167,7 +168,8 @@ def attn_prefill(q, k, v, cu: Optional[torch.Tensor] = None, scale: Optional[flo
     [T, kv_heads, head_dim] in fp32, rows of any 16-byte stride (slices of a
     fused projection's output); cu int32 [sequences + 1] token offsets on the
     device (None: one prompt). scale defaults to head_dim ** -0.5. Returns out
-    [T, heads, head_dim]; rows of no sequence are not written."""
+    [T, heads, head_dim], which must not alias an input; rows of no sequence are
+    not written."""
     T, H, D, qs = _heads(q, "q")
     at = q.get_device()
     Tk, Hk, Dk, ks = _heads(k, "k", at)
@@ -217,8 +219,8 @@ def attn_decode(q, cache: KVCache, table, lens, scale: Optional[float] = None, o
     """Attention of one query token per sequence over the cache: q
     [sequences, heads, head_dim] fp32, table int32 [sequences, max_pages], lens
     int32 [sequences] cached tokens (the new one included). scale defaults to
-    head_dim ** -0.5. Returns out like q: zeros where lens is 0, NaN where a
-    length or page lies outside the table or the cache."""
+    head_dim ** -0.5. Returns out like q (not aliasing an input): zeros where
+    lens is 0, NaN where a length or page lies outside the table or the cache."""
     B, H, D, qs = _heads(q, "q")
     at = q.get_device()
     c = cache._struct(at)
@@ -257,7 +259,8 @@ def residual_norm(h, y=None, post_weight=None, gate=None, alpha: float = 1.0, pr
     y None: h_out is h (the norm before the first block, not stored unless
     h_out is given). x_out is computed where pre_weight or x_out is given, or
     where norm is True (weight 1). Returns (h_out, x_out), None for what was
-    not computed. h_out may be h."""
+    not computed. h_out may be h; no other output may alias an input or the
+    other output."""
     if not (isinstance(h, _Tensor) and h.dtype is _F32 and h.dim() == 2 and h.is_cuda and h.is_contiguous()):
         raise ValueError("h must be a contiguous float32 device tensor [M, N]")
     at, shape = h.get_device(), h.shape
