@@ -416,7 +416,7 @@ int wq_attn_decode(const wq_kv_cache *cache, const float *q, int64_t q_stride, i
  * for all (gate_stride 0). h_out may be h itself; no other outputs alias an
  * input or each other. Rows are contiguous, N >= 1 of any size, and pointers need only
  * 4-byte alignment here. Squares in fp32, sums in fp32 (rows above 16384: in
- * fp64): a row whose squares pass fp32's range is normed to zeros.
+ * fp64): a row whose sum of squares passes fp32's range is normed to zeros.
  */
 int wq_residual_norm(const float *h, const float *y, const float *post_weight, const float *gate,
                      int64_t gate_stride, float alpha, const float *pre_weight, float eps,

@@ -234,3 +234,20 @@ def test_decode_rows_of_wider_rows(lens):
         wqa.attn_decode(qs, cache, dev(table), dev(np.array(lens, np.int32)), out=out)
         check_decode(out, q, host, table, lens, d ** -0.5)
         assert torch.isnan(wide[:, :4]).all() and torch.isnan(wide[:, 4 + heads * d:]).all()
+
+
+# ------------------------------------------------------------------ norms
+@pytest.mark.parametrize("N", [5, 300, 3000, 9000, 20001])
+def test_norm_of_squares_past_the_range(N):
+    """A row whose sum of squares passes fp32's range is normed to zeros, the block's output too; the other rows are not touched by it."""
+    note(f"norm past the range {N}")
+    rng = rng_for(59, N)
+    h, y = rng.standard_normal((2, 4, N)).astype(np.float32)
+    h[1] *= np.float32(1e25)
+    y[2] *= np.float32(1e30)
+    h_out, x = (t.cpu().numpy() for t in wqa.residual_norm(dev(h), dev(y), post_weight=dev(np.ones(N, np.float32)), norm=True))
+    assert np.array_equal(h_out[2], h[2]) and (x[1] == 0).all()
+    want = ref.residual_norm(h[[0, 3]], y[[0, 3]], np.ones(N), None, 1.0, None, float(np.float32(1e-6)))
+    # a norm is off by 40 half steps (64 levels of its sum halved by the root, root, division, products); twice, and h_out in between
+    assert np.allclose(h_out[[0, 3]], want[0], rtol=0, atol=80 * ref.U32 * want[1].max())
+    assert np.allclose(x[[0, 3]], want[2], rtol=0, atol=400 * ref.U32 * np.abs(want[2]).max())
