@@ -422,6 +422,123 @@ int wq_residual_norm(const float *h, const float *y, const float *post_weight, c
                      int64_t gate_stride, float alpha, const float *pre_weight, float eps,
                      int64_t M, int64_t N, float *h_out, float *x_out, hipStream_t stream);
 
+/* ------------------------------------------------------------------ a serving step
+ * What a step of a serving program adds around the cache: its plan, the norms and
+ * the rotation of queries and keys, and two more forms of attention. Conventions
+ * as between the projections.
+ */
+
+/*
+ * wq_kv_plan -- the plan of one step from the requests' lengths:
+ *   cu[b]     the tokens of the requests before b (cu[B]: of all), sums past
+ *             2^31 - 1 stay there;
+ *   lens[b]   start[b] + fresh[b], the cached tokens after the step;
+ *   table     request b's row [max_pages] gets a free page for every page that its
+ *             new tokens begin: entries ceil(start / 64) to ceil(lens / 64) - 1
+ *             (those inside the row). Pages are taken from free_pages [n_free] in
+ *             the order of the requests, from entry `taken` on; an entry that the
+ *             list no longer covers becomes -1. Other entries stay;
+ *   taken_out taken plus the pages the step wants (at most 2^31 - 1): more than
+ *             n_free where the list was too short;
+ *   positions of token t = cu[b] + i: start[b] + i;
+ *   slots     the token's place in the cache, page * 64 + position % 64, for
+ *             wq_kv_append_slots; -1 where the token has no page (past the row, or
+ *             an entry below 0).
+ * positions and slots hold T entries; those past cu[B] become -1, tokens past T
+ * are left out. start may be null (all 0), taken too (0); positions and slots may
+ * be null when not wanted. A request with a negative length, or of more than
+ * 2^31 - 1 tokens, gets no token and no page, and lens -1. B is below 2^24,
+ * max_pages below 2^25, n_free below 2^31, T below 2^30. taken_out must not be
+ * taken, and no other output may alias an input: the same inputs give the same
+ * plan again.
+ */
+int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *table, int64_t max_pages,
+               const int32_t *free_pages, int64_t n_free, const int32_t *taken, int64_t T, int32_t *cu, int32_t *lens,
+               int32_t *positions, int64_t *slots, int32_t *taken_out, hipStream_t stream);
+
+/*
+ * wq_qk_norm_rope -- the norms of queries and keys for each head, with the
+ * rotation by position in the same pass. For every head of q and k
+ *   y = x * rsqrt(mean(x^2) + eps) * weight       (norm 0: y = x)
+ *   (y_i, y_i') -> factor * (y_i cos a - y_i' sin a, y_i' cos a + y_i sin a),
+ *   a = positions[t] * inv_freq[i],  i < pairs;
+ * i' is i + pairs, or, interleaved, the pair is values 2 i and 2 i + 1; values from
+ * 2 pairs on keep y. inv_freq [pairs] is on the device; pairs is a multiple of
+ * 4, at most head_dim / 2 (0: no rotation, inv_freq may be null). q_weight and
+ * k_weight [head_dim] are 16-byte aligned, null for 1. The angle is computed in
+ * fp64 (off by 2^-53 of itself), reduced to a turn, and its sine and cosine taken
+ * in fp32; sums of squares in fp32, of values brought into its range where
+ * the squares leave it. Error: 28 2^-24 |factor| of the larger of |y_i| and |y_i'|,
+ * and as much of it as 4 times the angle's error.
+ * heads and kv_heads may be any number, one of them 0 (its pointers null then).
+ * Rows of tokens with a negative position are not written. q_out may be q and
+ * k_out may be k (with the same stride); no other aliasing.
+ */
+int wq_qk_norm_rope(const float *q, int64_t q_stride, int64_t heads, const float *k, int64_t k_stride,
+                    int64_t kv_heads, int64_t head_dim, int64_t T, const int32_t *positions, const float *inv_freq,
+                    int64_t pairs, int interleaved, float factor, int norm, const float *q_weight,
+                    const float *k_weight, float eps, float *q_out, int64_t q_out_stride, float *k_out,
+                    int64_t k_out_stride, hipStream_t stream);
+
+/*
+ * wq_kv_append_slots -- wq_kv_append with each token's place given: token t goes
+ * to row slots[t] % 64 of page slots[t] / 64. Rows whose slot lies outside the
+ * cache (negative ones, as wq_kv_plan leaves them) are dropped. Where two tokens
+ * have one slot, either may be kept, or parts of both.
+ */
+int wq_kv_append_slots(const wq_kv_cache *cache, const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                       int64_t T, const int64_t *slots, hipStream_t stream);
+
+/*
+ * wq_attn_prefill_window -- wq_attn_prefill where a query at position t of its
+ * sequence sees the keys u <= t with u > t - window or u < sinks: the last
+ * `window` ones, itself included, and the sequence's first `sinks`. window >= 1,
+ * sinks >= 0; sizes past T mean T. Workspace: wq_attn_prefill_ws. Error and
+ * non-finite data as there, over the keys a query sees; for the term with 2^-36 and
+ * 2^-37 max |v| is taken over the 32 keys (counted from the sequence's first) of
+ * every key it sees, hidden ones included.
+ */
+int wq_attn_prefill_window(const float *q, int64_t q_stride, const float *k, int64_t k_stride,
+                           const float *v, int64_t v_stride, int64_t T, const int32_t *cu, int64_t B,
+                           int64_t heads, int64_t kv_heads, int64_t head_dim, float scale, int64_t window,
+                           int64_t sinks, float *out, int64_t out_stride, void *workspace,
+                           uint64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace wq_attn_decode_window needs, as wq_attn_decode_ws. */
+uint64_t wq_attn_decode_window_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages,
+                                  int64_t window, int64_t sinks);
+
+/*
+ * wq_attn_decode_window -- wq_attn_decode over the last `window` of the lens[b]
+ * cached tokens and the first `sinks` ones. window >= 1, sinks >= 0. Pages that
+ * hold none of those are not looked at: their table entries may be anything, so
+ * they can be given to others.
+ */
+int wq_attn_decode_window(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
+                          const int32_t *lens, int64_t B, const int32_t *table, int64_t max_pages, float scale,
+                          int64_t window, int64_t sinks, float *out, int64_t out_stride, void *workspace,
+                          uint64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace wq_attn_decode_shared needs, as wq_attn_decode_ws. */
+uint64_t wq_attn_decode_shared_ws(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages,
+                                  int64_t prefix_pages);
+
+/*
+ * wq_attn_decode_shared -- wq_attn_decode for sequences that begin with the same
+ * tokens: every query sees the prefix's prefix_len[0] cached tokens, in the pages
+ * prefix [prefix_pages], and its own lens[b] ones, in its table row, as one
+ * softmax. The prefix is read once for all B queries of a head, whatever B;
+ * it need not fill its last page, own tokens begin in pages of their own. Error
+ * and non-finite data as wq_attn_decode's over all tokens a query sees; parts are
+ * joined in a fixed order. Both lengths 0: a row of zeros. A prefix_len outside
+ * [0, 64 * prefix_pages], or a page of the prefix outside the cache among those it
+ * covers, gives NaN in all rows. prefix_pages is below 2^25; other limits as wq_attn_decode's.
+ */
+int wq_attn_decode_shared(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
+                          const int32_t *prefix, int64_t prefix_pages, const int32_t *prefix_len, const int32_t *lens,
+                          int64_t B, const int32_t *table, int64_t max_pages, float scale, float *out,
+                          int64_t out_stride, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
 /* Human-readable text for a wq_status value (static storage). */
 const char *wq_strerror(int status);
 

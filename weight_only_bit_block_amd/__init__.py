@@ -20,13 +20,21 @@ Between the projections of a layer:
     attn_decode(q, cache, table, lens)  attention of one token per sequence over the cache
     residual_norm(h, y, ...)            norms around a block, its gate and its residual
 
+A serving step:
+
+    kv_plan(fresh, table, free, ...)    block tables, positions and slots from request lengths
+    qk_norm_rope(q, k, positions, ...)  norms of queries and keys, rotated by position
+    attn_prefill / attn_decode(..., window, sinks)   attention through a sliding window
+    attn_decode_shared(q, cache, ...)   attention of one token per sequence behind a shared prefix
+
 The library is loaded on first use and must have been built
 (``python -m weight_only_bit_block_amd.build``); there is no fallback.
 """
 from .wq import (BLOCK, GEMV_MAX_M, GroupedCall, Package, WqError, embed, gemm, gemm_noalloc, gemv,
                  header_symbols, linear, load, pack, table_layout, table_plan, table_plan_gemm, unpack)
 
-_LAYER = ("KV_PAGE", "KVCache", "attn_decode", "attn_prefill", "kv_append", "residual_norm")
+_LAYER = ("KV_PAGE", "KVCache", "KVPlan", "attn_decode", "attn_decode_shared", "attn_prefill", "kv_append", "kv_plan",
+          "qk_norm_rope", "residual_norm")
 
 
 def __getattr__(name):
@@ -40,4 +48,5 @@ def __getattr__(name):
 
 __all__ = ["BLOCK", "GEMV_MAX_M", "GroupedCall", "Package", "WqError", "embed", "gemm", "gemm_noalloc", "gemv",
            "header_symbols", "linear", "load", "pack", "table_layout", "table_plan", "table_plan_gemm", "unpack",
-           "KV_PAGE", "KVCache", "attn_decode", "attn_prefill", "kv_append", "residual_norm"]
+           "KV_PAGE", "KVCache", "KVPlan", "attn_decode", "attn_decode_shared", "attn_prefill", "kv_append", "kv_plan",
+           "qk_norm_rope", "residual_norm"]

@@ -20,7 +20,8 @@ OBJDIR = os.path.join(ROOT, "_build", "wq")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["wq_abi.cpp", "wq_pack.hip", "wq_gemv.hip", "wq_mgemv.hip", "wq_gemm.hip", "wq_embed.hip",
-           "wq_layer_abi.cpp", "wq_prompt.hip", "wq_kv.hip", "wq_norm.hip"]
+           "wq_layer_abi.cpp", "wq_prompt.hip", "wq_kv.hip", "wq_norm.hip",
+           "wq_serve_abi.cpp", "wq_shared.hip", "wq_rope.hip", "wq_plan.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -210,6 +210,7 @@ struct PromptArgs {
     float *out;
     int64_t out_stride;
     void *ws;
+    int window, sinks;                          // window 0: all keys up to the query
 };
 struct AppendArgs {
     wq_kv_cache cache;
@@ -220,6 +221,7 @@ struct AppendArgs {
     int B;
     const int32_t *table;
     int64_t max_pages;
+    const int64_t *slots;                       // in place of cu, start and table
 };
 struct DecodeArgs {
     wq_kv_cache cache;
@@ -234,6 +236,40 @@ struct DecodeArgs {
     float *out;
     int64_t out_stride;
     void *ws;
+    int64_t window, sinks;                      // window 0: all keys
+    float *sums;                                // [B][heads][2]: maximum (log2) and sum of weights; null: not wanted
+};
+struct SharedArgs {
+    DecodeArgs own;                             // the sequences' own tokens; own.ws the start of the workspace
+    const int32_t *prefix, *prefix_len;
+    int64_t prefix_pages;
+};
+struct RopeArgs {
+    const float *q, *k;                         // k null: kv_heads 0
+    int64_t q_stride, k_stride;
+    int heads, kv_heads, head_dim;
+    int64_t T;
+    const int32_t *positions;
+    const float *inv_freq;
+    int pairs;
+    float factor;
+    const float *q_weight, *k_weight;           // null: 1
+    float eps;
+    float *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+};
+struct PlanArgs {
+    const int32_t *fresh, *start;               // start null: 0
+    int64_t B;
+    int32_t *table;
+    int64_t max_pages;
+    const int32_t *free_pages;
+    int64_t n_free;
+    const int32_t *taken;                       // null: 0
+    int64_t T;
+    int32_t *cu, *lens, *positions;
+    int64_t *slots;
+    int32_t *taken_out;
 };
 struct NormArgs {
     const float *h, *y, *post, *gate;
@@ -250,6 +286,17 @@ hipError_t launch_attn_prefill(const PromptArgs &a, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream);
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream);
 hipError_t launch_residual_norm(const NormArgs &a, hipStream_t stream);
+// The pages of a table of max_pages that a query with this window can read.
+inline int64_t seen_pages(int64_t max_pages, int64_t window, int64_t sinks)
+{
+    if (window <= 0) return max_pages;
+    const int64_t n = (window - 1) / WQ_KV_PAGE + 2 + (sinks + WQ_KV_PAGE - 1) / WQ_KV_PAGE;
+    return n < max_pages ? n : max_pages;
+}
+uint64_t shared_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages);
+hipError_t launch_attn_decode_shared(const SharedArgs &a, hipStream_t stream);
+hipError_t launch_qk_norm_rope(const RopeArgs &a, bool norm, bool interleaved, hipStream_t stream);
+hipError_t launch_kv_plan(const PlanArgs &a, hipStream_t stream);
 
 }  // namespace wq
 

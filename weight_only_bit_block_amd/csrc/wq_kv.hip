@@ -1,9 +1,11 @@
 // wq_kv.hip -- the int4 key/value cache: append, and attention of single tokens.
 #include "wq_internal.h"
 #include "wq_device.h"
+#include "wq_kv_decode.h"
 #include "wq_seq.h"
 
 #include <math.h>
+#include <type_traits>
 
 namespace wq {
 namespace {
@@ -76,7 +78,8 @@ __device__ __forceinline__ void quantize4(f4 x, uint16_t &codes, uint16_t &scale
 // by_heads, shift: a row number below 2^27 divided by the heads is the upper half of its
 // product with by_heads = ceil(2^(32 + shift) / heads), shifted (heads <= 2^(shift + 1) keeps by_heads
 // within 32 bits and what it is too large by below 2^(shift + 5)).
-template <int D>
+// SLOTS: the rows' places in the cache are given, one number a token.
+template <int D, bool SLOTS>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t by_heads, int shift)
 {
     constexpr int kLanes = D / 4, kRows = 256 / kLanes;  // lanes of a row, rows of a workgroup at a time
@@ -97,7 +100,11 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t by_h
     for (int i = 0; i < kAppendRows; ++i) {
         const uint32_t row = (blockIdx.x * kAppendRows + i) * kRows + threadIdx.x / kLanes, t = by_heads ? __umulhi(row, by_heads) >> shift : row, h = row - t * H;
         dst[i] = -1;
-        if (row < rows) {
+        if (SLOTS && row < rows) {
+            const int64_t slot = a.slots[t];
+            if (slot >= 0 && slot < a.cache.n_pages * WQ_KV_PAGE)
+                dst[i] = (slot / WQ_KV_PAGE * H + h) * WQ_KV_PAGE + slot % WQ_KV_PAGE;
+        } else if (row < rows) {
             const int b = seq_of_token(a.cu, a.B, (int)t);
             const SeqRange r = seq_range(a.cu, (int)a.T, b);
             if ((int)t >= r.begin && (int)t < r.end) {
@@ -181,10 +188,6 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
 
-constexpr int kDecodeWaves = 4;
-constexpr int kTile = WQ_KV_PAGE;
-constexpr int kDecodeStep = kDecodeWaves * kTile;      // chunks are multiples of this many tokens
-constexpr int kMaxGroup = 8;                           // query heads of a workgroup
 constexpr int kWeightBits = 12;
 constexpr float kSlack = 3.0f;
 constexpr int kMinScaleExp = -24;                      // 2^-24 is binary16's smallest
@@ -235,43 +238,34 @@ __device__ __forceinline__ h8 codes8(uint32_t x)
     return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// ---- how the work is cut
-// kFill workgroups in all, 2 on each of 256 compute units; for every kv head and
-// group of query heads equally many. Finding its place makes every workgroup look
-// at all lengths, and the pieces cost a second kernel, so thousands of sequences
-// are not cut, one workgroup each, and neither are short ones: tables of up to 16 pages, or 32
-// where there are kFill / 2 workgroups without (us, uncut / cut, 8 kv heads of 128, 2 query
-// heads each: 1 x 500 tokens 8.1 / 10.8, 1 x 1000 10.9 / 10.9, 1 x 2040 17.0 / 11.1, 16 x 1500
-// 15.7 / 16.9, 32 x 777 12.7 / 17.6, 32 x 2040 20.4 / 23.7; 520 x 300 and one of 65536
-// 365 / 107, 1024 x 2560 497 / 526, 2048 ragged of 500 in the mean 359 / 350, 4096 of 300
-// 527 / 555). The limits do not follow all of these: batches of 16 to 31 sequences of 17 to 32
-// pages are cut and would be faster without (16 x 1100 13.4 / 15.5, 16 x 1500 15.3 / 17.9, 31 x 2040
-// 19.3 / 24.1; 8 x 2040 18.1 / 15.6). It is the table's width that decides, since the lengths are on the
-// device: short sequences in a table made for long ones are cut (1 x 300 7.6 us, 10.4 in a
-// table of 256 pages; 32 x 777 12.4, 18.3; 64 x 1000 19.2, 20.5).
-constexpr int kFill = 512;
-constexpr int kCutMaxSeqs = 2048;
-constexpr int kShortPages = 16;
-constexpr int kChangeSteps = 3;              // 2 and 4 measure the same
-
-__host__ __device__ inline int head_groups(int heads, int kv_heads) { return (heads / kv_heads + kMaxGroup - 1) / kMaxGroup; }
-__host__ __device__ inline bool cut_sequences(int64_t B, int per_step, int64_t max_pages)
-{
-    return B <= kCutMaxSeqs && max_pages > (B * per_step >= kFill / 2 ? 2 * kShortPages : kShortPages);
-}
-__host__ __device__ inline int runs_per_head(int per_step) { return per_step < kFill ? kFill / per_step : 1; }
-
-// Where a sequence's pieces are: runs first .. first + count - 1; the first one's
-// piece is its run's last, slot 1, unless the run begins with it.
-struct Pieces {
-    int first, count, slot, pad;
+// ---- how the work is cut (wq_kv_decode.h)
+// The tiles of a sequence that its query sees. With a window: the last `window`
+// tokens' and the first `sinks` ones'; what lies between is not walked, its pages
+// are not looked at.
+template <bool WIN>
+struct Tiles {
+    int64_t low, sink_end;                   // seen: tokens from low on, and those before sink_end
+    int sinks, skip, count;                  // tiles of first tokens, tiles left out behind them, tiles in all
+    __device__ __forceinline__ Tiles(const DecodeArgs &a, int64_t len) : low(0), sink_end(0), sinks(0), skip(0), count((int)((len + kTile - 1) / kTile))
+    {
+        if constexpr (WIN) {
+            low = len > a.window ? len - a.window : 0;
+            sink_end = a.sinks < low ? a.sinks : low;
+            const int from = (int)(low / kTile), first = (int)((sink_end + kTile - 1) / kTile);
+            sinks = first < from ? first : from;
+            skip = from - sinks;
+            count -= skip;
+        }
+    }
+    __device__ __forceinline__ int tile(int v) const { return WIN && v >= sinks ? v + skip : v; }
+    __device__ __forceinline__ int steps() const { return (count + kDecodeWaves - 1) / kDecodeWaves; }
 };
-constexpr int kSlots = 2;                    // pieces of a run that are not whole sequences: its first and its last
 
+template <bool WIN>
 __device__ __forceinline__ int steps_of(const DecodeArgs &a, int b)
 {
     const int64_t len = a.lens[b];
-    return len < 0 || len > a.max_pages * kTile ? 0 : (int)((len + kDecodeStep - 1) / kDecodeStep);
+    return len < 0 || len > a.max_pages * kTile ? 0 : Tiles<WIN>(a, len).steps();
 }
 
 // A run: sequence b from its step `skip` on, `left` steps in all, those that stand
@@ -282,11 +276,12 @@ struct Run {
 };
 
 // A whole wavefront calls it. left <= 0: nothing.
+template <bool WIN>
 __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
 {
     const int lane = threadIdx.x & 63;
     const auto cost = [&](int b) {
-        const int n = b < a.B ? steps_of(a, b) : 0;
+        const int n = b < a.B ? steps_of<WIN>(a, b) : 0;
         return n > 0 ? n + kChangeSteps : 0;
     };
     const auto scan = [&](int n) {           // sum of the lanes up to this one
@@ -324,18 +319,14 @@ __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
     return {0, 0, 0, 0};
 }
 
-constexpr int kPartialExtra = 4;             // a partial result: D values, then m and l, 16-byte aligned
+// What a call asks for: all keys, those of a window, or all with the maximum and
+// sum of each whole sequence's weights beside its output.
+enum class Form { plain, window, sums };
 
-// Piece `slot` of a workgroup, head hh.
-template <int D>
-__device__ __forceinline__ float *partial(const DecodeArgs &a, int64_t group, int slot, int hh)
-{
-    return (float *)((Pieces *)a.ws + kCutMaxSeqs) + ((group * kSlots + slot) * kMaxGroup + hh) * (D + kPartialExtra);
-}
-
-template <int D, int H, int WPS>
+template <int D, int H, int WPS, Form FORM>
 __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeArgs a, int groups, bool cut, float c_man, int c_exp)
 {
+    constexpr bool WIN = FORM == Form::window;
     constexpr int NB = D / 32, BC = 8 / H, R = NB / BC;          // blocks, of them side by side, chains
     constexpr int HL = H / 2;                                    // heads of a lane's scores
     static_assert(BC * H == 8 && BC * R == NB, "rows");
@@ -353,7 +344,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeAr
     const int64_t cap = a.max_pages * kTile;
     Run at = {run, 0, 0x7FFFFFFF, 0};                            // not cut: a whole sequence
     if (cut) {
-        at = find_run(a, run, runs_per_head(per_step));
+        at = find_run<WIN>(a, run, runs_per_head(per_step));
         if (at.left <= 0) return;
     } else if (a.lens[run] <= 0 || a.lens[run] > cap) {
         for (int i = tid; i < heads * D; i += 64 * kDecodeWaves)
@@ -385,14 +376,21 @@ next_sequence:
     const const_i32 *pages = (const const_i32 *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
     const int tile0 = __builtin_amdgcn_readfirstlane(at.skip) * kDecodeWaves + wave, tile1 = tile0 + kDecodeWaves;
     const int last_page = (int)a.max_pages - 1;
-    const int page1 = pages[tile0 < last_page ? tile0 : last_page];
-    int page2 = pages[tile1 < last_page ? tile1 : last_page];    // page of the tile after the next
+    int page1 = 0, page2 = 0;                                    // page2: of the tile after the next
+    if constexpr (!WIN) {
+        page1 = pages[tile0 < last_page ? tile0 : last_page];
+        page2 = pages[tile1 < last_page ? tile1 : last_page];
+    }
     const int64_t len = __builtin_amdgcn_readfirstlane(lens[b]);
-    const int all = (int)((len + kDecodeStep - 1) / kDecodeStep);      // steps of the sequence
+    const Tiles<WIN> walk(a, len);
+    if constexpr (WIN) {                                         // (which pages these are follows from the length)
+        page1 = pages[walk.tile(tile0 < walk.count ? tile0 : 0)];
+        page2 = pages[walk.tile(tile1 < walk.count ? tile1 : 0)];
+    }
+    const int all = walk.steps();                                // steps of the sequence
     const int mine = __builtin_amdgcn_readfirstlane(all - at.skip < at.left - done ? all - at.skip : at.left - done);
     const bool whole = mine == all;
-    const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane(at.skip) * kDecodeStep, end = len < t0 + (int64_t)mine * kDecodeStep ? len : t0 + (int64_t)mine * kDecodeStep;
-    const int tile_end = (int)((end + kTile - 1) / kTile);
+    const int upto = (__builtin_amdgcn_readfirstlane(at.skip) + mine) * kDecodeWaves, tile_end = walk.count < upto ? walk.count : upto;
 
     // copies of a tile: 16-byte pieces (a block of a token each), swizzled by token so that the reads below
     // take 64 banks
@@ -491,7 +489,7 @@ next_sequence:
         const bool more = tile + kDecodeWaves < tile_end;
         int64_t next = 0;
         if (more) next = row_of(page2);
-        if (tile + 2 * kDecodeWaves < tile_end) page2 = pages[tile + 2 * kDecodeWaves];
+        if (tile + 2 * kDecodeWaves < tile_end) page2 = pages[walk.tile(tile + 2 * kDecodeWaves)];
         __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): the tile has arrived
         asm volatile("" ::: "memory");
         uint32_t kc[4][NB];                                      // codes of the lane's tokens, 8 of each block
@@ -517,7 +515,10 @@ next_sequence:
             copy(a.cache.kq, a.cache.ks, next, kbuf, false);
             copy(a.cache.vq, a.cache.vs, next, vbuf, true);
         }
-        const int left = (int)(len - (int64_t)tile * kTile);     // tokens of the tile that count
+        const int64_t token0 = (int64_t)walk.tile(tile) * kTile;
+        const int left = (int)(len - token0 < kTile ? len - token0 : kTile);      // tokens of the tile that count
+        // (with a window: those from `low` on and those before `sink`)
+        const int low = WIN && walk.low > token0 ? (int)(walk.low - token0) : 0, sink = WIN && walk.sink_end > token0 ? (int)(walk.sink_end - token0 < kTile ? walk.sink_end - token0 : kTile) : 0;
         float s[4][HL], x[HL][2];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -536,10 +537,10 @@ next_sequence:
         for (int i = 0; i < HL; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) x[i][j] = add_halves(s[j][i], s[2 + j][i]);
-        if (left < kTile) {
+        if (left < kTile || (WIN && low > sink)) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (16 * (2 * (g >> 1) + j) + c >= left) {
+                if (16 * (2 * (g >> 1) + j) + c >= left || (WIN && 16 * (2 * (g >> 1) + j) + c < low && 16 * (2 * (g >> 1) + j) + c >= sink)) {
                     w[j] = hb{};
 #pragma unroll
                     for (int i = 0; i < HL; ++i) x[i][j] = -__builtin_inff();
@@ -649,6 +650,11 @@ next_sequence:
         }
         if (whole) {
             a.out[(int64_t)b * a.out_stride + head0 * D + i] = o / ll;
+            if (FORM == Form::sums && d == 0) {
+                float *sums = a.sums + ((int64_t)b * a.heads + head0 + hh) * 2;
+                sums[0] = mm;
+                sums[1] = ll;
+            }
         } else {
             float *p = partial<D>(a, blockIdx.x, done != 0, hh);
             p[d] = o;
@@ -764,8 +770,13 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream)
     const uint64_t H = a.cache.kv_heads, by = (((uint64_t)1 << (32 + shift)) + H - 1) / H;
     // one head: 2^32 does not fit, the quotient is the row
     const uint32_t by_heads = H == 1 ? 0 : (uint32_t)by;
-    if (a.cache.head_dim == 128) append_kernel<128><<<grid, 256, 0, stream>>>(a, by_heads, shift);
-    else append_kernel<64><<<grid, 256, 0, stream>>>(a, by_heads, shift);
+    if (a.slots) {
+        if (a.cache.head_dim == 128) append_kernel<128, true><<<grid, 256, 0, stream>>>(a, by_heads, shift);
+        else append_kernel<64, true><<<grid, 256, 0, stream>>>(a, by_heads, shift);
+    } else {
+        if (a.cache.head_dim == 128) append_kernel<128, false><<<grid, 256, 0, stream>>>(a, by_heads, shift);
+        else append_kernel<64, false><<<grid, 256, 0, stream>>>(a, by_heads, shift);
+    }
     return hipGetLastError();
 }
 
@@ -780,23 +791,31 @@ uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t hea
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
 {
     const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv), per_step = kv * groups;
-    const bool cut = cut_sequences(a.B, per_step, a.max_pages);
+    const bool cut = cut_sequences(a.B, per_step, seen_pages(a.max_pages, a.window, a.sinks));
     const unsigned grid = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : a.B));
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
     const float c_man = (float)(2.0 * c);
     const int per = (group + groups - 1) / groups;
     constexpr int T = 64 * kDecodeWaves;
-    if (a.cache.head_dim == 128) {
-        if (per <= 2) decode_kernel<128, 2, 2><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-        else if (per <= 4) decode_kernel<128, 4, 2><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-        else decode_kernel<128, 8, 2><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-    } else {
-        if (per <= 4) decode_kernel<64, 4, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-        else decode_kernel<64, 8, 3><<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1);
-    }
+    const auto start = [&](auto kernel) { kernel<<<grid, T, 0, stream>>>(a, groups, cut, c_man, c_exp - 1); };
+    const auto pick = [&](auto form) {
+        constexpr Form F = decltype(form)::value;
+        if (a.cache.head_dim == 128) {
+            if (per <= 2) start(decode_kernel<128, 2, 2, F>);
+            else if (per <= 4) start(decode_kernel<128, 4, 2, F>);
+            else start(decode_kernel<128, 8, 2, F>);
+        } else {
+            if (per <= 4) start(decode_kernel<64, 4, 3, F>);
+            else start(decode_kernel<64, 8, 3, F>);
+        }
+    };
+    // (a window as long as the table hides nothing)
+    if (a.window > 0 && a.window < a.max_pages * kTile) pick(std::integral_constant<Form, Form::window>{});
+    else if (a.sums) pick(std::integral_constant<Form, Form::sums>{});
+    else pick(std::integral_constant<Form, Form::plain>{});
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !cut) return e;
+    if (e != hipSuccess || !cut || a.sums) return e;             // (with sums, the caller joins)
     const unsigned jobs = (unsigned)(a.B * a.heads);
     if (a.cache.head_dim == 128) join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, groups);
     else join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, groups);

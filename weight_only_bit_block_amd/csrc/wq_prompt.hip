@@ -1,7 +1,8 @@
 // wq_prompt.hip -- causal attention over packed prompts (fp32, grouped heads).
 //
 //   out[t, j] = sum_u p_u v[u] / sum_u p_u,  p_u = exp(scale <q, k_u> - max),
-//   u <= t in t's own sequence.
+//   u <= t in t's own sequence; with a window also u > t - window, or u among the
+//   sequence's first `sinks` tokens.
 //
 // fp32 products on the fp16 matrix cores: every operand is normalised by a
 // power of two and split into two binary16 parts, x = x1 + x2 (22 bits), and a
@@ -353,13 +354,61 @@ __device__ __forceinline__ f16v scores(const h8 *q, const h8 (&k)[D / 8])
     return x;
 }
 
+// What this lane's query sees of a tile's keys: key u of it is `first` + u tokens
+// behind the query (all of them where not `edge`). With a window, the last
+// `window` keys up to the query itself, and the tile's first `sink` ones.
+template <bool WIN>
+struct Sight {
+    bool edge;
+    int first, window, sink;
+    // From a key `by` further on.
+    __device__ __forceinline__ Sight from(int by) const { return {edge, first + by, window, sink - by}; }
+    __device__ __forceinline__ bool hides(int u) const
+    {
+        if constexpr (WIN) return first + u > 0 || (first + u <= -window && u >= sink);
+        return first + u > 0;
+    }
+    // No key at all: a tile that other rows of the wavefront see.
+    __device__ __forceinline__ bool none() const
+    {
+        if constexpr (!WIN) return false;
+        const int newest = first + kTileKeys - 1 < 0 ? first + kTileKeys - 1 : 0;
+        return first > 0 || (newest <= -window && sink <= 0);
+    }
+};
+
+// The tiles a block of rows walks, and the place of its v-th: with a window the
+// first tokens' tiles and those from the first row's oldest key on.
+template <bool WIN>
+struct Walk {
+    int sinks, skip, last;                       // tiles of first tokens, tiles left out behind them, number of the last one
+    __device__ __forceinline__ Walk(const PromptArgs &a, int row0, int last_tile) : sinks(0), skip(0), last(last_tile)
+    {
+        if constexpr (WIN) {
+            const int from = (row0 >= a.window ? row0 - a.window + 1 : 0) / kTileKeys;
+            sinks = (a.sinks + kTileKeys - 1) / kTileKeys;
+            sinks = sinks < from ? sinks : from;
+            skip = from - sinks;
+            last -= skip;
+        }
+    }
+    __device__ __forceinline__ int tile(int v) const { return WIN && v >= sinks ? v + skip : v; }
+    // Sight of tile t from the lane's query at `pos`, one of the 32 rows from row0 on, whose last tile is t if `own`.
+    __device__ __forceinline__ Sight<WIN> sight(const PromptArgs &a, int t, bool own, int row0, int pos) const
+    {
+        const int key = t * kTileKeys;
+        if constexpr (WIN)
+            return {own || (key <= row0 + 31 - a.window && key + kTileKeys > a.sinks), key - pos, a.window, a.sinks - key};
+        return {own, key - pos, 0, 0};
+    }
+};
+
 // A tile's scores made ready: rows of wild k scaled, keys this query does not
-// see masked (where `edge`; `first`: position of the tile's first key minus
-// that of this lane's query), the running maximum and the units of the output
-// moved where they have to be. Leaves in s.f and s.up what turns a score into a
-// weight.
-template <int D>
-__device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const TileMeta *meta, bool edge, int first, int half)
+// see masked, the running maximum and the units of the output moved where they
+// have to be (a tile of which a query sees nothing leaves its units alone).
+// Leaves in s.f and s.up what turns a score into a weight.
+template <int D, bool WIN>
+__device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const TileMeta *meta, const Sight<WIN> &see, int half)
 {
     const int flags = h.flags;
     int e = s.q_exp - h.k_exp, ve = h.v_exp;
@@ -368,10 +417,12 @@ __device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const Ti
         for (int i = 0; i < 16; ++i) x[i] = ldexpf(x[i], s.q_exp - meta->k_row[8 * (i >> 2) + 4 * half + (i & 3)]);
         e = 0;
     }
-    if (edge) {
+    const Sight<WIN> mine = see.from(4 * half);  // of this half's keys
+    if (see.edge) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (first + 8 * (i >> 2) + 4 * half + (i & 3) > 0) x[i] = -__builtin_inff();
+            if (mine.hides(8 * (i >> 2) + (i & 3))) x[i] = -__builtin_inff();
+        if (see.none()) ve = kNoExp;
     }
     // (never 0: times a masked key's -inf that is no number. Products are below 2^38, so such scores are as good as equal)
     const float f = ldexpf(1.0f, e > 127 ? 127 : e < -126 ? -126 : e);
@@ -383,8 +434,8 @@ __device__ __forceinline__ void settle(Rows<D> &s, f16v &x, TileHead h, const Ti
         ve = kNoExp;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int u = 8 * (i >> 2) + 4 * half + (i & 3), r = meta->v_row[u];
-            if (!(edge && first + u > 0) && r > ve) ve = r;
+            const int u = 8 * (i >> 2) + (i & 3), r = meta->v_row[u + 4 * half];
+            if (!(see.edge && mine.hides(u)) && r > ve) ve = r;
         }
         const int o = __shfl_xor(ve, 32);
         ve = ve > o ? ve : o;
@@ -478,17 +529,18 @@ __device__ __forceinline__ void weigh_rows(const Rows<D> &s, f16v &x, const Tile
 
 // Values that are not finite (0 in the operands): counts, for each output, the
 // visible ones as a product of two masks.
-template <int D>
-__device__ __forceinline__ void odd_values(Rows<D> &s, bool edge, int first, const float *v_rows, int64_t v_stride,
+template <int D, bool WIN>
+__device__ __forceinline__ void odd_values(Rows<D> &s, const Sight<WIN> &see, const float *v_rows, int64_t v_stride,
                                            int live_keys, int lane)
 {
     const int half = lane >> 5;
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
+        const Sight<WIN> mine = see.from(16 * t + 4 * half);
         h8 seen;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            seen[e] = !edge || first + 16 * t + 8 * (e >> 2) + 4 * half + (e & 3) <= 0 ? (_Float16)1.0f : (_Float16)0.0f;
+            seen[e] = see.edge && mine.hides(8 * (e >> 2) + (e & 3)) ? (_Float16)0.0f : (_Float16)1.0f;
 #pragma unroll
         for (int db = 0; db < D / 32; ++db) {
             h8 odd;
@@ -523,7 +575,7 @@ __device__ __forceinline__ void store_rows(const Rows<D> &s, float *out, int hal
 
 // W wavefronts of consecutive 32-row blocks of one query head share the tiles
 // through a double buffer in LDS, filled by direct-to-LDS copies one tile ahead.
-template <int D, int W>
+template <int D, int W, bool WIN>
 __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _Float16 *__restrict__ tiles,
                                                           const TileMeta *__restrict__ metas, float c_man, int c_exp,
                                                           int slots)
@@ -551,14 +603,16 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
 #pragma unroll
         for (int f = 0; f < D / 16; ++f) split_query(x[f], e, c_man, q.q1[f], q.q2[f]);
     }
-    // last tile of the block
-    const int last = __builtin_amdgcn_readfirstlane((len - 1 < row0 + kRows - 1 ? len - 1 : row0 + kRows - 1) / kTileKeys);
+    // the block's tiles, to that of its last row
+    const Walk<WIN> walk(a, __builtin_amdgcn_readfirstlane(row0),
+                         __builtin_amdgcn_readfirstlane((len - 1 < row0 + kRows - 1 ? len - 1 : row0 + kRows - 1) / kTileKeys));
+    const int last = walk.last;
     const int step = a.kv_heads, at0 = __builtin_amdgcn_readfirstlane(first_slot(r.begin, b, kTileKeys) * step + kvh);
     // k of tile t is wanted one step before v of tile t: two buffers of each, t & 1
-    auto copy = [&](int tile, int values) {
-        const char *src = reinterpret_cast<const char *>(tiles + (int64_t)(at0 + tile * step) * tile_halves(D)) + values * (kBytes / 2) +
+    auto copy = [&](int t, int values) {
+        const char *src = reinterpret_cast<const char *>(tiles + (int64_t)(at0 + walk.tile(t) * step) * tile_halves(D)) + values * (kBytes / 2) +
                           wave * 1024 + lane * 16;
-        char *dst = reinterpret_cast<char *>(buf[tile & 1]) + values * (kBytes / 2) + wave * 1024;
+        char *dst = reinterpret_cast<char *>(buf[t & 1]) + values * (kBytes / 2) + wave * 1024;
 #pragma unroll
         for (int i = 0; i < kBytes / 2048 / W; ++i)
             __builtin_amdgcn_global_load_lds(
@@ -571,25 +625,27 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    const int mine = wrow < len ? wrow / kTileKeys : -1;         // this wave's last tile
+    const int mine = wrow < len ? wrow / kTileKeys - walk.skip : -1;      // this wave's last tile
+    const auto meta_of = [&](int t) __attribute__((always_inline)) { return metas + at0 + walk.tile(t) * step; };
+    const auto sight = [&](int t) __attribute__((always_inline)) { return walk.sight(a, walk.tile(t), t == mine, wrow, pos); };
     int odd = 0;
     copy(0, 0);
-    TileHead now = head_of(metas + at0), next = head_of(metas + at0 + (last > 0 ? step : 0));
+    TileHead now = head_of(meta_of(0)), next = head_of(meta_of(last > 0 ? 1 : 0));
     meet();
     copy(0, 1);
     if (last > 0) copy(1, 0);
     f16v x = {};
     if (mine >= 0) {
         x = scores<D>(q, reinterpret_cast<const h8 *>(buf[0]) + lane);
-        settle<D>(s, x, now, metas + at0, mine == 0, -pos, half);
+        settle<D>(s, x, now, meta_of(0), sight(0), half);
     }
     for (int t = 0; t <= last; ++t) {
-        const TileHead after = head_of(metas + at0 + (t + 2 <= last ? t + 2 : last) * step);
+        const TileHead after = head_of(meta_of(t + 2 <= last ? t + 2 : last));
         meet();                                  // v of tile t and k of tile t + 1
         if (t < last) copy(t + 1, 1);
         if (t + 1 < last) copy(t + 2, 0);
         if (t <= mine) {
-            const TileMeta *meta = metas + at0 + t * step;
+            const TileMeta *meta = meta_of(t);
             const int flags = now.flags;
             const h8 *v1 = reinterpret_cast<const h8 *>(buf[t & 1]) + 2 * D * kTileKeys / 8 + lane;
             const h8 *k1 = reinterpret_cast<const h8 *>(buf[(t + 1) & 1]) + lane;
@@ -622,7 +678,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
             odd |= flags & kOddV;
             if (t < mine) {
                 x = y;
-                settle<D>(s, x, next, meta + step, t + 1 == mine, (t + 1) * kTileKeys - pos, half);
+                settle<D>(s, x, next, meta_of(t + 1), sight(t + 1), half);
             }
         }
         now = next;
@@ -630,10 +686,10 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
     }
     if (odd)                                     // (apart from the loop, whose registers it would take)
         for (int t = 0; t <= mine; ++t)
-            if (metas[at0 + t * step].v_flags & kOddV)
-                odd_values<D>(s, t == mine, t * kTileKeys - pos,
-                              a.v + (int64_t)(r.begin + t * kTileKeys) * a.v_stride + kvh * D, a.v_stride,
-                              len - t * kTileKeys, lane);
+            if (meta_of(t)->v_flags & kOddV) {
+                const int key = walk.tile(t) * kTileKeys;
+                odd_values<D>(s, sight(t), a.v + (int64_t)(r.begin + key) * a.v_stride + kvh * D, a.v_stride, len - key, lane);
+            }
     if (wrow < len)
         store_rows<D>(s, live ? a.out + (int64_t)(r.begin + pos) * a.out_stride + head * D : nullptr, half);
 }
@@ -732,7 +788,7 @@ __device__ __forceinline__ void join_rows(const PromptArgs &a, const Block &x, c
 }
 
 // Prepared k and v come from L2 straight into registers, a tile ahead.
-template <int D>
+template <int D, bool WIN>
 __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArgs a, const _Float16 *__restrict__ tiles,
                                                                       const TileMeta *__restrict__ metas, float c_man,
                                                                       int c_exp, int slots)
@@ -742,16 +798,19 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
     __shared__ RowSums sh;
     const Block x = find_block(a, slots);
     if (x.row0 < 0 || x.row0 >= x.len) return;
-    const int lane = threadIdx.x & 63, half = lane >> 5, last = x.last;
+    const Walk<WIN> walk(a, x.row0, x.last);
+    const int lane = threadIdx.x & 63, half = lane >> 5, last = walk.last;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int pos = x.row0 + (lane & 31);
+    const auto sight = [&](int t) __attribute__((always_inline)) { return walk.sight(a, walk.tile(t), t == last, x.row0, pos); };
     const int step = a.kv_heads, at0 = __builtin_amdgcn_readfirstlane(first_slot(x.r.begin, x.b, kTileKeys) * step + x.kvh);
-    auto load = [&](int tile, int values, h8 (&y)[F]) {
-        const h8 *src = reinterpret_cast<const h8 *>(tiles + (int64_t)(at0 + tile * step) * tile_halves(D)) + values * (2 * D * kTileKeys / 8);
+    const auto meta_of = [&](int t) __attribute__((always_inline)) { return metas + at0 + walk.tile(t) * step; };
+    auto load = [&](int t, int values, h8 (&y)[F]) {
+        const h8 *src = reinterpret_cast<const h8 *>(tiles + (int64_t)(at0 + walk.tile(t) * step) * tile_halves(D)) + values * (2 * D * kTileKeys / 8);
 #pragma unroll
         for (int f = 0; f < F; ++f) y[f] = (src + 64 * f)[lane];
     };
-    const auto head_at = [&](int t) { return head_of(metas + at0 + (t <= last ? t : last) * step); };
+    const auto head_at = [&](int t) { return head_of(meta_of(t <= last ? t : last)); };
     h8 k[F], v[F];
     TileHead now = head_at(wave);
     int odd = 0;
@@ -762,10 +821,8 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
     if (wave <= last) load(wave, 1, v);
     __syncthreads();
     for (int t = wave; t <= last; t += kShare) {
-        const TileMeta *meta = metas + at0 + t * step;
+        const TileMeta *meta = meta_of(t);
         const TileHead next = head_at(t + kShare);
-        const bool edge = t == last;
-        const int first = t * kTileKeys - pos;
         __builtin_amdgcn_sched_barrier(0);
         f16v y = scores<D>(qs, k);
         // two reads of queries ahead, not all of them: registers are what is short
@@ -777,7 +834,7 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
         }
         __builtin_amdgcn_sched_barrier(0);       // (moved up, the loads would need registers of their own)
         if (t + kShare <= last) load(t + kShare, 0, k);
-        settle<D>(s, y, now, meta, edge, first, half);
+        settle<D>(s, y, now, meta, sight(t), half);
         weigh<D>(s, y);
         if (now.flags & kWildV) weigh_rows<D>(s, y, meta, half);
         accumulate_held<D>(s, v, y);
@@ -788,10 +845,10 @@ __global__ __launch_bounds__(64 * kShare, 2) void attend_shared_kernel(PromptArg
     }
     if (odd)                                     // (apart from the loop, whose registers it would take)
         for (int t = wave; t <= last; t += kShare)
-            if (metas[at0 + t * step].v_flags & kOddV)
-                odd_values<D>(s, t == last, t * kTileKeys - pos,
-                              a.v + (int64_t)(x.r.begin + t * kTileKeys) * a.v_stride + x.kvh * D, a.v_stride,
-                              x.len - t * kTileKeys, lane);
+            if (meta_of(t)->v_flags & kOddV) {
+                const int key = walk.tile(t) * kTileKeys;
+                odd_values<D>(s, sight(t), a.v + (int64_t)(x.r.begin + key) * a.v_stride + x.kvh * D, a.v_stride, x.len - key, lane);
+            }
     join_rows<D>(a, x, s, res, sh, lane, wave);
 }
 
@@ -867,7 +924,7 @@ __device__ __forceinline__ Factors factors(float top)
     return f;
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArgs a, float c_man, int c_exp, int slots)
 {
     constexpr int C = D / 4, kTileFloats = kTileKeys * D;        // pieces of a row
@@ -878,9 +935,11 @@ __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArg
     __shared__ TileMeta metas[kShare];
     const Block x = find_block(a, slots);
     if (x.row0 < 0 || x.row0 >= x.len) return;
-    const int lane = threadIdx.x & 63, half = lane >> 5, last = x.last;
+    const Walk<WIN> walk(a, x.row0, x.last);
+    const int lane = threadIdx.x & 63, half = lane >> 5, last = walk.last;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int pos = x.row0 + (lane & 31);
+    const auto sight = [&](int t) __attribute__((always_inline)) { return walk.sight(a, walk.tile(t), t == last, x.row0, pos); };
     TileMeta *const meta = &metas[wave];
     const float *const ks = a.k + (int64_t)x.r.begin * a.k_stride + x.kvh * D, *const vs = a.v + (int64_t)x.r.begin * a.v_stride + x.kvh * D;
     // (keys past the end: the last one's values, whose weights are 0)
@@ -894,9 +953,9 @@ __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArg
             at += 64 / C * stride;
         }
     };
-    auto load = [&](int tile) {
-        copy(ks, a.k_stride, tile, buf[wave][0]);
-        copy(vs, a.v_stride, tile, buf[wave][1]);
+    auto load = [&](int t) {
+        copy(ks, a.k_stride, walk.tile(t), buf[wave][0]);
+        copy(vs, a.v_stride, walk.tile(t), buf[wave][1]);
     };
     // half of row lane % 32, 8 values in turns
     auto read_row = [&](const float *src, float (&y)[D / 16][8]) {
@@ -926,8 +985,6 @@ __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArg
                      [&]() { if (wave <= last) load(wave); });
     __syncthreads();
     for (int t = wave; t <= last; t += kShare) {
-        const bool edge = t == last;
-        const int first = t * kTileKeys - pos;
         __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): the tile has arrived
         asm volatile("" ::: "memory");
         float x8[D / 16][8];                     // k's rows, then v's
@@ -974,7 +1031,7 @@ __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArg
         }
         asm volatile("" ::: "memory");
         const TileHead now = {fk.tile, fv.zero ? kNoExp : -fv.tile, (fk.wild ? kWildK : 0) | (fv.wild ? kWildV : 0)};
-        settle<D>(s, y, now, meta, edge, first, half);
+        settle<D>(s, y, now, meta, sight(t), half);
         weigh<D>(s, y);
         if (now.flags & kWildV) weigh_rows<D>(s, y, meta, half);
 #pragma unroll
@@ -999,9 +1056,10 @@ __global__ __launch_bounds__(64 * kShare, 1) void attend_direct_kernel(PromptArg
         }
     }
     if (any_odd)
-        for (int t = wave; t <= last; t += kShare)
-            odd_values<D>(s, t == last, t * kTileKeys - pos, vs + (int64_t)(t * kTileKeys) * a.v_stride, a.v_stride,
-                          x.len - t * kTileKeys, lane);
+        for (int t = wave; t <= last; t += kShare) {
+            const int key = walk.tile(t) * kTileKeys;
+            odd_values<D>(s, sight(t), vs + (int64_t)key * a.v_stride, a.v_stride, x.len - key, lane);
+        }
     join_rows<D>(a, x, s, buf[0][0], sh, lane, wave);
 }
 
@@ -1034,7 +1092,7 @@ inline bool direct(int64_t T, int64_t B, int64_t heads, int64_t head_dim)
     return T * head_dim <= 16384 && tile_slots(T, B, 32) * heads * head_dim <= 40960;
 }
 
-template <int D>
+template <int D, bool WIN>
 hipError_t launch(const PromptArgs &a, hipStream_t stream)
 {
     constexpr int W = 4;
@@ -1042,7 +1100,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
     const int64_t slots = tile_slots(a.T, a.B, kTileKeys);
     if (direct(a.T, a.B, a.heads, D)) {
-        attend_direct_kernel<D><<<(unsigned)(slots * a.heads), 64 * kShare, 0, stream>>>(a, (float)(2.0 * c), c_exp - 1, (int)slots);
+        attend_direct_kernel<D, WIN><<<(unsigned)(slots * a.heads), 64 * kShare, 0, stream>>>(a, (float)(2.0 * c), c_exp - 1, (int)slots);
         return hipGetLastError();
     }
     TileMeta *metas = reinterpret_cast<TileMeta *>(a.ws);
@@ -1053,11 +1111,11 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     const int64_t rows = tile_slots(a.T, a.B, 32 * W);
     if (rows * a.heads <= few_groups(D, a.B)) {
         const int64_t blocks = tile_slots(a.T, a.B, 32);
-        attend_shared_kernel<D><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c),
-                                                                                          c_exp - 1, (int)blocks);
+        attend_shared_kernel<D, WIN><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c),
+                                                                                               c_exp - 1, (int)blocks);
         return hipGetLastError();
     }
-    attend_kernel<D, W><<<(unsigned)(rows * a.heads), 64 * W, 0, stream>>>(a, tiles, metas, (float)(2.0 * c), c_exp - 1, (int)rows);
+    attend_kernel<D, W, WIN><<<(unsigned)(rows * a.heads), 64 * W, 0, stream>>>(a, tiles, metas, (float)(2.0 * c), c_exp - 1, (int)rows);
     return hipGetLastError();
 }
 
@@ -1072,7 +1130,9 @@ uint64_t prompt_ws_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, 
 
 hipError_t launch_attn_prefill(const PromptArgs &a, hipStream_t stream)
 {
-    return a.head_dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+    // (a window as long as the prompts hides nothing)
+    if (a.window > 0 && a.window < a.T) return a.head_dim == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
+    return a.head_dim == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
 }
 
 }  // namespace wq

@@ -1,0 +1,527 @@
+// wq_shared.hip -- attention of single tokens whose sequences share a prefix in
+// the int4 cache: the prefix is read once for all of them.
+//
+//   out[b, j] = sum_u p_u v_u,  softmax over the prefix's tokens and b's own
+//
+// Three steps: the sequences' own tokens (wq_kv.hip), the prefix, and the join of
+// both. This file holds the second, shared_kernel, and the third.
+//
+// For one key/value head the prefix meets R = B * group query rows, so that its
+// scores are a matrix product of R x L x D: bound by the matrix cores and the
+// softmax's vector instructions once R passes 32 or so, by HBM below.
+//   A workgroup takes 32 RW rows and a run of pages, and joins with the others
+// through the workspace. A page's 64 keys are two tiles of 32, one for each half
+// of the workgroup's 2 RW wavefronts, which meet at the end in LDS. All threads
+// turn the page's codes into operands in LDS, once for all rows:
+//   k   the codes themselves, exact in binary16. q is split in two parts (22
+//       bits) after a power of two, so a block's sum is two products; it is scaled
+//       in fp32, one multiplication a key and block: exact for every scale.
+//   v   code times scale (15 bits) in two binary16 parts that hold it exactly:
+//       hi = c s rounded, lo = fma(c, s, -hi), packed instructions. The scales are
+//       brought below 2^kScaleTop by the power of two of the largest seen, v_exp.
+// Scores come out transposed, S' = K Q' (a lane holds one query and 16 of the 32
+// keys), so the softmax runs within a lane but for one exchange between the
+// halves, and the weights, split in two parts, are already the second operand of
+// O' = V' P', three products. v lies in LDS by rows; ds_read_b64_tr_b16 turns it.
+#include "wq_internal.h"
+#include "wq_device.h"
+#include "wq_kv_decode.h"
+
+#include <math.h>
+
+namespace wq {
+namespace {
+
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kKeys = 32;                    // of a wavefront's tile; a page has two
+constexpr float kBig = 3.4028235e38f;
+constexpr int kWeightBits = 12;              // a weight of 1 is 2^12 as a binary16 operand
+constexpr float kSlack = 3.0f;               // log2 a score may pass the running maximum by before rescaling
+constexpr int kScaleTop = 12;                // |code| <= 8: values stay below 2^15
+constexpr int kMinScaleExp = -24;            // 2^-24 is binary16's smallest
+constexpr uint32_t kRankZero = 0x800;
+
+__device__ __forceinline__ f16v mfma(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// 8 codes of a dword as exact binary16 values, in the order of nibbles 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
+__device__ __forceinline__ h8 codes8(uint32_t x)
+{
+    const h2 off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+    const h2 off16 = {(_Float16)-72.0f, (_Float16)-72.0f}, inv16 = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const uint32_t y = x >> 8;
+    const h2 a = __builtin_bit_cast(h2, (x & 0x000F000Fu) ^ 0x64086408u) + off;
+    const h2 b = __builtin_elementwise_fma(__builtin_bit_cast(h2, (x & 0x00F000F0u) ^ 0x64806480u), inv16, off16);
+    const h2 c = __builtin_bit_cast(h2, (y & 0x000F000Fu) ^ 0x64086408u) + off;
+    const h2 d = __builtin_elementwise_fma(__builtin_bit_cast(h2, (y & 0x00F000F0u) ^ 0x64806480u), inv16, off16);
+    return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// x = hi + lo to 22 bits; x is made opaque so that the hi subtracted is the hi kept.
+__device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo)
+{
+    asm("" : "+v"(x));
+    hi = (_Float16)x;
+    lo = (_Float16)(x - (float)hi);
+}
+
+// The run of pages of a workgroup, from the prefix's length, which is on the device.
+struct PrefixRuns {
+    int64_t len;
+    int pages, per, count;                   // pages in all, of a run, runs
+    bool bad;
+};
+__device__ __forceinline__ PrefixRuns prefix_runs(const SharedArgs &a, int chunks)
+{
+    PrefixRuns r;
+    r.len = *a.prefix_len;
+    r.bad = r.len < 0 || r.len > a.prefix_pages * kTile;
+    if (r.bad) r.len = 0;
+    r.pages = (int)((r.len + kTile - 1) / kTile);
+    r.per = chunks > 0 ? (r.pages + chunks - 1) / chunks : 0;
+    r.count = r.per > 0 ? (r.pages + r.per - 1) / r.per : 0;
+    return r;
+}
+
+// Where a run's result for a row of a key/value head is: D values, then maximum and sum.
+__device__ __forceinline__ float *shared_part(float *parts, int64_t run, int kv_heads, int kh, int64_t rows, int64_t row, int D)
+{
+    return parts + ((run * kv_heads + kh) * rows + row) * (D + kPartialExtra);
+}
+
+// Place of 16 bytes (8 values, `piece` of the row's D / 8) of a key's v in LDS, in
+// bytes: written by 16 keys at once and read by 4 keys and 4 pieces, on different banks.
+template <int D>
+__device__ __forceinline__ int v_at(int key, int piece)
+{
+    if constexpr (D == 128) return key * 256 + (piece ^ ((key & 3) * 4 + (key >> 2 & 3))) * 16;
+    return key * 128 + (piece ^ ((key >> 1 & 1) * 4 + (key >> 2 & 3))) * 16;
+}
+
+template <int D, int RW>
+__global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp)
+{
+    constexpr int NB = D / 32, F = D / 16, NT = 128 * RW;
+    constexpr int kChunks = kTile * D / 16, kMine = kChunks < NT ? 1 : kChunks / NT;      // 8-byte pieces of a page's k or v; of a thread
+    constexpr int kRowBytes = D * 2;
+    constexpr int kOperands = 3 * kTile * kRowBytes + NB * kTile * 2, kResult = 32 * RW * (D + kPartialExtra) * 4;
+    typedef _Float16 hb __attribute__((ext_vector_type(NB)));
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kOperands > kResult ? kOperands : kResult];
+    uint8_t *const kb = lds, *const vb = lds + kTile * kRowBytes;                         // v: high parts, low parts
+    _Float16 *const ksb = reinterpret_cast<_Float16 *>(lds + 3 * kTile * kRowBytes);      // k's scales, [block][key]
+    const DecodeArgs &own = a.own;
+    const int kv = own.cache.kv_heads, group = own.heads / kv;
+    const int64_t rows = (int64_t)own.B * group;
+    // key/value heads next to each other: ids go round the 8 XCDs
+    const int kh = blockIdx.x % kv, run = blockIdx.x / kv % chunks;
+    const int64_t block = blockIdx.x / kv / chunks;
+    const PrefixRuns runs = prefix_runs(a, chunks);
+    if (run >= runs.count) return;
+    const int page0 = run * runs.per, page_end = page0 + runs.per < runs.pages ? page0 + runs.per : runs.pages;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), rw = wave % RW, kw = wave / RW;
+    const int64_t row = (block * RW + rw) * 32 + (lane & 31);
+    const bool live = row < rows;
+
+    // ---- pages come into registers one ahead: codes of this thread's pieces, scales of the lane's key
+    u2 kc[kMine], vc[kMine];
+    hb ks, vs;
+    bool bad = false;
+    const auto fetch = [&](int page) __attribute__((always_inline)) {
+        int id = __builtin_amdgcn_readfirstlane(a.prefix[page]);
+        if (id < 0 || id >= own.cache.n_pages) {
+            bad = true;
+            id = 0;
+        }
+        if (own.cache.n_pages <= 0) return;
+        const int64_t at = ((int64_t)id * kv + kh) * kTile;
+        const uint8_t *kq = reinterpret_cast<const uint8_t *>(own.cache.kq) + at * (D / 2), *vq = reinterpret_cast<const uint8_t *>(own.cache.vq) + at * (D / 2);
+        if (kChunks >= NT || wave * 64 < kChunks) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int o = lane * (D / 2) + (wave + i * 2 * RW) * 8;
+                kc[i] = *reinterpret_cast<const u2 *>(kq + o);
+                vc[i] = *reinterpret_cast<const u2 *>(vq + o);
+            }
+        }
+        ks = *reinterpret_cast<const hb *>(own.cache.ks + (at + lane) * NB);
+        vs = *reinterpret_cast<const hb *>(own.cache.vs + (at + lane) * NB);
+    };
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) kc[i] = vc[i] = u2{0, 0};
+    ks = vs = hb{};
+    fetch(page0);
+
+    // ---- the query: values 16 f + 8 half + nibble_of(e) of the lane's row
+    h8 q1[F], q2[F];
+    float f;                                 // scores in powers of two = sums times this
+    {
+        const float *src = own.q + (live ? row / group : 0) * own.q_stride + (kh * group + (live ? (int)(row % group) : 0)) * D + 8 * half;
+        float x[F][8], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f4 y = *reinterpret_cast<const f4 *>(src + 16 * i + 4 * j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[i][4 * j + e] = y[e];
+                    const float m = fabsf(y[e]);
+                    if (m <= kBig) top = fmaxf(top, m);
+                }
+            }
+        top = fmaxf(top, other_half(top));
+        const int e2 = top > 0.0f ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
+        // (never 0: times a masked key's -inf that is no number. Sums are below 2^42, so such scores are as good as equal)
+        f = ldexpf(1.0f, c_exp - e2 > 127 ? 127 : c_exp - e2 < -126 ? -126 : c_exp - e2);
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                _Float16 hi, lo;
+                split(ldexpf(x[i][nibble_of(e)], e2) * c_man, hi, lo);
+                q1[i][e] = hi;
+                q2[i][e] = lo;
+            }
+    }
+
+    f16v o[NB];                              // value positions 32 n + 8 (i / 4) + 4 half + i % 4
+#pragma unroll
+    for (int n = 0; n < NB; ++n) o[n] = f16v{};
+    float m = -3.0e38f, l = 0.0f;
+    int v_exp = kMinScaleExp;
+    uint32_t v_limit = kRankZero + 2;        // rank of 2^v_exp
+
+    for (int page = page0; page < page_end; ++page) {
+        const int left = (int)(runs.len - (int64_t)page * kTile < kTile ? runs.len - (int64_t)page * kTile : kTile);
+        // ---- units of v: magnitudes of the lane's scales in their order, what is not finite below zero
+        if (lane >= left) vs = hb{};
+        typedef uint16_t ub __attribute__((ext_vector_type(NB)));
+        const ub rank = __builtin_bit_cast(ub, vs) * (uint16_t)2 + (uint16_t)kRankZero;
+        uint16_t top = rank[0];
+#pragma unroll
+        for (int i = 1; i < NB; ++i) top = top > rank[i] ? top : rank[i];
+        if (__any(top > v_limit)) {          // (the same in every wavefront)
+            float vmax = top > kRankZero ? (float)__builtin_bit_cast(_Float16, (uint16_t)((top - kRankZero) >> 1)) : 0.0f;
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, s));
+            const int e = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
+            const float by = ldexpf(1.0f, v_exp - e);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[n][i] *= by;
+            v_exp = e;
+            v_limit = kRankZero + 2 * (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(1.0f, e));
+        }
+        // ---- operands
+        if (page != page0) __syncthreads();  // those of the page before have been read
+        if (kChunks >= NT || wave * 64 < kChunks) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int piece = wave + i * 2 * RW, b = piece >> 1;                      // 16 values, half a block
+                _Float16 sk = ks[0], sv = vs[0];
+#pragma unroll
+                for (int n = 1; n < NB; ++n)
+                    if (b == n) {
+                        sk = ks[n];
+                        sv = vs[n];
+                    }
+                const _Float16 sn = (_Float16)ldexpf((float)sv, kScaleTop - v_exp);
+                const h8 s = {sn, sn, sn, sn, sn, sn, sn, sn};
+                if ((piece & 1) == 0) ksb[b * kTile + lane] = sk;
+                // k: fragment `piece` of the key's tile, lane (key, half)
+                h8 *kd = reinterpret_cast<h8 *>(kb) + (lane >> 5) * (F * 64) + piece * 64 + (lane & 31);
+                kd[0] = codes8(kc[i].x);
+                kd[32] = codes8(kc[i].y);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const h8 c = codes8(vc[i][j]);
+                    h8 hi = c * s;
+                    asm("" : "+v"(hi));
+                    const h8 lo = __builtin_elementwise_fma(c, s, -hi);
+                    const int at = v_at<D>(lane, 2 * piece + j);
+                    *reinterpret_cast<h8 *>(vb + at) = hi;
+                    *reinterpret_cast<h8 *>(vb + kTile * kRowBytes + at) = lo;
+                }
+            }
+        }
+        if (page + 1 < page_end) fetch(page + 1);
+        lds_barrier();
+        // ---- scores of the wavefront's 32 keys
+        const h8 *kf = reinterpret_cast<const h8 *>(kb) + kw * (F * 64) + lane;
+        f16v x = {};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            f16v z = {};
+#pragma unroll
+            for (int i = 2 * b; i < 2 * b + 2; ++i) {
+                z = mfma(kf[64 * i], q2[i], z);
+                z = mfma(kf[64 * i], q1[i], z);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const h4 s = *reinterpret_cast<const h4 *>(ksb + b * kTile + kw * kKeys + 8 * g + 4 * half);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * g + i] = fmaf(z[4 * g + i], (float)s[i], x[4 * g + i]);
+            }
+        }
+        if (left < kTile) {
+            const int end = left - kw * kKeys - 4 * half;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (8 * (i >> 2) + (i & 3) >= end) x[i] = -__builtin_inff();
+        }
+        float high = fmaxf(x[0], x[1]);
+#pragma unroll
+        for (int i = 2; i < 16; ++i) high = fmaxf(high, x[i]);
+        high = fmaxf(high, other_half(high)) * f;
+        if (__any(high > m + kSlack)) {
+            const float mn = fmaxf(m, high), by = __builtin_amdgcn_exp2f(m - mn);
+            l *= by;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[n][i] *= by;
+            m = mn;
+        }
+        const float up = (float)kWeightBits - m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], f, up));
+            sum += x[i];
+        }
+        l += sum;
+        // ---- output: 16 keys at a time; a lane reads 4 keys of 16 values and gets its value of them
+        const int c = lane & 15;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            h8 p1, p2;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                _Float16 hi, lo;
+                split(x[8 * t + i], hi, lo);
+                p1[i] = hi;
+                p2[i] = lo;
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                h8 v[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    h4 r[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = kw * kKeys + 16 * t + 8 * e + 4 * half + (c >> 2), d = 32 * n + (lane & 16) + 4 * (c & 3);
+                        r[e] = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)(
+                            vb + w * kTile * kRowBytes + v_at<D>(key, d >> 3) + (d & 7) * 2)));
+                    }
+                    v[w] = __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+                o[n] = mfma(v[1], p1, o[n]);
+                o[n] = mfma(v[0], p2, o[n]);
+                o[n] = mfma(v[0], p1, o[n]);
+            }
+        }
+    }
+
+    // ---- the two halves of the keys meet in LDS; row position j of a block is value (j & ~7) + nibble_of(j & 7)
+    l += other_half(l);
+    constexpr int kPitch = D + kPartialExtra;
+    float *res = reinterpret_cast<float *>(lds) + (rw * 32 + (lane & 31)) * kPitch;
+    const auto place = [&](int n, int g, int k) { return 32 * n + 8 * g + 2 * half + 4 * k; };       // of values i = 4 g + k and 4 g + k + 2
+    __syncthreads();
+    if (kw == 1) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) *reinterpret_cast<f2 *>(res + place(n, g, k)) = f2{o[n][4 * g + k], o[n][4 * g + k + 2]};
+        if (half == 0) {
+            res[D] = m;
+            res[D + 1] = l;
+        }
+    }
+    __syncthreads();
+    if (kw == 1 || !live) return;
+    const float m1 = res[D], l1 = res[D + 1], mm = fmaxf(m, m1);
+    const float by0 = __builtin_amdgcn_exp2f(m - mm), by1 = __builtin_amdgcn_exp2f(m1 - mm);
+    const float unit = ldexpf(1.0f, -kWeightBits);
+    const int e = v_exp - kScaleTop - kWeightBits;
+    float *dst = shared_part(parts, run, kv, kh, rows, row, D);
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f2 y = *reinterpret_cast<const f2 *>(res + place(n, g, k));
+                const f2 z = {ldexpf(fmaf(by1, y.x, by0 * o[n][4 * g + k]), e), ldexpf(fmaf(by1, y.y, by0 * o[n][4 * g + k + 2]), e)};
+                *reinterpret_cast<f2 *>(dst + place(n, g, k)) = z;
+            }
+    if (half == 0) {
+        dst[D] = mm;
+        dst[D + 1] = bad ? __builtin_nanf("") : fmaf(by1, l1, by0 * l) * unit;
+    }
+}
+
+// Joins a head's parts in order: those of its own tokens, then the prefix's runs.
+// As wq_kv.hip's join: a thread takes 4 values of every kJoinParts-th part and asks
+// for kJoinAhead of them at once.
+constexpr int kJoinParts = 8, kJoinAhead = 4;
+
+template <int D>
+__global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedArgs a, float *parts, int chunks, int groups, bool cut)
+{
+    constexpr int V = D / 4;
+    __shared__ f4 red[kJoinParts][V];
+    __shared__ float ml[kJoinParts][2];
+    const DecodeArgs &own = a.own;
+    const int b = blockIdx.x / own.heads, j = blockIdx.x % own.heads, c = threadIdx.x % V, part = threadIdx.x / V;
+    const int64_t len = own.lens[b];
+    const PrefixRuns runs = prefix_runs(a, chunks);
+    f4 *out = (f4 *)(own.out + (int64_t)b * own.out_stride + j * D) + c;
+    if (runs.bad || len < 0 || len > own.max_pages * kTile || (len == 0 && runs.len == 0)) {
+        const float y = runs.bad || len != 0 ? __builtin_nanf("") : 0.0f;
+        if (part == 0) *out = f4{y, y, y, y};
+        return;
+    }
+    const int kv = own.cache.kv_heads, group = own.heads / kv, per_step = kv * groups, per = (group + groups - 1) / groups;
+    const int kh = j / group, hg = j % group / per, hh = j % group % per;
+    const int64_t rows = (int64_t)own.B * group, row = (int64_t)b * group + j % group;
+    Pieces at = {0, 1, 0, 0};
+    if (cut && len > 0) at = ((const Pieces *)own.ws)[b];
+    const int mine = len > 0 ? at.count : 0, count = mine + runs.count;
+    float m = -3.0e38f, l = 0.0f;
+    f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = part; i0 < count; i0 += kJoinAhead * kJoinParts) {
+        float pm[kJoinAhead], pl[kJoinAhead];
+        f4 po[kJoinAhead];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int i = i0 + k * kJoinParts;
+            pm[k] = -3.0e38f;
+            pl[k] = 0.0f;
+            po[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (i < count) {
+                const float *p;
+                if (i >= mine) p = shared_part(parts, i - mine, kv, kh, rows, row, D);
+                else if (mine > 1) p = partial<D>(own, (int64_t)(at.first + i) * per_step + hg * kv + kh, i == 0 ? at.slot : 0, hh);
+                else p = nullptr;
+                if (p) {
+                    pm[k] = p[D];
+                    pl[k] = p[D + 1];
+                    po[k] = ((const f4 *)p)[c];
+                } else {                     // one piece: divided already
+                    const float *s = own.sums + ((int64_t)b * own.heads + j) * 2;
+                    pm[k] = s[0];
+                    pl[k] = s[1];
+                    po[k] = *out * pl[k];
+                }
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) mn = fmaxf(mn, pm[k]);
+        const float by = __builtin_amdgcn_exp2f(m - mn);
+        l *= by;
+        o *= by;
+        m = mn;
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const float f = __builtin_amdgcn_exp2f(pm[k] - m);
+            l = fmaf(f, pl[k], l);
+            o += f * po[k];
+        }
+    }
+    red[part][c] = o;
+    if (c == 0) {
+        ml[part][0] = m;
+        ml[part][1] = l;
+    }
+    __syncthreads();
+    if (part == 0) {
+        float mn = ml[0][0];
+#pragma unroll
+        for (int w = 1; w < kJoinParts; ++w) mn = fmaxf(mn, ml[w][0]);
+        float ll = 0.0f;
+        f4 oo = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kJoinParts; ++w) {
+            const float f = __builtin_amdgcn_exp2f(ml[w][0] - mn);
+            ll = fmaf(f, ml[w][1], ll);
+            oo += f * red[w][c];
+        }
+        *out = oo / ll;
+    }
+}
+
+// ---- how the prefix is cut
+// Workgroups of 1, 2 or 4 x 32 rows, as many runs of pages as fill the card.
+inline int row_waves(int64_t rows) { return rows <= 32 ? 1 : rows <= 64 ? 2 : 4; }
+inline int64_t row_blocks(int64_t rows) { return (rows + 32 * row_waves(rows) - 1) / (32 * row_waves(rows)); }
+inline int64_t prefix_chunks(int64_t B, int64_t heads, int64_t kv_heads, int64_t prefix_pages)
+{
+    const int64_t rows = B * (heads / kv_heads), blocks = row_blocks(rows) * kv_heads;
+    const int64_t fill = 1024 / row_waves(rows), n = fill / blocks;
+    return n > prefix_pages ? prefix_pages : n < 1 ? (prefix_pages > 0) : n;
+}
+inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
+inline uint64_t sums_bytes(int64_t B, int64_t heads) { return round256((uint64_t)B * heads * 8); }
+
+}  // namespace
+
+uint64_t shared_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
+{
+    return round256(decode_ws_bytes(B, heads, kv_heads, head_dim, max_pages)) + sums_bytes(B, heads) +
+           (uint64_t)prefix_chunks(B, heads, kv_heads, prefix_pages) * B * heads * (uint64_t)(head_dim + kPartialExtra) * 4;
+}
+
+hipError_t launch_attn_decode_shared(const SharedArgs &args, hipStream_t stream)
+{
+    SharedArgs a = args;
+    DecodeArgs &own = a.own;
+    const int64_t rows = (int64_t)own.B * (own.heads / own.cache.kv_heads);
+    const int kv = own.cache.kv_heads, groups = head_groups(own.heads, kv);
+    const int chunks = (int)prefix_chunks(own.B, own.heads, kv, a.prefix_pages), rw = row_waves(rows), D = own.cache.head_dim;
+    char *ws = (char *)own.ws + round256(decode_ws_bytes(own.B, own.heads, kv, D, own.max_pages));
+    own.sums = (float *)ws;
+    float *parts = (float *)(ws + sums_bytes(own.B, own.heads));
+    hipError_t e = launch_attn_decode(own, stream);
+    if (e != hipSuccess) return e;
+    int c_exp = 0;
+    const double c = frexp((double)own.scale * 1.4426950408889634, &c_exp);    // softmax in powers of two
+    if (chunks > 0) {
+        const unsigned grid = (unsigned)(row_blocks(rows) * kv * chunks);
+        const auto start = [&](auto kernel) { kernel<<<grid, 128 * rw, 0, stream>>>(a, parts, chunks, (float)(2.0 * c), c_exp - 1); };
+        if (D == 128) {
+            if (rw == 1) start(shared_kernel<128, 1>);
+            else if (rw == 2) start(shared_kernel<128, 2>);
+            else start(shared_kernel<128, 4>);
+        } else {
+            if (rw == 1) start(shared_kernel<64, 1>);
+            else if (rw == 2) start(shared_kernel<64, 2>);
+            else start(shared_kernel<64, 4>);
+        }
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const bool cut = cut_sequences(own.B, kv * groups, own.max_pages);
+    const unsigned jobs = (unsigned)((int64_t)own.B * own.heads);
+    if (D == 128) shared_join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, parts, chunks, groups, cut);
+    else shared_join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, parts, chunks, groups, cut);
+    return hipGetLastError();
+}
+
+}  // namespace wq

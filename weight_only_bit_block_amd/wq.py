@@ -95,12 +95,24 @@ def load(path: Optional[str] = None):
     lib.wq_attn_decode_ws.restype = U64
     lib.wq_attn_decode.argtypes = [C, P, I64, I64, P, I64, P, I64, F, P, I64, P, U64, P]
     lib.wq_residual_norm.argtypes = [P, P, P, P, I64, F, P, F, I64, I64, P, P, P]
+    lib.wq_kv_plan.argtypes = [P, P, I64, P, I64, P, I64, P, I64, P, P, P, P, P, P]
+    lib.wq_qk_norm_rope.argtypes = [P, I64, I64, P, I64, I64, I64, I64, P, P, I64, I, F, I, P, P, F, P, I64, P, I64, P]
+    lib.wq_kv_append_slots.argtypes = [C, P, I64, P, I64, I64, P, P]
+    lib.wq_attn_prefill_window.argtypes = [P, I64, P, I64, P, I64, I64, P, I64, I64, I64, I64, F, I64, I64, P, I64, P, U64, P]
+    lib.wq_attn_decode_window_ws.argtypes = [I64] * 7
+    lib.wq_attn_decode_window_ws.restype = U64
+    lib.wq_attn_decode_window.argtypes = [C, P, I64, I64, P, I64, P, I64, F, I64, I64, P, I64, P, U64, P]
+    lib.wq_attn_decode_shared_ws.argtypes = [I64] * 6
+    lib.wq_attn_decode_shared_ws.restype = U64
+    lib.wq_attn_decode_shared.argtypes = [C, P, I64, I64, P, I64, P, P, I64, P, I64, F, P, I64, P, U64, P]
     lib.wq_strerror.argtypes = [I]
     lib.wq_strerror.restype = ctypes.c_char_p
     lib.wq_abi_version.argtypes = []
     for f in ("wq_pack", "wq_unpack", "wq_gemv", "wq_gemm", "wq_linear", "wq_gemm_noalloc", "wq_table_layout",
               "wq_table_plan", "wq_table_plan_gemm", "wq_gemv_grouped", "wq_gemm_grouped", "wq_embed",
-              "wq_attn_prefill", "wq_kv_append", "wq_attn_decode", "wq_residual_norm", "wq_abi_version"):
+              "wq_attn_prefill", "wq_kv_append", "wq_attn_decode", "wq_residual_norm", "wq_kv_plan", "wq_qk_norm_rope",
+              "wq_kv_append_slots", "wq_attn_prefill_window", "wq_attn_decode_window", "wq_attn_decode_shared",
+              "wq_abi_version"):
         getattr(lib, f).restype = I
     _lib = lib
     return lib
