@@ -237,7 +237,7 @@ struct DecodeArgs {
     int64_t out_stride;
     void *ws;
     int64_t window, sinks;                      // window 0: all keys
-    float *sums;                                // [B][heads][2]: maximum (log2) and sum of weights; null: not wanted
+    float *sums;                                // Form::sums: [B][heads][2], maximum (log2) and sum of weights of whole sequences
 };
 struct SharedArgs {
     DecodeArgs own;                             // the sequences' own tokens; own.ws the start of the workspace

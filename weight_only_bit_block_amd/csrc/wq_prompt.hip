@@ -105,16 +105,6 @@ __device__ __forceinline__ float finite_abs(float x)
 // Power of two that brings a (>= 0) into [2^(top-1), 2^top); 0 for a == 0.
 __device__ __forceinline__ int normaliser(float a, int top) { return a > 0.0f ? top - __builtin_amdgcn_frexp_expf(a) : 0; }
 
-// x = hi + lo to 22 bits (hi rounded to nearest, the remainder exact in fp32).
-// x is made opaque first: contracted with the product that made it, the hi
-// that is subtracted could be rounded differently from the hi that is kept.
-__device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo)
-{
-    asm("" : "+v"(x));
-    hi = (_Float16)x;
-    lo = (_Float16)(x - (float)hi);
-}
-
 // ---------------------------------------------------------------- prepare
 // One workgroup per (tile, key/value head, k or v); 8 threads share a row of D
 // values. All latency at short prompts; at long ones 4 D bytes in and as many out for a
@@ -210,11 +200,13 @@ __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__
             const int d0 = seg * E + 8 * c, f = d0 >> 4, half = (d0 >> 3) & 1;
             h8 hi, lo;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                _Float16 y, z;
-                split(ldexpf(x[8 * c + j], er), y, z);
-                hi[j] = y;
-                lo[j] = z;
+            for (int j = 0; j < 8; j += 2) {
+                half2_t y, z;
+                split2(ldexpf(x[8 * c + j], er), ldexpf(x[8 * c + j + 1], er), y, z);
+                hi[j] = y.x;
+                hi[j + 1] = y.y;
+                lo[j] = z.x;
+                lo[j + 1] = z.y;
             }
             const int o = f * 512 + (half * 32 + row) * 8;
             store_through<D>(dst, o, hi);
@@ -240,13 +232,20 @@ __global__ __launch_bounds__(256) void prepare_kernel(PromptArgs a, _Float16 *__
         const int d = (f >> 1) * 32 + (lane & 31), k0 = (f & 1) * 16 + 4 * (lane >> 5);
         h8 hi, lo;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int u = k0 + 8 * (j >> 2) + (j & 3);
-            const float y = rows[u][d];
-            _Float16 p, z;
-            split(fabsf(y) <= kBig ? ldexpf(y, factor[u]) : 0.0f, p, z);
-            hi[j] = p;
-            lo[j] = z;
+        for (int j = 0; j < 8; j += 2) {
+            float y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int u = k0 + 8 * (j >> 2) + (j & 3) + i;
+                y[i] = rows[u][d];
+                y[i] = fabsf(y[i]) <= kBig ? ldexpf(y[i], factor[u]) : 0.0f;
+            }
+            half2_t p, z;
+            split2(y[0], y[1], p, z);
+            hi[j] = p.x;
+            hi[j + 1] = p.y;
+            lo[j] = z.x;
+            lo[j + 1] = z.y;
         }
         store_through<D>(dst, c * 8, hi);
         store_through<D>(dst, D * kTileKeys + c * 8, lo);
@@ -315,11 +314,13 @@ __device__ __forceinline__ int start_rows(Rows<D> &s, float top, int c_exp)
 __device__ __forceinline__ void split_query(const float (&x)[8], int e, float c_man, h8 &q1, h8 &q2)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        _Float16 hi, lo;
-        split(ldexpf(x[j], e) * c_man, hi, lo);
-        q1[j] = hi;
-        q2[j] = lo;
+    for (int j = 0; j < 8; j += 2) {
+        half2_t hi, lo;
+        split2(ldexpf(x[j], e) * c_man, ldexpf(x[j + 1], e) * c_man, hi, lo);
+        q1[j] = hi.x;
+        q1[j + 1] = hi.y;
+        q2[j] = lo.x;
+        q2[j + 1] = lo.y;
     }
 }
 
@@ -477,11 +478,13 @@ __device__ __forceinline__ void weigh(Rows<D> &s, f16v &x)
 __device__ __forceinline__ void split8(const f16v &x, int t, h8 &p1, h8 &p2)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        _Float16 hi, lo;
-        split(x[8 * t + i], hi, lo);
-        p1[i] = hi;
-        p2[i] = lo;
+    for (int i = 0; i < 8; i += 2) {
+        half2_t hi, lo;
+        split2(x[8 * t + i], x[8 * t + i + 1], hi, lo);
+        p1[i] = hi.x;
+        p1[i + 1] = hi.y;
+        p2[i] = lo.x;
+        p2[i + 1] = lo.y;
     }
 }
 
@@ -900,11 +903,13 @@ __device__ __forceinline__ void scale_row(float (&x)[F][8], int e, float &by)
 __device__ __forceinline__ void split_by(const float (&x)[8], float by, h8 &y1, h8 &y2)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        _Float16 hi, lo;
-        split(x[j] * by, hi, lo);
-        y1[j] = hi;
-        y2[j] = lo;
+    for (int j = 0; j < 8; j += 2) {
+        half2_t hi, lo;
+        split2(x[j] * by, x[j + 1] * by, hi, lo);
+        y1[j] = hi.x;
+        y1[j + 1] = hi.y;
+        y2[j] = lo.x;
+        y2[j + 1] = lo.y;
     }
 }
 

@@ -9,10 +9,11 @@
 // For one key/value head the prefix meets R = B * group query rows, so that its
 // scores are a matrix product of R x L x D: bound by the matrix cores and the
 // softmax's vector instructions once R passes 32 or so, by HBM below.
-//   A workgroup takes 32 RW rows and a run of pages, and joins with the others
-// through the workspace. A page's 64 keys are two tiles of 32, one for each half
-// of the workgroup's 2 RW wavefronts, which meet at the end in LDS. All threads
-// turn the page's codes into operands in LDS, once for all rows:
+//   A workgroup of 4 wavefronts takes 32 RW rows and a run of pages, and joins with
+// the others through the workspace. A page's 64 keys are two tiles of 32: with 128
+// rows every wavefront walks both, with 64 two wavefronts share a row and
+// meet at the end in LDS. All threads turn the page's codes into operands in LDS, once
+// for all rows:
 //   k   the codes themselves, exact in binary16. q is split in two parts (22
 //       bits) after a power of two, so a block's sum is two products; it is scaled
 //       in fp32, one multiplication a key and block: exact for every scale.
@@ -27,52 +28,21 @@
 #include "wq_device.h"
 #include "wq_kv_decode.h"
 
-#include <math.h>
+#include <type_traits>
 
 namespace wq {
 namespace {
 
 typedef float f2 __attribute__((ext_vector_type(2)));
-typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef short s4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kKeys = 32;                    // of a wavefront's tile; a page has two
 constexpr float kBig = 3.4028235e38f;
-constexpr int kWeightBits = 12;              // a weight of 1 is 2^12 as a binary16 operand
-constexpr float kSlack = 3.0f;               // log2 a score may pass the running maximum by before rescaling
 constexpr int kScaleTop = 12;                // |code| <= 8: values stay below 2^15
-constexpr int kMinScaleExp = -24;            // 2^-24 is binary16's smallest
-constexpr uint32_t kRankZero = 0x800;
 
 __device__ __forceinline__ f16v mfma(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
-
-// 8 codes of a dword as exact binary16 values, in the order of nibbles 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
-__device__ __forceinline__ h8 codes8(uint32_t x)
-{
-    const h2 off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-    const h2 off16 = {(_Float16)-72.0f, (_Float16)-72.0f}, inv16 = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const uint32_t y = x >> 8;
-    const h2 a = __builtin_bit_cast(h2, (x & 0x000F000Fu) ^ 0x64086408u) + off;
-    const h2 b = __builtin_elementwise_fma(__builtin_bit_cast(h2, (x & 0x00F000F0u) ^ 0x64806480u), inv16, off16);
-    const h2 c = __builtin_bit_cast(h2, (y & 0x000F000Fu) ^ 0x64086408u) + off;
-    const h2 d = __builtin_elementwise_fma(__builtin_bit_cast(h2, (y & 0x00F000F0u) ^ 0x64806480u), inv16, off16);
-    return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
-// x = hi + lo to 22 bits; x is made opaque so that the hi subtracted is the hi kept.
-__device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo)
-{
-    asm("" : "+v"(x));
-    hi = (_Float16)x;
-    lo = (_Float16)(x - (float)hi);
-}
 
 // The run of pages of a workgroup, from the prefix's length, which is on the device.
 struct PrefixRuns {
@@ -107,48 +77,65 @@ __device__ __forceinline__ int v_at(int key, int piece)
     return key * 128 + (piece ^ ((key >> 1 & 1) * 4 + (key >> 2 & 3))) * 16;
 }
 
+// RW x 32 rows, two wavefronts for 32 of them. Two buffers of operands where a compute
+// unit holds one workgroup (128 rows), one where it holds two, which take turns.
+constexpr int operand_bytes(int D) { return 3 * kTile * D * 2 + D / 32 * kTile * 2; }
+constexpr int at_least(int a, int b) { return a > b ? a : b; }
+constexpr int prefix_lds_bytes(int D, int RW) { return at_least((RW == 4 ? 2 : 1) * operand_bytes(D), 32 * RW * (D + kPartialExtra) * 4); }
+
 template <int D, int RW>
-__global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp)
+__device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, int chunks, float c_man, int c_exp, uint8_t *lds, unsigned job)
 {
-    constexpr int NB = D / 32, F = D / 16, NT = 128 * RW;
-    constexpr int kChunks = kTile * D / 16, kMine = kChunks < NT ? 1 : kChunks / NT;      // 8-byte pieces of a page's k or v; of a thread
-    constexpr int kRowBytes = D * 2;
-    constexpr int kOperands = 3 * kTile * kRowBytes + NB * kTile * 2, kResult = 32 * RW * (D + kPartialExtra) * 4;
+    constexpr int NB = D / 32, F = D / 16, W = 2 * RW;
+    constexpr bool kTwo = RW == 4, kApart = F < W;                        // kApart: more wavefronts than pieces, k's and v's are others
+    constexpr int kMine = kApart ? 1 : F / W;                             // pieces of 16 values of a key's k or v, of a thread
+    constexpr int kRowBytes = D * 2, kPitch = D + kPartialExtra, kOperands = operand_bytes(D);
     typedef _Float16 hb __attribute__((ext_vector_type(NB)));
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kOperands > kResult ? kOperands : kResult];
-    uint8_t *const kb = lds, *const vb = lds + kTile * kRowBytes;                         // v: high parts, low parts
-    _Float16 *const ksb = reinterpret_cast<_Float16 *>(lds + 3 * kTile * kRowBytes);      // k's scales, [block][key]
     const DecodeArgs &own = a.own;
     const int kv = own.cache.kv_heads, group = own.heads / kv;
     const int64_t rows = (int64_t)own.B * group;
     // key/value heads next to each other: ids go round the 8 XCDs
-    const int kh = blockIdx.x % kv, run = blockIdx.x / kv % chunks;
-    const int64_t block = blockIdx.x / kv / chunks;
+    const int kh = job % kv, run = job / kv % chunks;
+    const int64_t block = job / kv / chunks;
     const PrefixRuns runs = prefix_runs(a, chunks);
     if (run >= runs.count) return;
     const int page0 = run * runs.per, page_end = page0 + runs.per < runs.pages ? page0 + runs.per : runs.pages;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), rw = wave % RW, kw = wave / RW;
     const int64_t row = (block * RW + rw) * 32 + (lane & 31);
-    const bool live = row < rows;
+    const bool live = row < rows, any = (block * RW + rw) * 32 < rows;
 
     // ---- pages come into registers one ahead: codes of this thread's pieces, scales of the lane's key
-    u2 kc[kMine], vc[kMine];
+    const bool do_k = !kApart || wave < F, do_v = !kApart || wave >= F;
+    u2 kc[kMine], vc[kMine];                 // (one and the same where kApart)
     hb ks, vs;
     bool bad = false;
-    const auto fetch = [&](int page) __attribute__((always_inline)) {
-        int id = __builtin_amdgcn_readfirstlane(a.prefix[page]);
-        if (id < 0 || id >= own.cache.n_pages) {
-            bad = true;
-            id = 0;
+    if (own.cache.n_pages <= 0) {            // no page to read at all
+        if (live && kw == 0 && half == 0) {
+            float *dst = shared_part(parts, run, kv, kh, rows, row, D);
+            for (int i = 0; i < D; ++i) dst[i] = 0.0f;
+            dst[D] = -3.0e38f;
+            dst[D + 1] = __builtin_nanf("");
         }
-        if (own.cache.n_pages <= 0) return;
+        return;
+    }
+    int ids = page0 + lane < page_end ? a.prefix[page0 + lane] : 0;       // numbers of the run's next 64 pages
+    // (past the run's end: its last page again. No branch around the loads: it would wait for them)
+    const auto fetch = [&](int next) __attribute__((always_inline)) {
+        const int page = next < page_end ? next : page_end - 1;
+        if (next < page_end && page != page0 && (page - page0) % 64 == 0) ids = page + lane < page_end ? a.prefix[page + lane] : 0;
+        int id = __builtin_amdgcn_readlane(ids, (page - page0) & 63);
+        const bool out = id < 0 || id >= own.cache.n_pages;
+        bad |= out;
+        id = out ? 0 : id;
         const int64_t at = ((int64_t)id * kv + kh) * kTile;
         const uint8_t *kq = reinterpret_cast<const uint8_t *>(own.cache.kq) + at * (D / 2), *vq = reinterpret_cast<const uint8_t *>(own.cache.vq) + at * (D / 2);
-        if (kChunks >= NT || wave * 64 < kChunks) {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int o = lane * (D / 2) + (wave + i * 2 * RW) * 8;
+        for (int i = 0; i < kMine; ++i) {
+            const int o = lane * (D / 2) + (wave + W * i) % F * 8;
+            if constexpr (kApart) {
+                kc[i] = vc[i] = *reinterpret_cast<const u2 *>((do_k ? kq : vq) + o);
+            } else {
                 kc[i] = *reinterpret_cast<const u2 *>(kq + o);
                 vc[i] = *reinterpret_cast<const u2 *>(vq + o);
             }
@@ -156,9 +143,62 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
         ks = *reinterpret_cast<const hb *>(own.cache.ks + (at + lane) * NB);
         vs = *reinterpret_cast<const hb *>(own.cache.vs + (at + lane) * NB);
     };
+    int v_exp = kMinScaleExp;
+    uint32_t v_limit = kRankZero + 2;        // rank of 2^v_exp
+    // The page in the registers becomes operands. Returns the power of two that the output's units change by.
+    const auto put = [&](int page) __attribute__((always_inline)) -> int {
+        uint8_t *const kb = lds + (kTwo ? page & 1 : 0) * kOperands, *const vb = kb + kTile * kRowBytes;      // v: high parts, low parts
+        _Float16 *const ksb = reinterpret_cast<_Float16 *>(kb + 3 * kTile * kRowBytes);                       // k's scales, [block][key]
+        // magnitudes of the lane's scales of v in their order, what is not finite below zero
+        if ((int64_t)page * kTile + lane >= runs.len) vs = hb{};
+        typedef uint16_t ub __attribute__((ext_vector_type(NB)));
+        const ub rank = __builtin_bit_cast(ub, vs) * (uint16_t)2 + (uint16_t)kRankZero;
+        uint16_t top = rank[0];
+        int by = 0;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) kc[i] = vc[i] = u2{0, 0};
-    ks = vs = hb{};
+        for (int i = 1; i < NB; ++i) top = top > rank[i] ? top : rank[i];
+        if (__any(top > v_limit)) {          // (the same in every wavefront)
+            float vmax = top > kRankZero ? (float)__builtin_bit_cast(_Float16, (uint16_t)((top - kRankZero) >> 1)) : 0.0f;
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, s));
+            const int e = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
+            by = __builtin_amdgcn_readfirstlane(v_exp - e);
+            v_exp = e;
+            v_limit = kRankZero + 2 * (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(1.0f, e));
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int piece = (wave + W * i) % F, b = piece >> 1;                         // 16 values, half a block
+            if (do_k) {
+                _Float16 s = ks[0];
+#pragma unroll
+                for (int n = 1; n < NB; ++n) s = b == n ? ks[n] : s;
+                if ((piece & 1) == 0) ksb[b * kTile + lane] = s;
+                // fragment `piece` of the key's tile, lane (key, half)
+                h8 *kd = reinterpret_cast<h8 *>(kb) + (lane >> 5) * (F * 64) + piece * 64 + (lane & 31);
+                kd[0] = codes8(kc[i].x);
+                kd[32] = codes8(kc[i].y);
+            }
+            if (do_v) {
+                _Float16 s1 = vs[0];
+#pragma unroll
+                for (int n = 1; n < NB; ++n) s1 = b == n ? vs[n] : s1;
+                s1 = (_Float16)ldexpf((float)s1, kScaleTop - v_exp);
+                const h8 s = {s1, s1, s1, s1, s1, s1, s1, s1};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const h8 c = codes8(vc[i][j]);
+                    h8 hi = c * s;
+                    asm("" : "+v"(hi));
+                    const h8 lo = __builtin_elementwise_fma(c, s, -hi);
+                    const int at = v_at<D>(lane, 2 * piece + j);
+                    *reinterpret_cast<h8 *>(vb + at) = hi;
+                    *reinterpret_cast<h8 *>(vb + kTile * kRowBytes + at) = lo;
+                }
+            }
+        }
+        return by;
+    };
     fetch(page0);
 
     // ---- the query: values 16 f + 8 half + nibble_of(e) of the lane's row
@@ -186,11 +226,13 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                _Float16 hi, lo;
-                split(ldexpf(x[i][nibble_of(e)], e2) * c_man, hi, lo);
-                q1[i][e] = hi;
-                q2[i][e] = lo;
+            for (int e = 0; e < 8; e += 2) {
+                half2_t hi, lo;
+                split2(ldexpf(x[i][nibble_of(e)], e2) * c_man, ldexpf(x[i][nibble_of(e + 1)], e2) * c_man, hi, lo);
+                q1[i][e] = hi.x;
+                q1[i][e + 1] = hi.y;
+                q2[i][e] = lo.x;
+                q2[i][e + 1] = lo.y;
             }
     }
 
@@ -198,85 +240,31 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
 #pragma unroll
     for (int n = 0; n < NB; ++n) o[n] = f16v{};
     float m = -3.0e38f, l = 0.0f;
-    int v_exp = kMinScaleExp;
-    uint32_t v_limit = kRankZero + 2;        // rank of 2^v_exp
-
-    for (int page = page0; page < page_end; ++page) {
-        const int left = (int)(runs.len - (int64_t)page * kTile < kTile ? runs.len - (int64_t)page * kTile : kTile);
-        // ---- units of v: magnitudes of the lane's scales in their order, what is not finite below zero
-        if (lane >= left) vs = hb{};
-        typedef uint16_t ub __attribute__((ext_vector_type(NB)));
-        const ub rank = __builtin_bit_cast(ub, vs) * (uint16_t)2 + (uint16_t)kRankZero;
-        uint16_t top = rank[0];
-#pragma unroll
-        for (int i = 1; i < NB; ++i) top = top > rank[i] ? top : rank[i];
-        if (__any(top > v_limit)) {          // (the same in every wavefront)
-            float vmax = top > kRankZero ? (float)__builtin_bit_cast(_Float16, (uint16_t)((top - kRankZero) >> 1)) : 0.0f;
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, s));
-            const int e = vmax > ldexpf(1.0f, v_exp) ? __builtin_amdgcn_frexp_expf(vmax) : v_exp;
-            const float by = ldexpf(1.0f, v_exp - e);
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[n][i] *= by;
-            v_exp = e;
-            v_limit = kRankZero + 2 * (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(1.0f, e));
-        }
-        // ---- operands
-        if (page != page0) __syncthreads();  // those of the page before have been read
-        if (kChunks >= NT || wave * 64 < kChunks) {
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int piece = wave + i * 2 * RW, b = piece >> 1;                      // 16 values, half a block
-                _Float16 sk = ks[0], sv = vs[0];
-#pragma unroll
-                for (int n = 1; n < NB; ++n)
-                    if (b == n) {
-                        sk = ks[n];
-                        sv = vs[n];
-                    }
-                const _Float16 sn = (_Float16)ldexpf((float)sv, kScaleTop - v_exp);
-                const h8 s = {sn, sn, sn, sn, sn, sn, sn, sn};
-                if ((piece & 1) == 0) ksb[b * kTile + lane] = sk;
-                // k: fragment `piece` of the key's tile, lane (key, half)
-                h8 *kd = reinterpret_cast<h8 *>(kb) + (lane >> 5) * (F * 64) + piece * 64 + (lane & 31);
-                kd[0] = codes8(kc[i].x);
-                kd[32] = codes8(kc[i].y);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const h8 c = codes8(vc[i][j]);
-                    h8 hi = c * s;
-                    asm("" : "+v"(hi));
-                    const h8 lo = __builtin_elementwise_fma(c, s, -hi);
-                    const int at = v_at<D>(lane, 2 * piece + j);
-                    *reinterpret_cast<h8 *>(vb + at) = hi;
-                    *reinterpret_cast<h8 *>(vb + kTile * kRowBytes + at) = lo;
-                }
-            }
-        }
-        if (page + 1 < page_end) fetch(page + 1);
-        lds_barrier();
-        // ---- scores of the wavefront's 32 keys
-        const h8 *kf = reinterpret_cast<const h8 *>(kb) + kw * (F * 64) + lane;
+    // The wavefront's tile of a page.
+    const auto attend = [&](int page) __attribute__((always_inline)) {
+        const uint8_t *const kb = lds + (kTwo ? page & 1 : 0) * kOperands, *const vb = kb + kTile * kRowBytes;
+        const h8 *const kf = reinterpret_cast<const h8 *>(kb) + kw * (F * 64) + lane;
+        const _Float16 *const sb = reinterpret_cast<const _Float16 *>(kb + 3 * kTile * kRowBytes) + kw * kKeys + 4 * half;
         f16v x = {};
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             f16v z = {};
 #pragma unroll
             for (int i = 2 * b; i < 2 * b + 2; ++i) {
-                z = mfma(kf[64 * i], q2[i], z);
-                z = mfma(kf[64 * i], q1[i], z);
+                const h8 k = kf[64 * i];
+                z = mfma(k, q2[i], z);
+                z = mfma(k, q1[i], z);
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const h4 s = *reinterpret_cast<const h4 *>(ksb + b * kTile + kw * kKeys + 8 * g + 4 * half);
+                const h4 s = *reinterpret_cast<const h4 *>(sb + b * kTile + 8 * g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[4 * g + i] = fmaf(z[4 * g + i], (float)s[i], x[4 * g + i]);
             }
         }
-        if (left < kTile) {
-            const int end = left - kw * kKeys - 4 * half;
+        const int64_t left = runs.len - (int64_t)page * kTile - kw * kKeys;
+        if (left < kKeys) {
+            const int end = (int)left - 4 * half;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (8 * (i >> 2) + (i & 3) >= end) x[i] = -__builtin_inff();
@@ -302,17 +290,19 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
             sum += x[i];
         }
         l += sum;
-        // ---- output: 16 keys at a time; a lane reads 4 keys of 16 values and gets its value of them
+        // output: 16 keys at a time; a lane reads 4 keys of 16 values and gets its value of them
         const int c = lane & 15;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             h8 p1, p2;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                _Float16 hi, lo;
-                split(x[8 * t + i], hi, lo);
-                p1[i] = hi;
-                p2[i] = lo;
+            for (int i = 0; i < 8; i += 2) {
+                half2_t hi, lo;
+                split2(x[8 * t + i], x[8 * t + i + 1], hi, lo);
+                p1[i] = hi.x;
+                p1[i + 1] = hi.y;
+                p2[i] = lo.x;
+                p2[i + 1] = lo.y;
             }
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -333,13 +323,40 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
                 o[n] = mfma(v[0], p1, o[n]);
             }
         }
+    };
+    const auto rescale = [&](int by) __attribute__((always_inline)) {
+        if (by == 0) return;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[n][i] = ldexpf(o[n][i], by);
+    };
+
+    put(page0);                              // (the output is zero: its units change for nothing)
+    fetch(page0 + 1);
+    for (int page = page0; page < page_end; ++page) {
+        lds_barrier();                       // the page's operands are there; with two buffers, those before have been read
+        if constexpr (kTwo) {
+            // wavefronts of a SIMD take turns: one's matrix instructions beside the other's operands
+            int by = 0;
+            if (any) attend(page);
+            by = put(page + 1);              // (past the run's end: into a buffer that is not read)
+            fetch(page + 2);
+            rescale(by);
+        } else {
+            if (any) attend(page);
+            if (page + 1 < page_end) {
+                lds_barrier();               // read
+                rescale(put(page + 1));
+                fetch(page + 2);
+            }
+        }
     }
 
-    // ---- the two halves of the keys meet in LDS; row position j of a block is value (j & ~7) + nibble_of(j & 7)
+    // ---- the two wavefronts of the same rows meet in LDS; row position j of a block is value (j & ~7) + nibble_of(j & 7)
     l += other_half(l);
-    constexpr int kPitch = D + kPartialExtra;
-    float *res = reinterpret_cast<float *>(lds) + (rw * 32 + (lane & 31)) * kPitch;
     const auto place = [&](int n, int g, int k) { return 32 * n + 8 * g + 2 * half + 4 * k; };       // of values i = 4 g + k and 4 g + k + 2
+    float *const res = reinterpret_cast<float *>(lds) + (rw * 32 + (lane & 31)) * kPitch;
     __syncthreads();
     if (kw == 1) {
 #pragma unroll
@@ -357,7 +374,6 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
     if (kw == 1 || !live) return;
     const float m1 = res[D], l1 = res[D + 1], mm = fmaxf(m, m1);
     const float by0 = __builtin_amdgcn_exp2f(m - mm), by1 = __builtin_amdgcn_exp2f(m1 - mm);
-    const float unit = ldexpf(1.0f, -kWeightBits);
     const int e = v_exp - kScaleTop - kWeightBits;
     float *dst = shared_part(parts, run, kv, kh, rows, row, D);
 #pragma unroll
@@ -372,8 +388,25 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
             }
     if (half == 0) {
         dst[D] = mm;
-        dst[D + 1] = bad ? __builtin_nanf("") : fmaf(by1, l1, by0 * l) * unit;
+        dst[D + 1] = bad ? __builtin_nanf("") : ldexpf(fmaf(by1, l1, by0 * l), -kWeightBits);
     }
+}
+
+// A step: workgroups of the sequences' own tokens, RW / 2 jobs each, then those of
+// the prefix. Apart, either would wait for the other's last.
+template <int D, int RW, int H>
+__global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp, int groups, bool cut, unsigned own_jobs)
+{
+    constexpr int kJobs = RW / 2, kJobBytes = (decode_lds_bytes(D, H) + 15) / 16 * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(prefix_lds_bytes(D, RW), kJobs * kJobBytes)];
+    const unsigned own_groups = (own_jobs + kJobs - 1) / kJobs;
+    if (blockIdx.x < own_groups) {
+        const int which = kJobs == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+        const unsigned job = blockIdx.x * kJobs + which;
+        if (job < own_jobs) decode_job<D, H, Form::sums>(a.own, groups, cut, c_man, c_exp, lds + which * kJobBytes, job, threadIdx.x & 255);
+        return;
+    }
+    prefix_job<D, RW>(a, parts, chunks, c_man, c_exp, lds, blockIdx.x - own_groups);
 }
 
 // Joins a head's parts in order: those of its own tokens, then the prefix's runs.
@@ -468,23 +501,28 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
 }
 
 // ---- how the prefix is cut
-// Workgroups of 1, 2 or 4 x 32 rows, as many runs of pages as fill the card.
-inline int row_waves(int64_t rows) { return rows <= 32 ? 1 : rows <= 64 ? 2 : 4; }
+// Workgroups of 64 or 128 rows, two on each compute unit, as many runs of pages as that takes.
+constexpr int kSharedFill = 512;
+inline int row_waves(int64_t rows) { return rows <= 64 ? 2 : 4; }
 inline int64_t row_blocks(int64_t rows) { return (rows + 32 * row_waves(rows) - 1) / (32 * row_waves(rows)); }
 inline int64_t prefix_chunks(int64_t B, int64_t heads, int64_t kv_heads, int64_t prefix_pages)
 {
     const int64_t rows = B * (heads / kv_heads), blocks = row_blocks(rows) * kv_heads;
-    const int64_t fill = 1024 / row_waves(rows), n = fill / blocks;
+    const int64_t n = kSharedFill * 2 / row_waves(rows) / blocks;
     return n > prefix_pages ? prefix_pages : n < 1 ? (prefix_pages > 0) : n;
 }
+// A sequence's own tokens are cut whenever that makes parts: there is a join anyway.
+inline bool cut_own(int64_t B, int64_t max_pages) { return B <= kCutMaxSeqs && max_pages > kDecodeWaves; }
 inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 inline uint64_t sums_bytes(int64_t B, int64_t heads) { return round256((uint64_t)B * heads * 8); }
+inline uint64_t own_bytes(int64_t B, int per_step, int64_t head_dim, int64_t max_pages) { return cut_own(B, max_pages) ? round256(pieces_bytes(per_step, head_dim)) : 0; }
 
 }  // namespace
 
 uint64_t shared_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
 {
-    return round256(decode_ws_bytes(B, heads, kv_heads, head_dim, max_pages)) + sums_bytes(B, heads) +
+    const int per_step = (int)kv_heads * head_groups((int)heads, (int)kv_heads);
+    return own_bytes(B, per_step, head_dim, max_pages) + sums_bytes(B, heads) +
            (uint64_t)prefix_chunks(B, heads, kv_heads, prefix_pages) * B * heads * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
 
@@ -492,32 +530,34 @@ hipError_t launch_attn_decode_shared(const SharedArgs &args, hipStream_t stream)
 {
     SharedArgs a = args;
     DecodeArgs &own = a.own;
-    const int64_t rows = (int64_t)own.B * (own.heads / own.cache.kv_heads);
-    const int kv = own.cache.kv_heads, groups = head_groups(own.heads, kv);
-    const int chunks = (int)prefix_chunks(own.B, own.heads, kv, a.prefix_pages), rw = row_waves(rows), D = own.cache.head_dim;
-    char *ws = (char *)own.ws + round256(decode_ws_bytes(own.B, own.heads, kv, D, own.max_pages));
+    const int kv = own.cache.kv_heads, group = own.heads / kv, groups = head_groups(own.heads, kv), per_step = kv * groups;
+    const int per = (group + groups - 1) / groups, D = own.cache.head_dim;
+    const int64_t rows = (int64_t)own.B * group;
+    const int chunks = (int)prefix_chunks(own.B, own.heads, kv, a.prefix_pages), rw = row_waves(rows);
+    const bool cut = cut_own(own.B, own.max_pages);
+    char *ws = (char *)own.ws + own_bytes(own.B, per_step, D, own.max_pages);
     own.sums = (float *)ws;
     float *parts = (float *)(ws + sums_bytes(own.B, own.heads));
-    hipError_t e = launch_attn_decode(own, stream);
-    if (e != hipSuccess) return e;
     int c_exp = 0;
     const double c = frexp((double)own.scale * 1.4426950408889634, &c_exp);    // softmax in powers of two
-    if (chunks > 0) {
-        const unsigned grid = (unsigned)(row_blocks(rows) * kv * chunks);
-        const auto start = [&](auto kernel) { kernel<<<grid, 128 * rw, 0, stream>>>(a, parts, chunks, (float)(2.0 * c), c_exp - 1); };
+    const unsigned own_jobs = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : own.B));
+    const unsigned grid = (own_jobs + rw / 2 - 1) / (rw / 2) + (unsigned)(row_blocks(rows) * kv * chunks);
+    const auto start = [&](auto kernel) { kernel<<<grid, 128 * rw, 0, stream>>>(a, parts, chunks, (float)(2.0 * c), c_exp - 1, groups, cut, own_jobs); };
+    const auto pick = [&](auto waves) {
+        constexpr int RW = decltype(waves)::value;
         if (D == 128) {
-            if (rw == 1) start(shared_kernel<128, 1>);
-            else if (rw == 2) start(shared_kernel<128, 2>);
-            else start(shared_kernel<128, 4>);
+            if (per <= 2) start(shared_kernel<128, RW, 2>);
+            else if (per <= 4) start(shared_kernel<128, RW, 4>);
+            else start(shared_kernel<128, RW, 8>);
         } else {
-            if (rw == 1) start(shared_kernel<64, 1>);
-            else if (rw == 2) start(shared_kernel<64, 2>);
-            else start(shared_kernel<64, 4>);
+            if (per <= 4) start(shared_kernel<64, RW, 4>);
+            else start(shared_kernel<64, RW, 8>);
         }
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const bool cut = cut_sequences(own.B, kv * groups, own.max_pages);
+    };
+    if (rw == 2) pick(std::integral_constant<int, 2>{});
+    else pick(std::integral_constant<int, 4>{});
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const unsigned jobs = (unsigned)((int64_t)own.B * own.heads);
     if (D == 128) shared_join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, parts, chunks, groups, cut);
     else shared_join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, parts, chunks, groups, cut);
