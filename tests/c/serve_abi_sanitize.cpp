@@ -10,7 +10,7 @@ static int launches = 0, failures = 0;
 
 namespace wq {
 uint64_t prompt_ws_bytes(int64_t T, int64_t B, int64_t, int64_t kv, int64_t d) { return (uint64_t)(T / 32 + B) * kv * d * 256; }
-uint64_t decode_ws_bytes(int64_t B, int64_t, int64_t, int64_t, int64_t pages) { return B <= 512 && pages > 16 ? 4096 : 0; }
+uint64_t decode_window_ws_bytes(int64_t B, int64_t, int64_t, int64_t, int64_t pages, int64_t window, int64_t) { return B <= 512 && pages > 16 && window > 1000 ? 4096 : 0; }
 uint64_t shared_ws_bytes(int64_t B, int64_t heads, int64_t, int64_t d, int64_t, int64_t) { return (uint64_t)B * heads * d; }
 hipError_t launch_attn_prefill(const PromptArgs &a, hipStream_t)
 {

@@ -282,6 +282,7 @@ struct NormArgs {
 };
 uint64_t prompt_ws_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim);
 uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages);
+uint64_t decode_window_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t window, int64_t sinks);
 hipError_t launch_attn_prefill(const PromptArgs &a, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream);
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream);

@@ -236,14 +236,19 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t stream)
 
 uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages)
 {
+    return decode_window_ws_bytes(B, heads, kv_heads, head_dim, max_pages, 0, 0);
+}
+
+uint64_t decode_window_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t window, int64_t sinks)
+{
     const int per_step = (int)kv_heads * head_groups((int)heads, (int)kv_heads);
-    return cut_sequences(B, per_step, max_pages) ? pieces_bytes(per_step, head_dim) : 0;
+    return cut_call(B, per_step, max_pages, window, sinks) ? pieces_bytes(per_step, head_dim) : 0;
 }
 
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
 {
     const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv), per_step = kv * groups;
-    const bool cut = cut_sequences(a.B, per_step, seen_pages(a.max_pages, a.window, a.sinks));
+    const bool cut = cut_call(a.B, per_step, a.max_pages, a.window, a.sinks);
     const unsigned grid = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : a.B));
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two

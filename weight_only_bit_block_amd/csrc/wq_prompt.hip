@@ -1084,7 +1084,17 @@ inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((u
 // (1248) 104 / 118, but one of 9700 (1216) 690 / 658, of 11300 (1246) 812 / 789. The number of
 // prompts stands for how their lengths differ, which only the device knows: one long prompt
 // beside empty ones counts as several.
-inline int64_t few_groups(int D, int64_t B) { return D == 64 ? 1200 : B >= 4 ? 880 : 528; }
+//
+// Through a window no block is longer than another, and the other kernel's blocks of 128 rows
+// walk 96 keys more than 32 rows need: 16 heads of 128, one prompt of 3000, window 300 (384)
+// 54 / 62; 3500, 1000 (448) 115 / 116; 4000, 1000 (512) 135 / 124; 13 of 5003, 300 (832) 87 / 92; 8 of
+// 8000, 300 (1120) 139 / 133. Heads of 64: one of 8000, 300 (882) 58 / 73; 16000, 300 (1764) 108 / 112;
+// 16000, 1000 (2016) 276 / 271.
+inline int64_t few_groups(int D, int64_t B, bool window)
+{
+    if (D == 64) return window ? 1800 : 1200;
+    return B >= 4 ? 880 : window ? 460 : 528;
+}
 
 // Prompts so short are not prepared: no wavefront has more than one tile of 128 values (two of
 // 64), and the workgroups, whose k and v fill a compute unit's LDS (half of it), run at
@@ -1114,7 +1124,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t rows = tile_slots(a.T, a.B, 32 * W);
-    if (rows * a.heads <= few_groups(D, a.B)) {
+    if (rows * a.heads <= few_groups(D, a.B, WIN)) {
         const int64_t blocks = tile_slots(a.T, a.B, 32);
         attend_shared_kernel<D, WIN><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c),
                                                                                                c_exp - 1, (int)blocks);

@@ -112,7 +112,7 @@ uint64_t wq_attn_decode_window_ws(int64_t B, int64_t heads, int64_t kv_heads, in
 {
     if (check_decode(B, heads, kv_heads, head_dim, max_pages) || check_window(window, sinks) || B == 0) return 0;
     const int64_t most = max_pages * WQ_KV_PAGE;
-    return wq::decode_ws_bytes(B, heads, kv_heads, head_dim, wq::seen_pages(max_pages, at_most(window, most), at_most(sinks, most)));
+    return wq::decode_window_ws_bytes(B, heads, kv_heads, head_dim, max_pages, at_most(window, most), at_most(sinks, most));
 }
 
 int wq_attn_decode_window(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
