@@ -408,7 +408,8 @@ def test_shared(heads, kv, d, prefix, lens):
 
 
 @pytest.mark.parametrize("count,heads,kv,d,prefix,longest", [(16, 16, 8, 128, 1300, 2000), (33, 4, 2, 64, 4000, 100), (70, 14, 2, 64, 2111, 300),
-                                                              (300, 8, 2, 64, 500, 40), (9, 32, 2, 128, 6000, 1500), (150, 2, 1, 128, 1000, 30)])
+                                                              (300, 8, 2, 64, 500, 40), (9, 32, 2, 128, 6000, 1500), (150, 2, 1, 128, 1000, 30),
+                                                              (1, 16, 2, 128, 40000, 700), (3, 16, 8, 128, 6000, 300), (8, 4, 2, 64, 9000, 700), (5, 6, 2, 64, 2500, 1200), (17, 2, 2, 128, 3000, 64)])
 def test_shared_large(count, heads, kv, d, prefix, longest):
     """More rows than a workgroup holds, prefixes in many runs, own tokens that are cut."""
     note(f"shared large {count} {heads} {kv} {d} {prefix} {longest}")

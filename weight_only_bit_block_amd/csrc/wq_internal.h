@@ -237,6 +237,7 @@ struct DecodeArgs {
     int64_t out_stride;
     void *ws;
     int64_t window, sinks;                      // window 0: all keys
+    int query_heads;                            // Form::prefix: heads of a query and key/value head
     float *sums;                                // Form::sums: [B][heads][2], maximum (log2) and sum of weights of whole sequences
 };
 struct SharedArgs {

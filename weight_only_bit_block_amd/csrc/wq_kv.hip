@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t by_h
 // ---------------------------------------------------------------- decode attention
 // (the work of a workgroup: wq_kv_decode.h)
 template <int D, int H, int WPS, Form FORM>
-__global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeArgs a, int groups, bool cut, float c_man, int c_exp)
+__global__ __launch_bounds__(64 * kDecodeWaves, WPS) void decode_kernel(DecodeArgs a, int groups, int cut, float c_man, int c_exp)
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[decode_lds_bytes(D, H)];
     decode_job<D, H, FORM>(a, groups, cut, c_man, c_exp, lds, blockIdx.x, threadIdx.x);
@@ -242,14 +242,14 @@ uint64_t decode_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t hea
 uint64_t decode_window_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t window, int64_t sinks)
 {
     const int per_step = (int)kv_heads * head_groups((int)heads, (int)kv_heads);
-    return cut_call(B, per_step, max_pages, window, sinks) ? pieces_bytes(per_step, head_dim) : 0;
+    return cut_call(B, per_step, max_pages, window, sinks) ? pieces_bytes(per_step, runs_per_head(per_step), head_dim) : 0;
 }
 
 hipError_t launch_attn_decode(const DecodeArgs &a, hipStream_t stream)
 {
     const int kv = a.cache.kv_heads, group = a.heads / kv, groups = head_groups(a.heads, kv), per_step = kv * groups;
-    const bool cut = cut_call(a.B, per_step, a.max_pages, a.window, a.sinks);
-    const unsigned grid = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : a.B));
+    const int cut = cut_call(a.B, per_step, a.max_pages, a.window, a.sinks) ? runs_per_head(per_step) : 0;
+    const unsigned grid = (unsigned)((int64_t)per_step * (cut ? cut : a.B));
     int c_exp = 0;
     const double c = frexp((double)a.scale * 1.4426950408889634, &c_exp);      // softmax in powers of two
     const float c_man = (float)(2.0 * c);

@@ -250,10 +250,10 @@ __device__ __forceinline__ Run find_run(const DecodeArgs &a, int run, int runs)
 
 constexpr int kPartialExtra = 4;             // a partial result: D values, then m and l, 16-byte aligned
 
-// Bytes of the pieces of a launch that is cut.
-inline uint64_t pieces_bytes(int per_step, int64_t head_dim)
+// Bytes of the pieces of a launch that is cut into so many runs for every kv head and group of heads.
+inline uint64_t pieces_bytes(int per_step, int runs, int64_t head_dim)
 {
-    return kCutMaxSeqs * sizeof(Pieces) + (uint64_t)per_step * runs_per_head(per_step) * kSlots * kMaxGroup * (uint64_t)(head_dim + kPartialExtra) * 4;
+    return kCutMaxSeqs * sizeof(Pieces) + (uint64_t)per_step * runs * kSlots * kMaxGroup * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
 
 // Piece `slot` of a workgroup, head hh.
@@ -263,19 +263,47 @@ __device__ __forceinline__ float *partial(const DecodeArgs &a, int64_t group, in
     return (float *)((Pieces *)a.ws + kCutMaxSeqs) + ((group * kSlots + slot) * kMaxGroup + hh) * (D + kPartialExtra);
 }
 
-// What a call asks for: all keys, those of a window, or all with the maximum and
-// sum of each whole sequence's weights beside its output.
-enum class Form { plain, window, sums };
+// What a call asks for: all keys, those of a window, all with the maximum and sum
+// of each whole sequence's weights beside its output, or parts of one sequence, a
+// prefix, for the queries of a batch (its heads are the batch's rows).
+enum class Form { plain, window, sums, prefix };
+
+// The runs of pages of a prefix, from its length, which is on the device: whole
+// numbers of `unit` pages.
+struct PrefixRuns {
+    int64_t len;
+    int pages, per, count;                   // pages in all, of a run, runs
+    bool bad;
+};
+__device__ __forceinline__ PrefixRuns prefix_runs(const int32_t *len, int64_t most_pages, int runs, int unit)
+{
+    PrefixRuns r;
+    r.len = *len;
+    r.bad = r.len < 0 || r.len > most_pages * kTile;
+    if (r.bad) r.len = 0;
+    r.pages = (int)((r.len + kTile - 1) / kTile);
+    const int units = (r.pages + unit - 1) / unit;
+    r.per = runs > 0 ? (units + runs - 1) / runs * unit : 0;
+    r.count = r.per > 0 ? (r.pages + r.per - 1) / r.per : 0;
+    return r;
+}
+
+// Where a run's result for a row of a key/value head is: D values, then maximum and sum.
+__device__ __forceinline__ float *prefix_part(float *parts, int64_t run, int kv_heads, int kh, int64_t rows, int64_t row, int D)
+{
+    return parts + ((run * kv_heads + kh) * rows + row) * (D + kPartialExtra);
+}
 
 // LDS of a job: every wavefront's buffers, then the state they are joined by.
 constexpr int decode_wave_bytes(int D) { return 2 * (kTile * D / 2 + kTile * D / 32 * 2) + kTile * 32; }
 constexpr int decode_lds_bytes(int D, int H) { return kDecodeWaves * (decode_wave_bytes(D) + H * 8); }
 
 // The work of kDecodeWaves wavefronts, job `job` of a launch, thread `tid` of it.
+// `cut`: into how many runs the work of a kv head and group of heads is cut, 0: not.
 // (Where a workgroup does several jobs at once, their wavefronts meet at more barriers than they
 // need; those that are done do not hold up the others.)
 template <int D, int H, Form FORM>
-__device__ __forceinline__ void decode_job(const DecodeArgs &a, int groups, bool cut, float c_man, int c_exp, uint8_t *lds, unsigned job, int tid)
+__device__ __forceinline__ void decode_job(const DecodeArgs &a, int groups, int cut, float c_man, int c_exp, uint8_t *lds, unsigned job, int tid)
 {
     constexpr bool WIN = FORM == Form::window;
     constexpr int NB = D / 32, BC = 8 / H, R = NB / BC;          // blocks, of them side by side, chains
@@ -293,8 +321,12 @@ __device__ __forceinline__ void decode_job(const DecodeArgs &a, int groups, bool
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t cap = a.max_pages * kTile;
     Run at = {run, 0, 0x7FFFFFFF, 0};                            // not cut: a whole sequence
-    if (cut) {
-        at = find_run<WIN>(a, run, runs_per_head(per_step));
+    if constexpr (FORM == Form::prefix) {
+        const PrefixRuns runs = prefix_runs(a.lens, a.max_pages, cut, kDecodeWaves);
+        if (run >= runs.count) return;
+        at = Run{0, run * (runs.per / kDecodeWaves), runs.per / kDecodeWaves, 0};
+    } else if (cut) {
+        at = find_run<WIN>(a, run, cut);
         if (at.left <= 0) return;
     } else if (a.lens[run] <= 0 || a.lens[run] > cap) {
         for (int i = tid; i < heads * D; i += 64 * kDecodeWaves)
@@ -317,6 +349,10 @@ next_sequence:
         const int h = ((c >> 2) & 1) * HL + (c & 3) / BC;
         const bool live = h < heads;
         const float *src = a.q + (int64_t)b * a.q_stride + (head0 + (live ? h : 0)) * D;
+        if constexpr (FORM == Form::prefix) {
+            const int row = hg * per + (live ? h : 0), q = row / a.query_heads;
+            src = a.q + q * a.q_stride + (kh * a.query_heads + (row - q * a.query_heads)) * D;
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -600,7 +636,14 @@ next_sequence:
             ll = fmaf(by, state[w][hh][1], ll);
             o = fmaf(by, rs[rw * D + d] + rs[(8 + rw) * D + d], o);
         }
-        if (whole) {
+        if constexpr (FORM == Form::prefix) {
+            float *p = prefix_part((float *)a.ws, run, kv, kh, group, hg * per + hh, D);
+            p[d] = o;
+            if (d == 0) {
+                p[D] = mm;
+                p[D + 1] = ll;
+            }
+        } else if (whole) {
             a.out[(int64_t)b * a.out_stride + head0 * D + i] = o / ll;
             if (FORM == Form::sums && d == 0) {
                 float *sums = a.sums + ((int64_t)b * a.heads + head0 + hh) * 2;
@@ -616,7 +659,7 @@ next_sequence:
             }
         }
     }
-    if (!cut) return;
+    if (FORM == Form::prefix || !cut) return;
     if (at.skip == 0 && kh == 0 && hg == 0 && tid == 0) {
         // the rest of the sequence fills runs of `span` from the next run's beginning on
         const int rest = all - mine;

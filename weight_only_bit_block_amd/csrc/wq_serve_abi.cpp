@@ -136,7 +136,7 @@ int wq_attn_decode_window(const wq_kv_cache *cache, const float *q, int64_t q_st
     const int64_t most = max_pages * WQ_KV_PAGE;
     // (no pages: every length but 0 is out of range, whatever the window)
     const wq::DecodeArgs a = {*cache, q, q_stride, (int)heads, lens, (int)B, table, max_pages, scale, out, out_stride, workspace,
-                              at_most(window, most), at_most(sinks, most), nullptr};
+                              at_most(window, most), at_most(sinks, most), 0, nullptr};
     return hip_status(wq::launch_attn_decode(a, stream));
 }
 
@@ -165,7 +165,7 @@ int wq_attn_decode_shared(const wq_kv_cache *cache, const float *q, int64_t q_st
     st = check_ws(workspace, workspace_bytes,
                   wq::shared_ws_bytes(B, heads, cache->kv_heads, cache->head_dim, max_pages, prefix_pages));
     if (st) return st;
-    const wq::SharedArgs a = {{*cache, q, q_stride, (int)heads, lens, (int)B, table, max_pages, scale, out, out_stride, workspace, 0, 0, nullptr},
+    const wq::SharedArgs a = {{*cache, q, q_stride, (int)heads, lens, (int)B, table, max_pages, scale, out, out_stride, workspace, 0, 0, 0, nullptr},
                               prefix, prefix_len, prefix_pages};
     return hip_status(wq::launch_attn_decode_shared(a, stream));
 }

@@ -44,30 +44,6 @@ constexpr int kScaleTop = 12;                // |code| <= 8: values stay below 2
 __device__ __forceinline__ f16v mfma(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
 
-// The run of pages of a workgroup, from the prefix's length, which is on the device.
-struct PrefixRuns {
-    int64_t len;
-    int pages, per, count;                   // pages in all, of a run, runs
-    bool bad;
-};
-__device__ __forceinline__ PrefixRuns prefix_runs(const SharedArgs &a, int chunks)
-{
-    PrefixRuns r;
-    r.len = *a.prefix_len;
-    r.bad = r.len < 0 || r.len > a.prefix_pages * kTile;
-    if (r.bad) r.len = 0;
-    r.pages = (int)((r.len + kTile - 1) / kTile);
-    r.per = chunks > 0 ? (r.pages + chunks - 1) / chunks : 0;
-    r.count = r.per > 0 ? (r.pages + r.per - 1) / r.per : 0;
-    return r;
-}
-
-// Where a run's result for a row of a key/value head is: D values, then maximum and sum.
-__device__ __forceinline__ float *shared_part(float *parts, int64_t run, int kv_heads, int kh, int64_t rows, int64_t row, int D)
-{
-    return parts + ((run * kv_heads + kh) * rows + row) * (D + kPartialExtra);
-}
-
 // Place of 16 bytes (8 values, `piece` of the row's D / 8) of a key's v in LDS, in
 // bytes: written by 16 keys at once and read by 4 keys and 4 pieces, on different banks.
 template <int D>
@@ -97,7 +73,7 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
     // key/value heads next to each other: ids go round the 8 XCDs
     const int kh = job % kv, run = job / kv % chunks;
     const int64_t block = job / kv / chunks;
-    const PrefixRuns runs = prefix_runs(a, chunks);
+    const PrefixRuns runs = prefix_runs(a.prefix_len, a.prefix_pages, chunks, 1);
     if (run >= runs.count) return;
     const int page0 = run * runs.per, page_end = page0 + runs.per < runs.pages ? page0 + runs.per : runs.pages;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -112,7 +88,7 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
     bool bad = false;
     if (own.cache.n_pages <= 0) {            // no page to read at all
         if (live && kw == 0 && half == 0) {
-            float *dst = shared_part(parts, run, kv, kh, rows, row, D);
+            float *dst = prefix_part(parts, run, kv, kh, rows, row, D);
             for (int i = 0; i < D; ++i) dst[i] = 0.0f;
             dst[D] = -3.0e38f;
             dst[D + 1] = __builtin_nanf("");
@@ -375,7 +351,7 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
     const float m1 = res[D], l1 = res[D + 1], mm = fmaxf(m, m1);
     const float by0 = __builtin_amdgcn_exp2f(m - mm), by1 = __builtin_amdgcn_exp2f(m1 - mm);
     const int e = v_exp - kScaleTop - kWeightBits;
-    float *dst = shared_part(parts, run, kv, kh, rows, row, D);
+    float *dst = prefix_part(parts, run, kv, kh, rows, row, D);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -395,7 +371,7 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
 // A step: workgroups of the sequences' own tokens, RW / 2 jobs each, then those of
 // the prefix. Apart, either would wait for the other's last.
 template <int D, int RW, int H>
-__global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp, int groups, bool cut, unsigned own_jobs)
+__global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp, int groups, int cut, unsigned own_jobs)
 {
     constexpr int kJobs = RW / 2, kJobBytes = (decode_lds_bytes(D, H) + 15) / 16 * 16;
     __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(prefix_lds_bytes(D, RW), kJobs * kJobBytes)];
@@ -409,13 +385,34 @@ __global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float
     prefix_job<D, RW>(a, parts, chunks, c_man, c_exp, lds, blockIdx.x - own_groups);
 }
 
+// The same for few rows: the prefix as one sequence of the attention of single
+// tokens, whose heads are the rows, 8 a workgroup.
+template <int D, int H>
+__global__ __launch_bounds__(64 * kDecodeWaves, 2) void shared_few_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp, int groups, int cut, unsigned own_jobs)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(decode_lds_bytes(D, H), decode_lds_bytes(D, kMaxGroup))];
+    if (blockIdx.x < own_jobs) {
+        decode_job<D, H, Form::sums>(a.own, groups, cut, c_man, c_exp, lds, blockIdx.x, threadIdx.x);
+        return;
+    }
+    DecodeArgs p = a.own;
+    p.query_heads = p.heads / p.cache.kv_heads;
+    p.heads = p.cache.kv_heads * p.B * p.query_heads;
+    p.B = 1;
+    p.lens = a.prefix_len;
+    p.table = a.prefix;
+    p.max_pages = a.prefix_pages;
+    p.ws = parts;
+    decode_job<D, kMaxGroup, Form::prefix>(p, head_groups(p.heads, p.cache.kv_heads), chunks, c_man, c_exp, lds, blockIdx.x - own_jobs, threadIdx.x);
+}
+
 // Joins a head's parts in order: those of its own tokens, then the prefix's runs.
 // As wq_kv.hip's join: a thread takes 4 values of every kJoinParts-th part and asks
 // for kJoinAhead of them at once.
 constexpr int kJoinParts = 8, kJoinAhead = 4;
 
 template <int D>
-__global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedArgs a, float *parts, int chunks, int groups, bool cut)
+__global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedArgs a, float *parts, int chunks, int unit, int groups, int cut)
 {
     constexpr int V = D / 4;
     __shared__ f4 red[kJoinParts][V];
@@ -423,7 +420,7 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
     const DecodeArgs &own = a.own;
     const int b = blockIdx.x / own.heads, j = blockIdx.x % own.heads, c = threadIdx.x % V, part = threadIdx.x / V;
     const int64_t len = own.lens[b];
-    const PrefixRuns runs = prefix_runs(a, chunks);
+    const PrefixRuns runs = prefix_runs(a.prefix_len, a.prefix_pages, chunks, unit);
     f4 *out = (f4 *)(own.out + (int64_t)b * own.out_stride + j * D) + c;
     if (runs.bad || len < 0 || len > own.max_pages * kTile || (len == 0 && runs.len == 0)) {
         const float y = runs.bad || len != 0 ? __builtin_nanf("") : 0.0f;
@@ -449,7 +446,7 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
             po[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
             if (i < count) {
                 const float *p;
-                if (i >= mine) p = shared_part(parts, i - mine, kv, kh, rows, row, D);
+                if (i >= mine) p = prefix_part(parts, i - mine, kv, kh, rows, row, D);
                 else if (mine > 1) p = partial<D>(own, (int64_t)(at.first + i) * per_step + hg * kv + kh, i == 0 ? at.slot : 0, hh);
                 else p = nullptr;
                 if (p) {
@@ -501,66 +498,99 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
 }
 
 // ---- how the prefix is cut
-// Workgroups of 64 or 128 rows, two on each compute unit, as many runs of pages as that takes.
+// Workgroups of 8 rows (few_rows), of 64, two on each compute unit, or of 128, one; as many runs of pages
+// as that takes. Measured, 8 / 64 rows (us a call, prefixes of 32768, heads of 128, 8 key/value heads): 8 rows
+// 30.8 / 41.9, 16 35.5 / 43.1, 24 43.5 / 44.7, 32 47.0 / 45.8; of 16000, heads of 64: 16 rows 19.2 / 24.3, 32
+// 22.4 / 26.2; prefixes of 2048 the same within 1 us. 64 / 128 rows: 32768, 64 rows 52 / 62.
+inline int64_t few_rows(int64_t head_dim) { return head_dim == 64 ? 32 : 24; }
 constexpr int kSharedFill = 512;
 inline int row_waves(int64_t rows) { return rows <= 64 ? 2 : 4; }
-inline int64_t row_blocks(int64_t rows) { return (rows + 32 * row_waves(rows) - 1) / (32 * row_waves(rows)); }
-inline int64_t prefix_chunks(int64_t B, int64_t heads, int64_t kv_heads, int64_t prefix_pages)
+inline int64_t row_blocks(int64_t rows, int64_t head_dim)
 {
-    const int64_t rows = B * (heads / kv_heads), blocks = row_blocks(rows) * kv_heads;
-    const int64_t n = kSharedFill * 2 / row_waves(rows) / blocks;
-    return n > prefix_pages ? prefix_pages : n < 1 ? (prefix_pages > 0) : n;
+    const int64_t of = rows <= few_rows(head_dim) ? kMaxGroup : 32 * row_waves(rows);
+    return (rows + of - 1) / of;
 }
-// A sequence's own tokens are cut whenever that makes parts: there is a join anyway.
-inline bool cut_own(int64_t B, int64_t max_pages) { return B <= kCutMaxSeqs && max_pages > kDecodeWaves; }
+inline int run_unit(int64_t rows, int64_t head_dim) { return rows <= few_rows(head_dim) ? kDecodeWaves : 1; }        // pages
+// A sequence's own tokens are cut whenever that makes parts, since there is a join anyway, into no more
+// runs than there can be steps; the prefix into as many as fill what is left of the card, half of it at
+// least, and all of it where its runs are longer than kRunPages.
+constexpr int kRunPages = 4;
+struct SharedCut {
+    int groups, per_step;                        // of the sequences' own heads
+    int own, chunks;                             // runs of own tokens (0: whole sequences), of the prefix
+    int waves, together;                         // row_waves (0: few rows), own jobs of a workgroup
+    unsigned own_jobs;
+    int64_t blocks;                              // of rows and key/value heads
+};
+inline SharedCut shared_cut(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
+{
+    SharedCut c;
+    const int64_t rows = B * (heads / kv_heads), steps = (max_pages + kDecodeWaves - 1) / kDecodeWaves;
+    c.groups = head_groups((int)heads, (int)kv_heads);
+    c.per_step = (int)kv_heads * c.groups;
+    const int64_t most = runs_per_head(c.per_step);
+    c.own = B > kCutMaxSeqs || steps <= 1 ? 0 : (int)(B * steps < most ? B * steps : most);
+    c.own_jobs = (unsigned)((int64_t)c.per_step * (c.own ? c.own : B));
+    c.waves = rows <= few_rows(head_dim) ? 0 : row_waves(rows);
+    c.together = c.waves == 4 ? 2 : 1;
+    c.blocks = row_blocks(rows, head_dim) * kv_heads;
+    const int64_t slots = c.waves == 4 ? kSharedFill / 2 : kSharedFill, taken = (c.own_jobs + c.together - 1) / c.together;
+    const int64_t unit = run_unit(rows, head_dim), units = (prefix_pages + unit - 1) / unit;
+    const int64_t left = (taken > slots / 2 ? slots / 2 : slots - taken) / c.blocks, all = slots / c.blocks;
+    int64_t n = prefix_pages / kRunPages < all ? prefix_pages / kRunPages : all;
+    if (n < left) n = left;
+    c.chunks = (int)(n > units ? units : n < 1 ? (units > 0) : n);
+    return c;
+}
 inline uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 inline uint64_t sums_bytes(int64_t B, int64_t heads) { return round256((uint64_t)B * heads * 8); }
-inline uint64_t own_bytes(int64_t B, int per_step, int64_t head_dim, int64_t max_pages) { return cut_own(B, max_pages) ? round256(pieces_bytes(per_step, head_dim)) : 0; }
+inline uint64_t own_bytes(const SharedCut &c, int64_t head_dim) { return c.own ? round256(pieces_bytes(c.per_step, c.own, head_dim)) : 0; }
 
 }  // namespace
 
 uint64_t shared_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
 {
-    const int per_step = (int)kv_heads * head_groups((int)heads, (int)kv_heads);
-    return own_bytes(B, per_step, head_dim, max_pages) + sums_bytes(B, heads) +
-           (uint64_t)prefix_chunks(B, heads, kv_heads, prefix_pages) * B * heads * (uint64_t)(head_dim + kPartialExtra) * 4;
+    const SharedCut c = shared_cut(B, heads, kv_heads, head_dim, max_pages, prefix_pages);
+    return own_bytes(c, head_dim) + sums_bytes(B, heads) + (uint64_t)c.chunks * B * heads * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
 
 hipError_t launch_attn_decode_shared(const SharedArgs &args, hipStream_t stream)
 {
     SharedArgs a = args;
     DecodeArgs &own = a.own;
-    const int kv = own.cache.kv_heads, group = own.heads / kv, groups = head_groups(own.heads, kv), per_step = kv * groups;
-    const int per = (group + groups - 1) / groups, D = own.cache.head_dim;
-    const int64_t rows = (int64_t)own.B * group;
-    const int chunks = (int)prefix_chunks(own.B, own.heads, kv, a.prefix_pages), rw = row_waves(rows);
-    const bool cut = cut_own(own.B, own.max_pages);
-    char *ws = (char *)own.ws + own_bytes(own.B, per_step, D, own.max_pages);
+    const int D = own.cache.head_dim, group = own.heads / own.cache.kv_heads;
+    const SharedCut cut = shared_cut(own.B, own.heads, own.cache.kv_heads, D, own.max_pages, a.prefix_pages);
+    const int per = (group + cut.groups - 1) / cut.groups;
+    char *ws = (char *)own.ws + own_bytes(cut, D);
     own.sums = (float *)ws;
     float *parts = (float *)(ws + sums_bytes(own.B, own.heads));
     int c_exp = 0;
     const double c = frexp((double)own.scale * 1.4426950408889634, &c_exp);    // softmax in powers of two
-    const unsigned own_jobs = (unsigned)((int64_t)per_step * (cut ? runs_per_head(per_step) : own.B));
-    const unsigned grid = (own_jobs + rw / 2 - 1) / (rw / 2) + (unsigned)(row_blocks(rows) * kv * chunks);
-    const auto start = [&](auto kernel) { kernel<<<grid, 128 * rw, 0, stream>>>(a, parts, chunks, (float)(2.0 * c), c_exp - 1, groups, cut, own_jobs); };
-    const auto pick = [&](auto waves) {
-        constexpr int RW = decltype(waves)::value;
-        if (D == 128) {
-            if (per <= 2) start(shared_kernel<128, RW, 2>);
-            else if (per <= 4) start(shared_kernel<128, RW, 4>);
-            else start(shared_kernel<128, RW, 8>);
-        } else {
-            if (per <= 4) start(shared_kernel<64, RW, 4>);
-            else start(shared_kernel<64, RW, 8>);
-        }
+    const unsigned grid = (cut.own_jobs + cut.together - 1) / cut.together + (unsigned)(cut.blocks * cut.chunks);
+    const auto start = [&](auto kernel) {
+        kernel<<<grid, cut.waves == 4 ? 512 : 256, 0, stream>>>(a, parts, cut.chunks, (float)(2.0 * c), c_exp - 1, cut.groups, cut.own, cut.own_jobs);
     };
-    if (rw == 2) pick(std::integral_constant<int, 2>{});
-    else pick(std::integral_constant<int, 4>{});
+    const auto pick = [&](auto dim, auto heads) {
+        constexpr int DIM = decltype(dim)::value, H = decltype(heads)::value;
+        if (cut.waves == 0) start(shared_few_kernel<DIM, H>);
+        else if (cut.waves == 2) start(shared_kernel<DIM, 2, H>);
+        else start(shared_kernel<DIM, 4, H>);
+    };
+    using std::integral_constant;
+    if (D == 128) {
+        if (per <= 2) pick(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+        else if (per <= 4) pick(integral_constant<int, 128>{}, integral_constant<int, 4>{});
+        else pick(integral_constant<int, 128>{}, integral_constant<int, 8>{});
+    } else {
+        if (per <= 4) pick(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+        else pick(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned jobs = (unsigned)((int64_t)own.B * own.heads);
-    if (D == 128) shared_join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, parts, chunks, groups, cut);
-    else shared_join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, parts, chunks, groups, cut);
+    const int unit = run_unit((int64_t)own.B * group, D);
+    if (D == 128) shared_join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, parts, cut.chunks, unit, cut.groups, cut.own);
+    else shared_join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, parts, cut.chunks, unit, cut.groups, cut.own);
     return hipGetLastError();
 }
 
