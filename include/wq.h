@@ -449,8 +449,8 @@ int wq_residual_norm(const float *h, const float *y, const float *post_weight, c
  * be null when not wanted. A request with a negative length, or of more than
  * 2^31 - 1 tokens, gets no token and no page, and lens -1. B is below 2^24,
  * max_pages below 2^25, n_free below 2^31, T below 2^30. taken_out must not be
- * taken, and no other output may alias an input: the same inputs give the same
- * plan again.
+ * taken (WQ_ERR_SHAPE), and no other output may alias an input: the same inputs
+ * give the same plan again.
  */
 int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *table, int64_t max_pages,
                const int32_t *free_pages, int64_t n_free, const int32_t *taken, int64_t T, int32_t *cu, int32_t *lens,
@@ -470,7 +470,7 @@ int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *t
  * in fp32; sums of squares in fp32, of values brought into its range where
  * the squares leave it. Error: 28 2^-24 |factor| of the larger of |y_i| and |y_i'|,
  * and as much of it as 4 times the angle's error.
- * heads and kv_heads may be any number, one of them 0 (its pointers null then).
+ * T is below 2^24. heads and kv_heads may be any number, one of them 0 (its pointers null then).
  * Rows of tokens with a negative position are not written. q_out may be q and
  * k_out may be k (with the same stride); no other aliasing.
  */

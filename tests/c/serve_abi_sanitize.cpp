@@ -39,7 +39,7 @@ hipError_t launch_attn_decode_shared(const SharedArgs &a, hipStream_t)
 hipError_t launch_qk_norm_rope(const RopeArgs &a, bool, bool, hipStream_t)
 {
     ++launches;
-    if (a.T <= 0 || a.pairs * 2 > a.head_dim || a.heads + a.kv_heads < 1) ++failures;
+    if (a.T <= 0 || a.T >= (1 << 24) || a.pairs * 2 > a.head_dim || a.heads + a.kv_heads < 1) ++failures;
     return hipSuccess;
 }
 hipError_t launch_kv_plan(const PlanArgs &a, hipStream_t)
@@ -87,7 +87,7 @@ int main()
         wq_attn_decode_shared(&c, F, st, h, I, window, I, I, B, I, W, 1.0f, F, st, F, ws, nullptr);
         wq_kv_append_slots(&c, F, st, F, st, T, L, nullptr);
         wq_qk_norm_rope(F, st, h, F, st, kv, d, T, I, F, pick(32), 0, 1.0f, 1, F, F, 1e-6f, F, st, F, st, nullptr);
-        wq_kv_plan(I, I, B, I, W, I, pick(9), I, T, I, I, I, L, I, nullptr);
+        wq_kv_plan(I, I, B, I, W, I, pick(9), I, T, I, I, I, L, I + 64, nullptr);
     }
     if (launches < 100000) {
         std::fprintf(stderr, "only %d launches\n", launches);

@@ -700,6 +700,59 @@ def test_serving_calls_on_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(g, want))
 
 
+def test_serving_past_four_gib():
+    """Pages whose byte offsets pass 32 bits: slots, windows and a shared prefix."""
+    note("serving past 4 GiB")
+    torch = torch_cuda()
+    n, kv, d, heads = 140000, 8, 128, 16           # 4.27 GiB of codes each for keys and values
+    big = wqa.KVCache(*(torch.empty((n, kv, 64, w), dtype=t, device="cuda")
+                        for w, t in ((64, torch.uint8), (4, torch.int16), (64, torch.uint8), (4, torch.int16))))
+    rng = rng_for(93)
+    T = 1200
+    _, (q, k, v) = qkv(rng, T, heads, kv, d)
+    ids = np.array([n - 1, 0, 131072, 131071] + list(range(n - 20, n - 5)), np.int64)
+    small = wqa.KVCache.empty(len(ids), kv, d)
+    t = np.arange(T)
+    wqa.kv_append(big, k, v, slots=dev(ids[t // 64] * 64 + t % 64))
+    wqa.kv_append(small, k, v, slots=dev(t.astype(np.int64)))
+    at = torch.from_numpy(ids).cuda()
+    assert all(torch.equal(a[at][:18], b[:18]) for a, b in zip(big, small))
+    for rows in (2, 40):
+        ln = ints([T - 3 * i for i in range(rows)])
+        qr = q[:rows].contiguous()
+        for c, tab in ((big, ids), (small, np.arange(len(ids)))):
+            table = ints(np.tile(tab, (rows, 1)))
+            got = (wqa.attn_decode(qr, c, table, ln, window=700, sinks=3),
+                   wqa.attn_decode_shared(qr, c, table[0], ln[:1], table[:, :3].contiguous(), ln.clamp(max=150)))
+            if c is big:
+                want = got
+        assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_serving_random_shapes(seed):
+    """Sizes no list has: windows of prompts and of single tokens, shared prefixes."""
+    torch = torch_cuda()
+    rng = rng_for(94, seed)
+    heads, kv, d = [(16, 8, 128), (4, 4, 64), (14, 2, 64), (12, 1, 128), (6, 3, 128), (9, 1, 64), (34, 2, 64)][rng.integers(7)]
+    window, sinks = int(np.exp(rng.uniform(0, 7))), int(rng.choice([0, 1, 5, 31, 64, 100]))
+    lens = [int(x) for x in rng.integers(0, int(rng.choice([5, 70, 400])), rng.integers(1, 9))]
+    note(f"random {seed} {heads} {kv} {d} {window} {sinks} {lens}")
+    host, (q, k, v) = qkv(rng, sum(lens) + 1, heads, kv, d)
+    out = torch.full((sum(lens) + 1, heads, d), NAN, device="cuda")
+    wqa.attn_prefill(q, k, v, cu=cu_of(lens), out=out, window=window, sinks=sinks)
+    check_window_prompt(out, host, lens, d ** -0.5, window, sinks)
+    count, prefix = int(rng.integers(1, 60)), int(rng.integers(0, 3000))
+    lens = [int(x) for x in rng.integers(0, int(rng.choice([3, 200, 2500])), count)]
+    pre, table, host, cache, q = shared_case(rng, heads, kv, d, prefix, lens)
+    kval, vval = ref.values(host[0], host[1]), ref.values(host[2], host[3])
+    out = wqa.attn_decode(dev(q), cache, dev(table), ints(lens), window=window, sinks=sinks)
+    want, sums = sref.decode(q, kval, vval, host[3], d ** -0.5, lambda b: [(table[b], lens[b], sref.seen(lens[b], window, sinks))])
+    check_rows(out, want, sums, min(max(lens), window + sinks), d)
+    out = wqa.attn_decode_shared(dev(q), cache, dev(pre), ints([prefix]), dev(table), ints(lens))
+    check_shared(out, q, host, pre, prefix, table, lens, d ** -0.5)
+
+
 def test_serving_refusals():
     torch = torch_cuda()
     q, k = torch.zeros((4, 4, 64), device="cuda"), torch.zeros((4, 2, 64), device="cuda")

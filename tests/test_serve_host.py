@@ -24,7 +24,7 @@ def _rope(lib, **kw):  # noqa: F811
 
 def test_rope_refusals(lib):  # noqa: F811
     assert _rope(lib, T=0) == OK and _rope(lib, H=0, Hk=0, q=None, k=None) == OK
-    for bad in (dict(D=96), dict(D=256), dict(T=-1), dict(T=1 << 30), dict(H=-1), dict(Hk=-1), dict(H=1 << 23), dict(Hk=1 << 40), dict(pairs=65),
+    for bad in (dict(D=96), dict(D=256), dict(T=-1), dict(T=1 << 24), dict(H=-1), dict(Hk=-1), dict(H=1 << 23), dict(Hk=1 << 40), dict(pairs=65),
                 dict(pairs=-4), dict(pairs=6), dict(D=64, pairs=36), dict(qs=2044), dict(qs=2050), dict(ks=1 << 30), dict(qos=1024), dict(kos=1026)):
         assert _rope(lib, **bad) == SHAPE, bad
     for bad in (dict(q=None), dict(k=None), dict(qo=None), dict(ko=None), dict(pos=None), dict(inv=None)):
@@ -34,19 +34,19 @@ def test_rope_refusals(lib):  # noqa: F811
 
 
 def _plan(lib, **kw):  # noqa: F811
-    a = dict(fresh=FAKE, start=FAKE, B=3, table=FAKE, W=4, free=FAKE, F=9, taken=FAKE, T=5, cu=FAKE, lens=FAKE, pos=FAKE, slots=FAKE, out=FAKE)
+    a = dict(fresh=FAKE, start=FAKE, B=3, table=FAKE, W=4, free=FAKE, F=9, taken=FAKE, T=5, cu=FAKE, lens=FAKE, pos=FAKE, slots=FAKE, out=2 * FAKE)
     a.update(kw)
     return lib.wq_kv_plan(a["fresh"], a["start"], a["B"], a["table"], a["W"], a["free"], a["F"], a["taken"], a["T"], a["cu"], a["lens"],
                           a["pos"], a["slots"], a["out"], None)
 
 
 def test_plan_refusals(lib):  # noqa: F811
-    for bad in (dict(B=-1), dict(B=1 << 24), dict(W=-1), dict(W=1 << 25), dict(F=-1), dict(F=1 << 31), dict(T=-1), dict(T=1 << 30)):
+    for bad in (dict(B=-1), dict(B=1 << 24), dict(W=-1), dict(W=1 << 25), dict(F=-1), dict(F=1 << 31), dict(T=-1), dict(T=1 << 30), dict(out=FAKE)):
         assert _plan(lib, **bad) == SHAPE, bad
     for bad in (dict(fresh=None), dict(table=None), dict(free=None), dict(cu=None), dict(lens=None), dict(out=None)):
         assert _plan(lib, **bad) == NULL, bad
     for name in ("fresh", "start", "table", "free", "taken", "cu", "lens", "pos", "out"):
-        assert _plan(lib, **{name: FAKE + 2}) == ALIGN, name
+        assert _plan(lib, **{name: 3 * FAKE + 2}) == ALIGN, name
     assert _plan(lib, slots=FAKE + 4) == ALIGN
 
 

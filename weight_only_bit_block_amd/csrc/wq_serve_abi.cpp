@@ -37,7 +37,8 @@ int wq_qk_norm_rope(const float *q, int64_t q_stride, int64_t heads, const float
                     int64_t k_out_stride, hipStream_t stream)
 {
     if (head_dim != 64 && head_dim != 128) return WQ_ERR_SHAPE;
-    if (T < 0 || T >= kLim || heads < 0 || kv_heads < 0 || heads >= kLim / head_dim || kv_heads >= kLim / head_dim)
+    // workgroups of 256 threads for 1 token or more, below 2^32 threads in all
+    if (T < 0 || T >= (int64_t)1 << 24 || heads < 0 || kv_heads < 0 || heads >= kLim / head_dim || kv_heads >= kLim / head_dim)
         return WQ_ERR_SHAPE;
     if (pairs < 0 || pairs > head_dim / 2 || pairs % 4 != 0) return WQ_ERR_SHAPE;
     if (T == 0 || heads + kv_heads == 0) return WQ_OK;
@@ -59,6 +60,7 @@ int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *t
     if (B < 0 || B >= kMaxSeqs || max_pages < 0 || max_pages >= (int64_t)1 << 25 || n_free < 0 || n_free >= (int64_t)1 << 31 ||
         T < 0 || T >= kLim)
         return WQ_ERR_SHAPE;
+    if (taken_out && taken_out == taken) return WQ_ERR_SHAPE;     // read by all workgroups, written by one
     if (!cu || !taken_out || (B > 0 && (!fresh || !lens)) || (B > 0 && max_pages > 0 && !table) || (n_free > 0 && !free_pages))
         return WQ_ERR_NULL;
     if (!aligned(fresh, 4) || !aligned(start, 4) || !aligned(table, 4) || !aligned(free_pages, 4) || !aligned(taken, 4) ||
