@@ -10,7 +10,8 @@
 // value changes lanes, only the sum of squares goes over them.
 //
 // Angles: their products and the reduction to a turn in fp64 (a position and a
-// factor of 24 bits: off by 2^-53 of the angle), sine and cosine of what is left in fp32.
+// factor of 24 bits: off by 2^-53 of the angle), sine and cosine in fp32 of what is
+// left, in two parts.
 // They are the same for all heads of a token, so a workgroup makes each of them
 // once, one a thread, while its rows are on the way.
 #include "wq_internal.h"
@@ -101,8 +102,11 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
         float2 z = {1.0f, 0.0f};
         if (pair < a.pairs && t < a.T) {
             const double turns = (double)a.positions[t] * (double)a.inv_freq[pair] * 0.15915494309189533577;
-            const float x = 2.0f * (float)(turns - rint(turns));
-            z = float2{cospif(x) * a.factor, sinpif(x) * a.factor};
+            // half turns in two parts, the second one by its tangent
+            const double half = 2.0 * (turns - rint(turns));
+            const float x = (float)half, rest = 3.14159265f * (float)(half - (double)x);
+            const float c = cospif(x), s = sinpif(x);
+            z = float2{fmaf(-rest, s, c) * a.factor, fmaf(rest, c, s) * a.factor};
         }
         turn[i / (D / 2)][pair] = z;
     }
