@@ -1,11 +1,12 @@
 // wq_plan.hip -- the plan of a serving step from request lengths: token offsets,
 // lengths, positions, pages for the new tokens, and their places in the cache.
 //
-// Bound by latency: a few bytes a token. One launch, whatever the sizes: every
-// workgroup adds up all requests' tokens and pages (kChunk requests at a time, in
-// LDS), and takes its share of the tokens, of the new pages and of the requests.
-// Nothing that one workgroup writes is read by another: a new token's page comes
-// from the list of free ones where it is new, from the table where it was there.
+// Bound by latency: a few bytes a token (64 requests of one token 4.5 us, 24 of
+// 65521 tokens in all 5.1). One launch, whatever the sizes: every workgroup adds up
+// all requests' tokens and pages (kChunk requests at a time, in LDS), and takes its
+// share of the tokens, of the new pages and of the requests. Nothing that one
+// workgroup writes is read by another: a new token's page comes from the list of free
+// ones where it is new, from the table where it was there.
 #include "wq_internal.h"
 
 namespace wq {

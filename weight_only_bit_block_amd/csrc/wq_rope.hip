@@ -5,9 +5,12 @@
 //   (y_i, y_i') -> factor (y_i cos a - y_i' sin a, y_i' cos a + y_i sin a),
 //   a = position * inv_freq[i], for `pairs` pairs; the other values keep y
 //
-// HBM-bound: 8 D bytes for a token and head. A row is D / 8 lanes with two groups
-// of 4 values each, chosen so that a lane holds both sides of its pairs: no
-// value changes lanes, only the sum of squares goes over them.
+// HBM-bound: 8 D bytes for a token and head (8192 tokens of 24 heads of 128: 201 MB,
+// 34 us, 5.9 TB/s with inputs partly in the last-level cache; in a program's turns
+// of inputs 39). A row is D / 8 lanes with two groups of 4 values each, chosen so
+// that a lane holds both sides of its pairs: no value changes lanes, only the sum of
+// squares goes over them. Asking for 2 rows ahead instead of 4 costs as much, 6 more
+// (36.4); stores past the L2: 2048 tokens 10.9 -> 10.2 us, 8192 34.1 -> 34.9.
 //
 // Angles: their products and the reduction to a turn in fp64 (a position and a
 // factor of 24 bits: off by 2^-53 of the angle), sine and cosine in fp32 of what is
@@ -181,7 +184,10 @@ hipError_t launch(const RopeArgs &a, bool norm, bool interleaved, hipStream_t st
 
 hipError_t launch_qk_norm_rope(const RopeArgs &a, bool norm, bool interleaved, hipStream_t stream)
 {
-    if (a.T < 1024) return a.head_dim == 128 ? launch<128, 1>(a, norm, interleaved, stream) : launch<64, 1>(a, norm, interleaved, stream);
+    // Few tokens: a workgroup each, whose wavefronts share its heads; else one wavefront a token, which
+    // computes angles for 4 tokens at once. us in a graph, 1 / 4 tokens: 24 heads of 128, 1 token 3.0 / 4.3, 512 4.2 / 6.1,
+    // 1024 7.1 / 7.3, 2048 11.4 / 10.9, 8192 35.8 / 34.1; 16 heads of 64, 512 3.5 / 3.4, 1003 4.5 / 3.7, 4096 12.4 / 8.5.
+    if (a.T * (128 / a.head_dim) < 1024) return a.head_dim == 128 ? launch<128, 1>(a, norm, interleaved, stream) : launch<64, 1>(a, norm, interleaved, stream);
     return a.head_dim == 128 ? launch<128, 4>(a, norm, interleaved, stream) : launch<64, 4>(a, norm, interleaved, stream);
 }
 

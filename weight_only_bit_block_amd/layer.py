@@ -165,12 +165,15 @@ def _out_heads(out, q, shape, at, name="out"):
     return out, stride
 
 
-def _window(window, sinks):
-    """The checked sizes of a window."""
-    for x, name, least in ((window, "window", 1), (sinks, "sinks", 0)):
-        if not isinstance(x, int) or isinstance(x, bool) or x < least:
-            raise ValueError(f"{name} must be a whole number, {least} at least")
-    return min(window, _MOST), min(sinks, _MOST)
+def _count(x, name, least):
+    """A whole number (of any integer type), at least `least`."""
+    if type(x) is not int:
+        if isinstance(x, bool) or not hasattr(x, "__index__") or isinstance(x, _Tensor):
+            raise ValueError(f"{name} must be a whole number")
+        x = x.__index__()
+    if x < least:
+        raise ValueError(f"{name} must be {least} at least")
+    return x if x < _MOST else _MOST
 
 
 def attn_prefill(q, k, v, cu: Optional[torch.Tensor] = None, scale: Optional[float] = None, out=None, stream=None,
@@ -191,7 +194,7 @@ def attn_prefill(q, k, v, cu: Optional[torch.Tensor] = None, scale: Optional[flo
     pcu, B = _cu(cu, at)
     _need(window is not None or sinks == 0, "sinks need a window")
     if window is not None:
-        window, sinks = _window(window, sinks)
+        window, sinks = _count(window, "window", 1), _count(sinks, "sinks", 0)
     lib = load()
 
     def launch(s):
@@ -266,7 +269,7 @@ def attn_decode(q, cache: KVCache, table, lens, scale: Optional[float] = None, o
     pl = _index(lens, (B,), "lens", at)
     _need(window is not None or sinks == 0, "sinks need a window")
     if window is not None:
-        window, sinks = _window(window, sinks)
+        window, sinks = _count(window, "window", 1), _count(sinks, "sinks", 0)
     lib = load()
 
     def launch(s):
@@ -356,8 +359,7 @@ def kv_plan(fresh, table, free, taken: Optional[torch.Tensor] = None, tokens: in
     pfree = _index(free, (n_free,), "free", at)
     ptaken = None if taken is None else _index(taken, (1,), "taken", at)
     pst = None if start is None else _index(start, (B,), "start", at)
-    if not isinstance(tokens, int) or isinstance(tokens, bool) or tokens < 0:
-        raise ValueError("tokens must be a whole number, 0 at least")
+    tokens = _count(tokens, "tokens", 0)
     if out is not None:
         for t, n, name in ((out.cu, B + 1, "cu"), (out.lens, B, "lens"), (out.positions, tokens, "positions"), (out.taken, 1, "taken")):
             _index(t, (n,), "out." + name, at)
