@@ -633,6 +633,11 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
     const int mine = wrow < len ? wrow / kTileKeys - walk.skip : -1;      // this wave's last tile
     const auto meta_of = [&](int t) __attribute__((always_inline)) { return metas + at0 + walk.tile(t) * step; };
     const auto sight = [&](int t) __attribute__((always_inline)) { return walk.sight(a, walk.tile(t), t == mine, wrow, pos); };
+    // Tiles the block's first rows see and this wave's do not, [firsts, from): of those it walks the one before `from` (for
+    // its first tile's scores) and the one behind the first tokens, all masked; the scores of what lies between stay masked.
+    // (Tiles of first tokens have the same numbers whether any are left out behind them or not.)
+    const int firsts = WIN ? (a.sinks + kTileKeys - 1) / kTileKeys : 0;
+    const int from = WIN ? (wrow >= a.window ? wrow - a.window + 1 : 0) / kTileKeys - walk.skip : 0;
     int odd = 0;
     copy(0, 0);
     TileHead now = head_of(meta_of(0)), next = head_of(meta_of(last > 0 ? 1 : 0));
@@ -649,7 +654,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
         meet();                                  // v of tile t and k of tile t + 1
         if (t < last) copy(t + 1, 1);
         if (t + 1 < last) copy(t + 2, 0);
-        if (t <= mine) {
+        if (t <= mine && !(WIN && t >= firsts && t + 1 < from)) {
             const TileMeta *meta = meta_of(t);
             const int flags = now.flags;
             const h8 *v1 = reinterpret_cast<const h8 *>(buf[t & 1]) + 2 * D * kTileKeys / 8 + lane;
