@@ -423,6 +423,24 @@ def test_shared_large(count, heads, kv, d, prefix, longest):
     check_shared(out, q, host, pre, prefix, table, lens, -0.07)
 
 
+@pytest.mark.parametrize("count,heads,kv,d,prefix,longest", [(40, 4, 2, 128, 9000, 60), (70, 2, 2, 128, 9001, 700), (33, 4, 2, 64, 17000, 50),
+                                                              (200, 14, 2, 64, 16700, 20), (65, 8, 1, 128, 8300, 9)])
+@pytest.mark.parametrize("shown", [1.0, 0.03, 0.0])
+def test_shared_long_tables(count, heads, kv, d, prefix, longest, shown):
+    """Workgroups of 128 rows, with all of a long prefix and with little of it in a table made for all."""
+    note(f"shared long {count} {heads} {kv} {d} {prefix} {longest} {shown}")
+    torch = torch_cuda()
+    rng = rng_for(87, count, prefix)
+    lens = [int(x) for x in rng.integers(0, longest, count)]
+    lens[-1], lens[count // 2] = longest, 0
+    pre, table, host, cache, q = shared_case(rng, heads, kv, d, prefix, lens)
+    seen = int(prefix * shown)
+    pre[-(-seen // 64):] = -3                      # past it: anything
+    out = torch.full(q.shape, NAN, device="cuda")
+    wqa.attn_decode_shared(dev(q), cache, dev(pre), ints([seen]), dev(table), ints(lens), out=out)
+    check_shared(out, q, host, pre, seen, table, lens, d ** -0.5)
+
+
 def test_shared_strides_and_wide_rows():
     note("shared strides")
     torch = torch_cuda()

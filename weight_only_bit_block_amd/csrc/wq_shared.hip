@@ -514,22 +514,23 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
 }
 
 // ---- how the prefix is cut
-// Workgroups of 8 rows (few_rows), of 64, two on each compute unit, or of 128, one; as many runs of pages
-// as that takes. Measured, 8 / 64 rows (us a call, prefixes of 32768, heads of 128, 8 key/value heads): 8 rows
-// 30.8 / 41.9, 16 35.5 / 43.1, 24 43.5 / 44.7, 32 47.0 / 45.8; of 16000, heads of 64: 16 rows 19.2 / 24.3, 32
-// 22.4 / 26.2; prefixes of 2048 the same within 1 us. 64 / 128 rows: 32768, 64 rows 52 / 62.
-inline int64_t few_rows(int64_t head_dim) { return head_dim == 64 ? 32 : 24; }
+// Workgroups of 8 rows (few_rows), of 64, two on each compute unit, or of 128, one. us a call, prefixes in
+// tokens, 8 / 64 rows: heads of 128, 8 key/value heads, 32768 tokens: 8 rows 30.8 / 41.9, 16 35.5 / 43.1, 24 43.5
+// / 44.7, 32 47.0 / 45.8; heads of 64, 16000: 16 rows 19.2 / 24.3, 32 22.4 / 26.2; 2048 tokens the same within 1 us.
+// 64 / 128 rows, 16/8 heads of 128: 64 rows, 32768 tokens 52 / 62; 128 rows, 2048 26.8 / 33.8, 8192 46.5 / 46.6, 16000
+// 55.8 / 55.4, 32768 79 / 77; heads of 64, 14/2, 525 rows: 4000 22.0 / 29.9, 8191 31.5 / 34.1, 16000 38.8 / 40.6.
 constexpr int kSharedFill = 512;
-inline int row_waves(int64_t rows) { return rows <= 64 ? 2 : 4; }
-inline int64_t row_blocks(int64_t rows, int64_t head_dim)
+inline int64_t few_rows(int64_t head_dim) { return head_dim == 64 ? 32 : 24; }
+inline int row_waves(int64_t rows, int64_t head_dim, int64_t prefix_pages)
 {
-    const int64_t of = rows <= few_rows(head_dim) ? kMaxGroup : 32 * row_waves(rows);
-    return (rows + of - 1) / of;
+    return rows <= 64 || prefix_pages <= (head_dim == 64 ? 256 : 128) ? 2 : 4;
 }
 inline int run_unit(int64_t rows, int64_t head_dim) { return rows <= few_rows(head_dim) ? kDecodeWaves : 1; }        // pages
 // A sequence's own tokens are cut whenever that makes parts, since there is a join anyway, into no more
 // runs than there can be steps; the prefix into as many as fill what is left of the card, half of it at
-// least, and all of it where its runs are longer than kRunPages.
+// least, and all of it where its runs are longer than kRunPages. With workgroups of 64 rows own tokens take
+// half of the card at most, so that a short prefix has a place from the start (64 sequences behind 4096
+// tokens 37.7 -> 31.1 us; with those of 128 rows and long prefixes it costs: 64 behind 16000 55.4 -> 58.2).
 constexpr int kRunPages = 4;
 struct SharedCut {
     int groups, per_step;                        // of the sequences' own heads
@@ -544,12 +545,14 @@ inline SharedCut shared_cut(int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     const int64_t rows = B * (heads / kv_heads), steps = (max_pages + kDecodeWaves - 1) / kDecodeWaves;
     c.groups = head_groups((int)heads, (int)kv_heads);
     c.per_step = (int)kv_heads * c.groups;
-    const int64_t most = runs_per_head(c.per_step);
+    int64_t most = runs_per_head(c.per_step);
+    c.waves = rows <= few_rows(head_dim) ? 0 : row_waves(rows, head_dim, prefix_pages);
+    c.together = c.waves == 4 ? 2 : 1;
+    if (c.waves != 4) most = (most + 1) / 2;     // beside the prefix, not before it
     c.own = B > kCutMaxSeqs || steps <= 1 ? 0 : (int)(B * steps < most ? B * steps : most);
     c.own_jobs = (unsigned)((int64_t)c.per_step * (c.own ? c.own : B));
-    c.waves = rows <= few_rows(head_dim) ? 0 : row_waves(rows);
-    c.together = c.waves == 4 ? 2 : 1;
-    c.blocks = row_blocks(rows, head_dim) * kv_heads;
+    const int64_t each = c.waves ? 32 * c.waves : kMaxGroup;
+    c.blocks = (rows + each - 1) / each * kv_heads;
     const int64_t slots = c.waves == 4 ? kSharedFill / 2 : kSharedFill, taken = (c.own_jobs + c.together - 1) / c.together;
     const int64_t unit = run_unit(rows, head_dim), units = (prefix_pages + unit - 1) / unit;
     const int64_t left = (taken > slots / 2 ? slots / 2 : slots - taken) / c.blocks, all = slots / c.blocks;
