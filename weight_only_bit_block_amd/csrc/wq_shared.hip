@@ -422,9 +422,9 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void shared_few_kernel(Shared
     decode_job<D, kMaxGroup, Form::prefix>(p, head_groups(p.heads, p.cache.kv_heads), chunks, c_man, c_exp, lds, blockIdx.x - own_jobs, threadIdx.x);
 }
 
-// Joins a head's parts in order: those of its own tokens, then the prefix's runs.
-// As wq_kv.hip's join: a thread takes 4 values of every kJoinParts-th part and asks
-// for kJoinAhead of them at once.
+// Joins a head's parts: those of the prefix's runs, then its own tokens', each in a
+// fixed order. As wq_kv.hip's join: a thread takes 4 values of every kJoinParts-th part and
+// asks for kJoinAhead of them at once; for the prefix's before it is known how many there are.
 constexpr int kJoinParts = 8, kJoinAhead = 4;
 
 template <int D>
@@ -435,51 +435,31 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
     __shared__ float ml[kJoinParts][2];
     const DecodeArgs &own = a.own;
     const int b = blockIdx.x / own.heads, j = blockIdx.x % own.heads, c = threadIdx.x % V, part = threadIdx.x / V;
-    const int64_t len = own.lens[b];
-    const PrefixRuns runs = prefix_runs(a.prefix_len, a.prefix_pages, chunks, unit);
-    f4 *out = (f4 *)(own.out + (int64_t)b * own.out_stride + j * D) + c;
-    if (runs.bad || len < 0 || len > own.max_pages * kTile || (len == 0 && runs.len == 0)) {
-        const float y = runs.bad || len != 0 ? __builtin_nanf("") : 0.0f;
-        if (part == 0) *out = f4{y, y, y, y};
-        return;
-    }
     const int kv = own.cache.kv_heads, group = own.heads / kv, per_step = kv * groups, per = (group + groups - 1) / groups;
     const int kh = j / group, hg = j % group / per, hh = j % group % per;
     const int64_t rows = (int64_t)own.B * group, row = (int64_t)b * group + j % group;
-    Pieces at = {0, 1, 0, 0};
-    if (cut && len > 0) at = ((const Pieces *)own.ws)[b];
-    const int mine = len > 0 ? at.count : 0, count = mine + runs.count;
+    f4 *out = (f4 *)(own.out + (int64_t)b * own.out_stride + j * D) + c;
     float m = -3.0e38f, l = 0.0f;
     f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i0 = part; i0 < count; i0 += kJoinAhead * kJoinParts) {
-        float pm[kJoinAhead], pl[kJoinAhead];
-        f4 po[kJoinAhead];
-#pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-            const int i = i0 + k * kJoinParts;
-            pm[k] = -3.0e38f;
-            pl[k] = 0.0f;
-            po[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (i < count) {
-                const float *p;
-                if (i >= mine) p = prefix_part(parts, i - mine, kv, kh, rows, row, D);
-                else if (mine > 1) p = partial<D>(own, (int64_t)(at.first + i) * per_step + hg * kv + kh, i == 0 ? at.slot : 0, hh);
-                else p = nullptr;
-                if (p) {
-                    pm[k] = p[D];
-                    pl[k] = p[D + 1];
-                    po[k] = ((const f4 *)p)[c];
-                } else {                     // one piece: divided already
-                    const float *s = own.sums + ((int64_t)b * own.heads + j) * 2;
-                    pm[k] = s[0];
-                    pl[k] = s[1];
-                    po[k] = *out * pl[k];
-                }
-            }
-        }
+    float pm[kJoinAhead], pl[kJoinAhead];
+    f4 po[kJoinAhead];
+    // (an entry of an empty sequence, and a part that no run wrote, may hold anything: they are not used)
+    const auto ask = [&](int k, const float *p) __attribute__((always_inline)) {
+        pm[k] = p[D];
+        pl[k] = p[D + 1];
+        po[k] = ((const f4 *)p)[c];
+    };
+    const auto add = [&](int i0, int count) __attribute__((always_inline)) {
         float mn = m;
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) mn = fmaxf(mn, pm[k]);
+        for (int k = 0; k < kJoinAhead; ++k) {
+            if (i0 + k * kJoinParts >= count) {
+                pm[k] = -3.0e38f;
+                pl[k] = 0.0f;
+                po[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            mn = fmaxf(mn, pm[k]);
+        }
         const float by = __builtin_amdgcn_exp2f(m - mn);
         l *= by;
         o *= by;
@@ -489,6 +469,47 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
             const float f = __builtin_amdgcn_exp2f(pm[k] - m);
             l = fmaf(f, pl[k], l);
             o += f * po[k];
+        }
+    };
+    const auto ask_prefix = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int i = i0 + k * kJoinParts;
+            if (i < chunks) ask(k, prefix_part(parts, i, kv, kh, rows, row, D));
+        }
+    };
+    ask_prefix(part);
+    Pieces at = {0, 1, 0, 0};
+    if (cut) at = ((const Pieces *)own.ws)[b];
+    const int64_t len = own.lens[b];
+    const PrefixRuns runs = prefix_runs(a.prefix_len, a.prefix_pages, chunks, unit);
+    if (runs.bad || len < 0 || len > own.max_pages * kTile || (len == 0 && runs.len == 0)) {
+        const float y = runs.bad || len != 0 ? __builtin_nanf("") : 0.0f;
+        if (part == 0) *out = f4{y, y, y, y};
+        return;
+    }
+    add(part, runs.count);
+    for (int i0 = part + kJoinAhead * kJoinParts; i0 < runs.count; i0 += kJoinAhead * kJoinParts) {
+        ask_prefix(i0);
+        add(i0, runs.count);
+    }
+    const int mine = len > 0 ? at.count : 0;
+    if (mine == 1) {                             // one piece: divided already
+        if (part == 0) {
+            const float *s = own.sums + ((int64_t)b * own.heads + j) * 2;
+            pm[0] = s[0];
+            pl[0] = s[1];
+            po[0] = *out * pl[0];
+            add(0, 1);
+        }
+    } else {
+        for (int i0 = part; i0 < mine; i0 += kJoinAhead * kJoinParts) {
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int i = i0 + k * kJoinParts;
+                if (i < mine) ask(k, partial<D>(own, (int64_t)(at.first + i) * per_step + hg * kv + kh, i == 0 ? at.slot : 0, hh));
+            }
+            add(i0, mine);
         }
     }
     red[part][c] = o;
