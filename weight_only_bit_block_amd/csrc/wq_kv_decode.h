@@ -60,6 +60,9 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 // that lies in one run is finished there; the pieces of others go to a workspace
 // and a second kernel joins them in order.
 //
+// With a window only its tiles are walked, and those of the first tokens (Tiles); their
+// pages follow from the length, so that they are asked for after it.
+//
 // 8 heads of 128: one sequence of 131072, 2 query heads each, 30 us (5.0 TB/s), joining
 // them 5.9; 64 sequences of 262139 in all, 4 query heads each, 63 us (4.8 TB/s, bound by the
 // vector instructions that make weights of scores and numbers of codes), joining 4.8.

@@ -30,10 +30,14 @@
 // walked first to last, so that its precision never depends on values it does
 // not see by more than the 2^14 of one tile.
 //
-// Bound: in long prompts the rate of binary16 products (8192 tokens, 16 heads of 128: 815 us,
-// 1012 TFLOP/s where a large library product reaches 1205 of nominal 2500), the
-// latency of a launch or two in short ones (128 tokens: 10.6 us), in between the L2's
-// k and v and the issue of matrix and vector instructions in turns (1024 tokens: 30 us).
+// Bound: in long prompts the rate of binary16 products (8192 tokens, 16 heads of 128: 766 us,
+// 1077 TFLOP/s where a large library product reaches 1153 to 1205 of nominal 2500), the
+// latency of a launch or two in short ones (128 tokens: 10.4 us), in between the L2's
+// k and v and the issue of matrix and vector instructions in turns (1024 tokens: 29 us).
+//
+// A window changes which tiles a block of rows walks (Walk) and what its rows see
+// of them (Sight): 8192 tokens through 1024 and the first 4, 252 us with prepare's 34;
+// a block of 128 rows walks 37 tiles where each row sees 32 to 33 tiles' worth.
 #include "wq_internal.h"
 #include "wq_device.h"
 #include "wq_seq.h"
