@@ -448,9 +448,9 @@ int wq_residual_norm(const float *h, const float *y, const float *post_weight, c
  * are left out. start may be null (all 0), taken too (0); positions and slots may
  * be null when not wanted. A request with a negative length, or of more than
  * 2^31 - 1 tokens, gets no token and no page, and lens -1. B is below 2^24,
- * max_pages below 2^25, n_free below 2^31, T below 2^30. taken_out must not be
- * taken (WQ_ERR_SHAPE), and no other output may alias an input: the same inputs
- * give the same plan again.
+ * max_pages below 2^25, n_free below 2^31, T below 2^30. No output may share
+ * memory with an input or another output (WQ_ERR_SHAPE): a loop of steps copies
+ * lens to start and taken_out to taken between them.
  */
 int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *table, int64_t max_pages,
                const int32_t *free_pages, int64_t n_free, const int32_t *taken, int64_t T, int32_t *cu, int32_t *lens,
@@ -472,7 +472,7 @@ int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *t
  * and as much of it as 4 times the angle's error.
  * T is below 2^24. heads and kv_heads may be any number, one of them 0 (its pointers null then).
  * Rows of tokens with a negative position are not written. q_out may be q and
- * k_out may be k (with the same stride); no other aliasing.
+ * k_out may be k (with the same stride, else WQ_ERR_SHAPE); no other aliasing.
  */
 int wq_qk_norm_rope(const float *q, int64_t q_stride, int64_t heads, const float *k, int64_t k_stride,
                     int64_t kv_heads, int64_t head_dim, int64_t T, const int32_t *positions, const float *inv_freq,

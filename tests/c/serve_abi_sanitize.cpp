@@ -88,6 +88,10 @@ int main()
         wq_kv_append_slots(&c, F, st, F, st, T, L, nullptr);
         wq_qk_norm_rope(F, st, h, F, st, kv, d, T, I, F, pick(32), 0, 1.0f, 1, F, F, 1e-6f, F, st, F, st, nullptr);
         wq_kv_plan(I, I, B, I, W, I, pick(9), I, T, I, I, I, L, I + 64, nullptr);
+        // (memory of their own, 2^52 bytes apart, which no size reaches)
+        const auto far = [](int n) { return (uintptr_t)0x10000 + ((uintptr_t)n << 52); };
+        const auto ints = [&](int n) { return reinterpret_cast<int32_t *>(far(n)); };
+        wq_kv_plan(ints(1), ints(2), B, ints(3), W, ints(4), pick(9), ints(5), T, ints(6), ints(7), ints(8), reinterpret_cast<int64_t *>(far(9)), ints(10), nullptr);
     }
     if (launches < 100000) {
         std::fprintf(stderr, "only %d launches\n", launches);

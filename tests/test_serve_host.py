@@ -50,6 +50,31 @@ def test_plan_refusals(lib):  # noqa: F811
     assert _plan(lib, slots=FAKE + 4) == ALIGN
 
 
+def _spread(**kw):
+    """Arguments of a plan that share no memory: 3 requests, rows of 4 pages, 9 free ones, 5 tokens."""
+    a = {name: FAKE + 256 * i for i, name in enumerate(("fresh", "start", "free", "taken", "table", "cu", "lens", "pos", "slots", "out"))}
+    a.update(kw)
+    return a
+
+
+def test_plan_refuses_outputs_in_other_memory_of_the_call(lib):  # noqa: F811
+    """The next step's start in this one's lens would be read before or after it is written."""
+    at = _spread()
+    size = dict(fresh=12, start=12, free=36, taken=4, table=48, cu=16, lens=12, pos=20, slots=40, out=4)
+    outputs = ("table", "cu", "lens", "pos", "slots", "out")
+    for name in outputs:
+        for other in at:
+            if other != name:
+                step = 8 if name == "slots" else 4
+                last = (size[other] - 1) // step * step
+                for where in (at[other], at[other] + last, at[other] - size[name] + step):
+                    assert _plan(lib, **_spread(**{name: where})) == SHAPE, (name, other, where)
+
+
+def test_rope_in_place_needs_the_same_stride(lib):  # noqa: F811
+    assert _rope(lib, q=FAKE, qo=FAKE, qs=4096, qos=4100) == SHAPE and _rope(lib, k=FAKE, ko=FAKE, ks=4096, kos=4100) == SHAPE
+
+
 def _slots(lib, cache=None, **kw):  # noqa: F811
     a = dict(k=FAKE, ks=1024, v=FAKE, vs=1024, T=8, slots=FAKE)
     a.update(kw)

@@ -19,6 +19,16 @@ int check_rows(const float *in, int64_t in_stride, const float *out, int64_t out
     return aligned(in, 16) && aligned(out, 16) ? WQ_OK : WQ_ERR_ALIGN;
 }
 
+// Memory of a plan's call.
+struct Span {
+    const void *at;
+    uint64_t bytes;
+};
+bool meet(const Span &a, const Span &b)
+{
+    return a.at && b.at && a.bytes && b.bytes && (uintptr_t)a.at < (uintptr_t)b.at + b.bytes && (uintptr_t)b.at < (uintptr_t)a.at + a.bytes;
+}
+
 int check_shared(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
 {
     int st = check_decode(B, heads, kv_heads, head_dim, max_pages);
@@ -47,6 +57,9 @@ int wq_qk_norm_rope(const float *q, int64_t q_stride, int64_t heads, const float
     if (kv_heads > 0 && (st = check_rows(k, k_stride, k_out, k_out_stride, kv_heads, head_dim))) return st;
     if (!positions || (pairs > 0 && !inv_freq)) return WQ_ERR_NULL;
     if (!aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(q_weight, 16) || !aligned(k_weight, 16)) return WQ_ERR_ALIGN;
+    // in place row by row only: with other strides a row would be written over one that is still to be read
+    if (T > 1 && ((heads > 0 && q == q_out && q_stride != q_out_stride) || (kv_heads > 0 && k == k_out && k_stride != k_out_stride)))
+        return WQ_ERR_SHAPE;
     const wq::RopeArgs a = {q, k, q_stride, k_stride, (int)heads, (int)kv_heads, (int)head_dim, T, positions, inv_freq,
                             (int)pairs, factor, norm ? q_weight : nullptr, norm ? k_weight : nullptr, eps, q_out, k_out,
                             q_out_stride, k_out_stride};
@@ -66,6 +79,17 @@ int wq_kv_plan(const int32_t *fresh, const int32_t *start, int64_t B, int32_t *t
     if (!aligned(fresh, 4) || !aligned(start, 4) || !aligned(table, 4) || !aligned(free_pages, 4) || !aligned(taken, 4) ||
         !aligned(cu, 4) || !aligned(lens, 4) || !aligned(positions, 4) || !aligned(slots, 8) || !aligned(taken_out, 4))
         return WQ_ERR_ALIGN;
+    // Every workgroup reads all inputs and writes its share of the outputs, in no order: start of the next step in
+    // the lengths of this one would be read before or after they are written.
+    const uint64_t n = (uint64_t)B * 4;
+    const Span in[] = {{fresh, n}, {start, n}, {free_pages, (uint64_t)n_free * 4}, {taken, 4}};
+    const Span outs[] = {{table, n * (uint64_t)max_pages}, {cu, n + 4}, {lens, n}, {positions, (uint64_t)T * 4}, {slots, (uint64_t)T * 8}, {taken_out, 4}};
+    for (const Span &o : outs) {
+        for (const Span &i : in)
+            if (meet(o, i)) return WQ_ERR_SHAPE;
+        for (const Span *p = outs; p != &o; ++p)
+            if (meet(o, *p)) return WQ_ERR_SHAPE;
+    }
     const wq::PlanArgs a = {fresh, start, B, table, max_pages, free_pages, n_free, taken, T, cu, lens, positions, slots, taken_out};
     return hip_status(wq::launch_kv_plan(a, stream));
 }

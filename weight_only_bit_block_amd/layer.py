@@ -345,9 +345,10 @@ def kv_plan(fresh, table, free, taken: Optional[torch.Tensor] = None, tokens: in
     is used up); returns the token offsets cu, the lengths after the step, each
     token's position and its slot in the cache for up to `tokens` tokens (-1
     past the last one, slots also where there is no page), and the new `taken`
-    (past len(free): the list was too short). `out`: a plan to write into, with
-    another `taken` than the one given. A request with a bad length gets lens -1
-    and no tokens."""
+    (past len(free): the list was too short). `out`: a plan to write into, which
+    shares no memory with the inputs (start and taken are copies of the last step's
+    lens and taken, or those of another plan). A request with a bad length gets
+    lens -1 and no tokens."""
     if not (isinstance(fresh, _Tensor) and fresh.dim() == 1 and fresh.is_cuda):
         raise ValueError("fresh must be an int32 device tensor [requests]")
     B, at = fresh.shape[0], fresh.get_device()
