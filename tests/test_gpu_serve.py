@@ -807,3 +807,129 @@ def test_serving_refusals():
     assert wqa.attn_decode_shared(q[:0], cache, ln, one, tab[:0], ln[:0]).shape == (0, 4, 64)
     assert wqa.qk_norm_rope(q[:0], k[:0], ln[:0], inv)[1].shape == (0, 2, 64)
     wqa.kv_append(cache, k[:0], k[:0], slots=slots[:0])
+
+
+@pytest.mark.parametrize("count,heads,kv,d", [(4, 8, 2, 128), (40, 4, 2, 64), (70, 2, 1, 128)])
+def test_pages_that_are_named_more_than_once(count, heads, kv, d):
+    """Rows that share pages with one another, with the prefix and with themselves."""
+    note(f"pages twice {count} {heads} {kv} {d}")
+    torch = torch_cuda()
+    rng = rng_for(95, count)
+    host, cache = cache_arrays(rng, 4, kv, d)
+    table, pre = rng.integers(0, 4, (count, 9)).astype(np.int32), np.array([2, 2, 0, 1, 2, 3, 3], np.int32)
+    table[1] = table[0]
+    lens = rng.integers(0, 9 * 64 + 1, count)
+    lens[:2] = 9 * 64
+    q = (rng.standard_normal((count, heads, d)) * 2).astype(np.float32)
+    out = torch.full(q.shape, NAN, device="cuda")
+    wqa.attn_decode_shared(dev(q), cache, dev(pre), ints([7 * 64 - 1]), dev(table), ints(lens), out=out)
+    check_shared(out, q, host, pre, 7 * 64 - 1, table, lens, d ** -0.5)
+    kval, vval = ref.values(host[0], host[1]), ref.values(host[2], host[3])
+    out = wqa.attn_decode(dev(q), cache, dev(table), ints(lens), window=150, sinks=70)
+    want, sums = sref.decode(q, kval, vval, host[3], d ** -0.5, lambda b: [(table[b], lens[b], sref.seen(lens[b], 150, 70))])
+    check_rows(out, want, sums, 220, d)
+
+
+def test_one_slot_for_two_tokens_spoils_only_itself():
+    note("slot twice")
+    torch = torch_cuda()
+    kv, d, T = 2, 128, 300
+    _, (_, k, v) = qkv(rng_for(96), T, kv, kv, d)
+    slots = np.arange(T) + 20
+    slots[[5, 250]] = 150                          # the place of token 130
+    caches = [wqa.KVCache.empty(6, kv, d) for _ in range(2)]
+    for c in caches:
+        for t in c:
+            t.zero_()
+    wqa.kv_append(caches[0], k, v, slots=dev(slots))
+    slots[[5, 250, 130]] = -1
+    wqa.kv_append(caches[1], k, v, slots=dev(slots))
+    for a, b in zip(*caches):
+        a[150 // 64, :, 150 % 64] = 0
+        assert torch.equal(a, b)
+
+
+def test_plan_of_no_requests_and_into_its_own_inputs():
+    note("plan edges")
+    torch = torch_cuda()
+    none = ints([])
+    p = wqa.kv_plan(none, none.view(0, 4), ints([1, 2]), ints([1]), tokens=5)
+    assert p.cu.tolist() == [0] and p.lens.numel() == 0 and p.positions.tolist() == [-1] * 5 == p.slots.tolist() and p.taken.tolist() == [1]
+    fresh, table, free = ints([1, 1]), ints([[-1] * 3] * 2), ints([4, 5, 6])
+    p = wqa.kv_plan(fresh, table, free, tokens=2)
+    before = [t.clone() for t in p] + [table.clone()]
+    for kw in (dict(start=p.lens), dict(taken=p.taken), dict(start=p.positions)):
+        with pytest.raises((ValueError, wqa.WqError)):
+            wqa.kv_plan(fresh, table, free, tokens=2, out=p, **kw)
+    with pytest.raises(wqa.WqError):
+        wqa.kv_plan(p.lens, table, free, tokens=2, out=p)
+    with pytest.raises(wqa.WqError):
+        wqa.kv_plan(fresh, table, table.view(-1), tokens=2)
+    with pytest.raises(wqa.WqError):
+        wqa.kv_plan(fresh, table, free, tokens=2, out=p._replace(positions=p.lens))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, tuple(p) + (table,)))
+
+
+def test_a_captured_step_that_goes_on_by_itself():
+    """Lengths and the place in the list of free pages advance on the device: replays are steps."""
+    note("captured loop")
+    torch = torch_cuda()
+    B, width, pages = 5, 6, 40
+    rng = rng_for(97)
+    first = rng.integers(0, 130, B)
+    free, fresh = ints(rng.permutation(pages)), ints([1, 1, 0, 2, 1])
+
+    def state():
+        table = ints(np.full((B, width), -1))
+        p = wqa.kv_plan(ints(first), table, free)
+        return table, p.lens.clone(), p.taken.clone()
+
+    def step(table, start, taken):
+        p = wqa.kv_plan(fresh, table, free, taken, tokens=8, start=start)
+        start.add_(fresh)
+        torch.add(p.taken, 0, out=taken)
+        return p
+
+    eager, caught = state(), state()
+    step(*state())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = step(*caught)
+    for i in range(70):
+        graph.replay()
+        p = step(*eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(tuple(p) + eager, tuple(q) + caught)), i
+    want = sref.plan((70 * fresh.cpu().numpy() + first).tolist(), [0] * B, np.full((B, width), -1, np.int32), free.cpu().numpy(), 0, 0)
+    assert np.array_equal(np.sort(caught[0].cpu().numpy(), None), np.sort(want[0], None)) and np.array_equal(p.taken.cpu().numpy(), want[5])
+
+
+def test_two_graphs_of_one_pool():
+    """Replayed in turns: neither keeps anything of its workspace from one replay to the next."""
+    note("two graphs")
+    torch = torch_cuda()
+    rng = rng_for(98)
+    cases, graphs, caught, want = [], [], [], []
+    for heads, kv, d, prefix, lens in ((8, 2, 128, 3000, [700, 1500, 64]), (14, 2, 64, 2000, [300] * 40)):
+        pre, table, _, cache, q = shared_case(rng, heads, kv, d, prefix, lens)
+        cases.append((dev(q), cache, dev(pre), ints([prefix]), dev(table), ints(lens), *qkv(rng, 500, heads, kv, d)[1]))
+
+    def calls(q, cache, pre, n, table, lens, pq, pk, pv):
+        return (wqa.attn_decode_shared(q, cache, pre, n, table, lens), wqa.attn_decode(q, cache, table, lens, window=600, sinks=3),
+                wqa.attn_prefill(pq, pk, pv, window=77, sinks=5))
+    for c in cases:
+        want.append(calls(*c))
+    torch.cuda.synchronize()
+    pool = torch.cuda.graph_pool_handle()
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], pool=pool):
+            caught.append(calls(*c))
+    for i in (0, 1, 1, 0, 1, 0, 0, 1):
+        for t in caught[i]:
+            t.fill_(NAN)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(caught[i], want[i])), i
