@@ -9,7 +9,7 @@
 // behind 777 tokens 22.5 us apart, 15.4 together; 64 behind 32768 85 and 76).
 //
 // For one key/value head the prefix meets R = B * group query rows, so that its
-// scores are a matrix product of R x L x D. Few rows (few_rows) run as one sequence
+// scores are a matrix product of R x L x D. Few rows (kFewRows) run as one sequence
 // of the attention of single tokens with 8 heads a workgroup, near HBM's rate.
 // More, on prefix_job:
 //   A workgroup takes 64 or 128 rows and a run of pages. A page's 64 keys are two
@@ -65,7 +65,7 @@ __device__ __forceinline__ int v_at(int key, int piece)
 }
 
 // RW x 32 rows, two wavefronts for 32 of them. Two buffers of operands where a compute
-// unit holds one workgroup (128 rows), one where it holds two, which take turns.
+// unit holds one workgroup (128 rows), one where it holds two (heads of 64: three), which take turns.
 constexpr int operand_bytes(int D) { return 3 * kTile * D * 2 + D / 32 * kTile * 2; }
 constexpr int at_least(int a, int b) { return a > b ? a : b; }
 constexpr int prefix_lds_bytes(int D, int RW) { return at_least((RW == 4 ? 2 : 1) * operand_bytes(D), 32 * RW * (D + kPartialExtra) * 4); }
@@ -74,8 +74,9 @@ template <int D, int RW>
 __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, int chunks, float c_man, int c_exp, uint8_t *lds, unsigned job)
 {
     constexpr int NB = D / 32, F = D / 16, W = 2 * RW;
-    constexpr bool kTwo = RW == 4, kApart = F < W;                        // kApart: more wavefronts than pieces, k's and v's are others
-    constexpr int kMine = kApart ? 1 : F / W;                             // pieces of 16 values of a key's k or v, of a thread
+    constexpr bool kTwo = RW == 4;
+    constexpr int kMine = F / W;                                          // pieces of 16 values of a key's k and v, of a thread
+    static_assert(F % W == 0, "pieces");
     constexpr int kRowBytes = D * 2, kPitch = D + kPartialExtra, kOperands = operand_bytes(D);
     typedef _Float16 hb __attribute__((ext_vector_type(NB)));
     const DecodeArgs &own = a.own;
@@ -93,8 +94,7 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
     const bool live = row < rows, any = (block * RW + rw) * 32 < rows;
 
     // ---- pages come into registers one ahead: codes of this thread's pieces, scales of the lane's key
-    const bool do_k = !kApart || wave < F, do_v = !kApart || wave >= F;
-    u2 kc[kMine], vc[kMine];                 // (one and the same where kApart)
+    u2 kc[kMine], vc[kMine];
     hb ks, vs;
     bool bad = false;
     if (own.cache.n_pages <= 0) {            // no page to read at all
@@ -120,12 +120,8 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int o = lane * (D / 2) + (wave + W * i) % F * 8;
-            if constexpr (kApart) {
-                kc[i] = vc[i] = *reinterpret_cast<const u2 *>((do_k ? kq : vq) + o);
-            } else {
-                kc[i] = *reinterpret_cast<const u2 *>(kq + o);
-                vc[i] = *reinterpret_cast<const u2 *>(vq + o);
-            }
+            kc[i] = *reinterpret_cast<const u2 *>(kq + o);
+            vc[i] = *reinterpret_cast<const u2 *>(vq + o);
         }
         ks = *reinterpret_cast<const hb *>(own.cache.ks + (at + lane) * NB);
         vs = *reinterpret_cast<const hb *>(own.cache.vs + (at + lane) * NB);
@@ -156,32 +152,28 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int piece = (wave + W * i) % F, b = piece >> 1;                         // 16 values, half a block
-            if (do_k) {
-                _Float16 s = ks[0];
+            _Float16 s = ks[0], s1 = vs[0];
 #pragma unroll
-                for (int n = 1; n < NB; ++n) s = b == n ? ks[n] : s;
-                if ((piece & 1) == 0) ksb[b * kTile + lane] = s;
-                // fragment `piece` of the key's tile, lane (key, half)
-                h8 *kd = reinterpret_cast<h8 *>(kb) + (lane >> 5) * (F * 64) + piece * 64 + (lane & 31);
-                kd[0] = codes8(kc[i].x);
-                kd[32] = codes8(kc[i].y);
+            for (int n = 1; n < NB; ++n) {
+                s = b == n ? ks[n] : s;
+                s1 = b == n ? vs[n] : s1;
             }
-            if (do_v) {
-                _Float16 s1 = vs[0];
+            if ((piece & 1) == 0) ksb[b * kTile + lane] = s;
+            // fragment `piece` of the key's tile, lane (key, half)
+            h8 *kd = reinterpret_cast<h8 *>(kb) + (lane >> 5) * (F * 64) + piece * 64 + (lane & 31);
+            kd[0] = codes8(kc[i].x);
+            kd[32] = codes8(kc[i].y);
+            s1 = (_Float16)ldexpf((float)s1, kScaleTop - v_exp);
+            const h8 s8 = {s1, s1, s1, s1, s1, s1, s1, s1};
 #pragma unroll
-                for (int n = 1; n < NB; ++n) s1 = b == n ? vs[n] : s1;
-                s1 = (_Float16)ldexpf((float)s1, kScaleTop - v_exp);
-                const h8 s = {s1, s1, s1, s1, s1, s1, s1, s1};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const h8 c = codes8(vc[i][j]);
-                    h8 hi = c * s;
-                    asm("" : "+v"(hi));
-                    const h8 lo = __builtin_elementwise_fma(c, s, -hi);
-                    const int at = v_at<D>(lane, 2 * piece + j);
-                    *reinterpret_cast<h8 *>(vb + at) = hi;
-                    *reinterpret_cast<h8 *>(vb + kTile * kRowBytes + at) = lo;
-                }
+            for (int j = 0; j < 2; ++j) {
+                const h8 c = codes8(vc[i][j]);
+                h8 hi = c * s8;
+                asm("" : "+v"(hi));
+                const h8 lo = __builtin_elementwise_fma(c, s8, -hi);
+                const int at = v_at<D>(lane, 2 * piece + j);
+                *reinterpret_cast<h8 *>(vb + at) = hi;
+                *reinterpret_cast<h8 *>(vb + kTile * kRowBytes + at) = lo;
             }
         }
         return by;
@@ -385,9 +377,12 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
 }
 
 // A step: workgroups of the sequences' own tokens, RW / 2 jobs each, then those of
-// the prefix. Apart, either would wait for the other's last.
+// the prefix. Apart, either would wait for the other's last. Heads of 64 leave room for a
+// third workgroup of 64 rows on a compute unit if registers are held to a third (one fewer than
+// the compiler takes): all workgroups of a call begin at once. 64 requests of 16/8 heads behind 8000
+// tokens 32.8 -> 27.0 us, 75 of 14/2 behind 8191 30.7 -> 27.7 (behind 2000 18.4 -> 19.6).
 template <int D, int RW, int H>
-__global__ __launch_bounds__(128 * RW, 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp, int groups, int cut, unsigned own_jobs)
+__global__ __launch_bounds__(128 * RW, D == 64 ? 3 : 2) void shared_kernel(SharedArgs a, float *parts, int chunks, float c_man, int c_exp, int groups, int cut, unsigned own_jobs)
 {
     constexpr int kJobs = RW / 2, kJobBytes = (decode_lds_bytes(D, H) + 15) / 16 * 16;
     __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(prefix_lds_bytes(D, RW), kJobs * kJobBytes)];
@@ -535,18 +530,20 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
 }
 
 // ---- how the prefix is cut
-// Workgroups of 8 rows (few_rows), of 64, two on each compute unit, or of 128, one. us a call, prefixes in
+// Workgroups of 8 rows (up to kFewRows), of 64, two or three on each compute unit, or of 128, one. us a call, prefixes in
 // tokens, 8 / 64 rows: heads of 128, 8 key/value heads, 32768 tokens: 8 rows 30.8 / 41.9, 16 35.5 / 43.1, 24 43.5
-// / 44.7, 32 47.0 / 45.8; heads of 64, 16000: 16 rows 19.2 / 24.3, 32 22.4 / 26.2; 2048 tokens the same within 1 us.
+// / 44.7, 32 47.0 / 45.8; heads of 64, 4 key/value heads, 16000: 16 rows 13.8 / 15.0, 24 14.7
+// / 15.2, 32 15.6 / 15.3; 8, 8000: 24 16.4 / 14.6; 2, 4000: 28 11.5 / 13.0; 2048 tokens the same within 1 us.
 // 64 / 128 rows, 16/8 heads of 128: 64 rows, 32768 tokens 52 / 62; 128 rows, 2048 26.8 / 33.8, 8192 46.5 / 46.6, 16000
-// 55.8 / 55.4, 32768 79 / 77; heads of 64, 14/2, 525 rows: 4000 22.0 / 29.9, 8191 31.5 / 34.1, 16000 38.8 / 40.6.
+// 55.8 / 55.4, 32768 79 / 77. Heads of 64 take 64 always: 14/2, 525 rows, 16000 tokens 34 / 41, 32000 45 / 52, 131000 129
+// / 137, 262000 241 / 249; 16/8, 128 rows, 65000 67 / 71, 131000 118 / 118.
 constexpr int kSharedFill = 512;
-inline int64_t few_rows(int64_t head_dim) { return head_dim == 64 ? 32 : 24; }
+constexpr int64_t kFewRows = 24;
 inline int row_waves(int64_t rows, int64_t head_dim, int64_t prefix_pages)
 {
-    return rows <= 64 || prefix_pages <= (head_dim == 64 ? 256 : 128) ? 2 : 4;
+    return head_dim == 64 || rows <= 64 || prefix_pages <= 128 ? 2 : 4;
 }
-inline int run_unit(int64_t rows, int64_t head_dim) { return rows <= few_rows(head_dim) ? kDecodeWaves : 1; }        // pages
+inline int run_unit(int64_t rows) { return rows <= kFewRows ? kDecodeWaves : 1; }        // pages
 // A sequence's own tokens are cut whenever that makes parts, since there is a join anyway, into no more
 // runs than there can be steps; the prefix into as many as fill what is left of the card, half of it at
 // least, and all of it where its runs are longer than kRunPages. With workgroups of 64 rows own tokens take
@@ -567,7 +564,7 @@ inline SharedCut shared_cut(int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     c.groups = head_groups((int)heads, (int)kv_heads);
     c.per_step = (int)kv_heads * c.groups;
     int64_t most = runs_per_head(c.per_step);
-    c.waves = rows <= few_rows(head_dim) ? 0 : row_waves(rows, head_dim, prefix_pages);
+    c.waves = rows <= kFewRows ? 0 : row_waves(rows, head_dim, prefix_pages);
     c.together = c.waves == 4 ? 2 : 1;
     if (c.waves != 4) most = (most + 1) / 2;     // beside the prefix, not before it
     c.own = B > kCutMaxSeqs || steps <= 1 ? 0 : (int)(B * steps < most ? B * steps : most);
@@ -575,7 +572,7 @@ inline SharedCut shared_cut(int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     const int64_t each = c.waves ? 32 * c.waves : kMaxGroup;
     c.blocks = (rows + each - 1) / each * kv_heads;
     const int64_t slots = c.waves == 4 ? kSharedFill / 2 : kSharedFill, taken = (c.own_jobs + c.together - 1) / c.together;
-    const int64_t unit = run_unit(rows, head_dim), units = (prefix_pages + unit - 1) / unit;
+    const int64_t unit = run_unit(rows), units = (prefix_pages + unit - 1) / unit;
     const int64_t left = (taken > slots / 2 ? slots / 2 : slots - taken) / c.blocks, all = slots / c.blocks;
     int64_t n = prefix_pages / kRunPages < all ? prefix_pages / kRunPages : all;
     if (n < left) n = left;
@@ -613,8 +610,8 @@ hipError_t launch_attn_decode_shared(const SharedArgs &args, hipStream_t stream)
     const auto pick = [&](auto dim, auto heads) {
         constexpr int DIM = decltype(dim)::value, H = decltype(heads)::value;
         if (cut.waves == 0) start(shared_few_kernel<DIM, H>);
-        else if (cut.waves == 2) start(shared_kernel<DIM, 2, H>);
-        else start(shared_kernel<DIM, 4, H>);
+        else if (DIM == 64 || cut.waves == 2) start(shared_kernel<DIM, 2, H>);
+        else if constexpr (DIM == 128) start(shared_kernel<DIM, 4, H>);
     };
     using std::integral_constant;
     if (D == 128) {
@@ -628,7 +625,7 @@ hipError_t launch_attn_decode_shared(const SharedArgs &args, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned jobs = (unsigned)((int64_t)own.B * own.heads);
-    const int unit = run_unit((int64_t)own.B * group, D);
+    const int unit = run_unit((int64_t)own.B * group);
     if (D == 128) shared_join_kernel<128><<<jobs, 128 / 4 * kJoinParts, 0, stream>>>(a, parts, cut.chunks, unit, cut.groups, cut.own);
     else shared_join_kernel<64><<<jobs, 64 / 4 * kJoinParts, 0, stream>>>(a, parts, cut.chunks, unit, cut.groups, cut.own);
     return hipGetLastError();
