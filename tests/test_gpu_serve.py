@@ -933,3 +933,38 @@ def test_two_graphs_of_one_pool():
         graphs[i].replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(caught[i], want[i])), i
+
+
+def test_rows_gigabytes_apart():
+    """Tokens 2 GiB from one another: offsets pass 32 bits in every operator that takes rows with a stride."""
+    note("rows far apart")
+    torch = torch_cuda()
+    rng = rng_for(99)
+    heads, kv, d, T, far = 8, 2, 128, 6, 1 << 29
+    host, (q, k, v) = qkv(rng, T, heads, kv, d)
+    big = torch.empty((T - 1) * far + 8 * heads * d, device="cuda")
+    spots = iter(range(0, 8 * heads * d, heads * d))
+
+    def away(t=None, n=heads):
+        y = big.as_strided((T, n, d), (far, d, 1), next(spots))
+        return y if t is None else y.copy_(t)
+    fq, fk, fv = away(q), away(k, kv), away(v, kv)
+    pos, inv, w = ints(np.arange(T) * 1000), dev(freqs(64)), dev(rng.standard_normal(d).astype(np.float32))
+    want = wqa.qk_norm_rope(q, k, pos, inv, q_weight=w)
+    got = wqa.qk_norm_rope(fq, fk, pos, inv, q_weight=w, q_out=away(), k_out=away(n=kv))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    out = away()
+    assert torch.equal(wqa.attn_prefill(fq, fk, fv, out=out, window=3, sinks=1), wqa.attn_prefill(q, k, v, window=3, sinks=1))
+    slots = dev(np.arange(T, dtype=np.int64) * 70)
+    caches = [wqa.KVCache(*(t.zero_() for t in wqa.KVCache.empty(8, kv, d))) for _ in range(2)]
+    wqa.kv_append(caches[0], k, v, slots=slots)
+    wqa.kv_append(caches[1], fk, fv, slots=slots)
+    assert all(torch.equal(a, b) for a, b in zip(*caches))
+    table, lens = ints(rng.integers(0, 8, (T, 5))), ints([300, 0, 64, 65, 1, 320])
+    pre, n = ints([3, 1, 2]), ints([150])
+    out.fill_(NAN)
+    assert torch.equal(wqa.attn_decode(fq, caches[0], table, lens, out=out, window=100, sinks=3), wqa.attn_decode(q, caches[0], table, lens, window=100, sinks=3))
+    out.fill_(NAN)
+    assert torch.equal(wqa.attn_decode_shared(fq, caches[0], pre, n, table, lens, out=out), wqa.attn_decode_shared(q, caches[0], pre, n, table, lens))
+    del big
+    torch.cuda.empty_cache()
