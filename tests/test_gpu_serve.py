@@ -968,3 +968,27 @@ def test_rows_gigabytes_apart():
     assert torch.equal(wqa.attn_decode_shared(fq, caches[0], pre, n, table, lens, out=out), wqa.attn_decode_shared(q, caches[0], pre, n, table, lens))
     del big
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,heads", [(64, 4), (300, 4), (330, 300)])
+def test_window_prompt_offsets_out_of_range_stay_in_bounds(T, heads):
+    """Offsets past T, below 0 and decreasing: rows of valid ranges come out right, others stay in bounds; tokens before the
+    first sequence and behind the last are left alone."""
+    note(f"window bad cu {T} {heads}")
+    torch = torch_cuda()
+    host, (q, k, v) = qkv(rng_for(100, T), T, heads, 2, 64)
+    for cu in ([-5, 20, 1000], [0, 64, 64, 10], [T + 6, T + 9], [-9, -3], [30, 20, 64]):
+        out = torch.full((T, heads, 64), NAN, device="cuda")
+        wqa.attn_prefill(q, k, v, cu=ints(cu), out=out, window=33, sinks=2)
+        torch.cuda.synchronize()
+        if cu[-1] < 0 or cu[0] > T:
+            assert torch.isnan(out).all()
+    some = [0, heads // 2 - 1, heads // 2, heads - 1]
+    part = [host[0][:, some], host[1][:, [j // (heads // 2) for j in some]], host[2][:, [j // (heads // 2) for j in some]]]
+    out = torch.full((T, heads, 64), NAN, device="cuda")
+    wqa.attn_prefill(q, k, v, cu=ints([-5, 20, 1000]), out=out, window=33, sinks=2)
+    check_window_prompt(out[:, some], part, [20, T - 20], 0.125, 33, 2)
+    out.fill_(NAN)
+    wqa.attn_prefill(q, k, v, cu=ints([7, 50, T - 3]), out=out, window=33, sinks=2)
+    assert torch.isnan(out[:7]).all() and torch.isnan(out[T - 3:]).all()
+    check_window_prompt(out[7:T - 3, some], [x[7:T - 3] for x in part], [43, T - 53], 0.125, 33, 2)
