@@ -537,6 +537,8 @@ __global__ __launch_bounds__(D / 4 * kJoinParts) void shared_join_kernel(SharedA
 // 64 / 128 rows, 16/8 heads of 128: 64 rows, 32768 tokens 52 / 62; 128 rows, 2048 26.8 / 33.8, 8192 46.5 / 46.6, 16000
 // 55.8 / 55.4, 32768 79 / 77. Heads of 64 take 64 always: 14/2, 525 rows, 16000 tokens 34 / 41, 32000 45 / 52, 131000 129
 // / 137, 262000 241 / 249; 16/8, 128 rows, 65000 67 / 71, 131000 118 / 118.
+// Two places on each compute unit: the third of heads of 64 takes what comes beside them (filled with runs of its own, 768
+// places: 16/8 heads, 64 requests behind 4000 tokens 21 -> 26, behind 16000 33 -> 39).
 constexpr int kSharedFill = 512;
 constexpr int64_t kFewRows = 24;
 inline int row_waves(int64_t rows, int64_t head_dim, int64_t prefix_pages)
