@@ -131,6 +131,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
     float2 t[4];                             // of the lane's pairs
 #pragma unroll
     for (int j = 0; j < 4; ++j) t[j] = z[INTER ? 2 * l + (j & 1) + (j >> 1) * (D / 4) : p + j];
+    // Values that are not rotated go round the rotation: by an angle of 0 one that is not finite would spoil its
+    // partner. (pairs is a multiple of 4, so that a lane's four values on a side are of one kind)
+    const bool turns1 = (INTER ? 2 * l : p) < a.pairs, turns2 = INTER ? 2 * l + D / 4 < a.pairs : turns1;
     for (int r0 = first; r0 - first < rows; r0 += kAhead * kStep) {
         if (r0 != first) load(r0);
 #pragma unroll
@@ -157,6 +160,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
                     v[j] = fmaf(y[i][j], t[j].x, x[i][j] * t[j].y);
                 }
             }
+            if (!turns1) u = x[i];
+            if (!turns2) v = y[i];
             if (r < rows && position >= 0) {
                 float *dst = r < a.heads ? a.q_out + token * a.q_out_stride + r * D : a.k_out + token * a.k_out_stride + (r - a.heads) * D;
                 *reinterpret_cast<f4 *>(dst + at1) = u;
