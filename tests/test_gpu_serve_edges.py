@@ -4,10 +4,11 @@ import numpy as np
 import pytest
 
 import weight_only_bit_block_amd as wqa
+from tests import layer_ref as ref
 from tests import serve_ref as sref
 from tests.gpu_util import note, torch_cuda
-from tests.test_gpu_layer import NAN, dev, qkv, rng_for
-from tests.test_gpu_serve import freqs
+from tests.test_gpu_layer import NAN, cu_of, dev, qkv, rng_for
+from tests.test_gpu_serve import check_window_prompt, freqs, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,62 @@ def test_rope_values_that_are_not_rotated_are_kept(d, pairs, inter, T):
         assert not np.isfinite(got[..., own]).any()
         want, lim = sref.rope(host[0], pos, inv, np.where(own, 1, w).astype(np.float32), 1e-6, True, inter, 1.0)
         assert (np.abs(got - want)[..., ~own] <= lim[..., ~own]).all()
+
+
+# ------------------------------------------------------------------ prompts through a window
+def few(heads, T, host, out):
+    """Some heads of a wide layout with 2 key/value heads: the plain form is slow."""
+    some = [0, heads // 2 - 1, heads // 2, heads - 1]
+    return out[:, some], [host[0][:, some], *(x[:, [j // (heads // 2) for j in some]] for x in host[1:])]
+
+
+@pytest.mark.parametrize("heads,d", [(800, 64), (500, 128)])
+@pytest.mark.parametrize("window,sinks", [(40, 0), (64, 3), (1, 40), (100, 33)])
+def test_window_of_many_heads_hides_what_it_hides(heads, d, window, sinks):
+    """Wavefronts that share tiles of 128 rows: those that they leave out may hold anything, wild rows and rows that
+    are not finite among them, at both ends of what is left out."""
+    note(f"window many {heads} {d} {window} {sinks}")
+    torch = torch_cuda()
+    T, kv = 330, 2
+    host, _ = qkv(rng_for(111, heads), T, heads, kv, d)
+    t = np.arange(T)
+    want, lim = None, None
+    for at in (0, 2, 33, 70, 127, 128, 190, 256):
+        sees = (t >= at) & ((at > t - window) | (at < sinks))
+        for which in (1, 2):
+            for bad in (NAN, np.inf, 1e20):
+                arr = [host[0], host[1].copy(), host[2].copy()]
+                arr[which][at, 1, 5] = bad
+                out = torch.full((T, heads, d), NAN, device="cuda")
+                wqa.attn_prefill(*(dev(x) for x in arr), out=out, window=window, sinks=sinks)
+                got, part = few(heads, T, host, out)
+                got = got.cpu().numpy()
+                if want is None:
+                    want, sums = sref.window_prompt(*part, [T], d ** -0.5, window, sinks)
+                    lim = ref.bound(sums, min(T, window + sinks), d)
+                hit = np.zeros(got.shape, bool)
+                hit[sees, 2:] = True
+                if which == 2 and bad != 1e20:
+                    hit[..., :5] = hit[..., 6:] = False
+                if bad != 1e20:
+                    assert (np.isnan(got[hit]) if which == 1 else ~np.isfinite(got[hit])).all(), (at, which, bad)
+                # (hidden rows of 1e20's tile keep units of their own: it is more than 2^14 above them)
+                assert (np.abs(got - want)[~hit] <= lim[~hit]).all(), (at, which, bad)
+
+
+@pytest.mark.parametrize("heads,d", [(800, 64), (500, 128)])
+def test_window_of_many_heads_with_offsets_out_of_range(heads, d):
+    """Offsets past T, below 0 and decreasing; tokens of no sequence are left alone."""
+    note(f"window many cu {heads} {d}")
+    torch = torch_cuda()
+    T = 330
+    host, (q, k, v) = qkv(rng_for(112, heads), T, heads, 2, d)
+    for cu, lens, at in (([-5, 20, 1000], [20, T - 20], 0), ([7, 50, T - 3], [43, T - 53], 7), ([0, 200, 200, 90], [200], 0),
+                         ([T + 6, T + 9], [], 0), ([-9, -3], [], 0)):
+        out = torch.full((T, heads, d), NAN, device="cuda")
+        wqa.attn_prefill(q, k, v, cu=ints(cu), out=out, window=33, sinks=2)
+        end = at + sum(lens)
+        got, part = few(heads, T, host, out)
+        assert torch.isnan(out[:at]).all() and torch.isnan(out[end:]).all()
+        if lens:
+            check_window_prompt(got[at:end], [x[at:end] for x in part], lens, d ** -0.5, 33, 2, str(cu))
