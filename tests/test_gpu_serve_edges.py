@@ -104,3 +104,17 @@ def test_window_of_many_heads_with_offsets_out_of_range(heads, d):
         assert torch.isnan(out[:at]).all() and torch.isnan(out[end:]).all()
         if lens:
             check_window_prompt(got[at:end], [x[at:end] for x in part], lens, d ** -0.5, 33, 2, str(cu))
+
+
+@pytest.mark.parametrize("lens,heads,d", [([330], 450, 64), ([330], 170, 128), ([90, 100, 80, 60], 260, 64), ([330], 500, 64), ([330], 160, 128), ([200, 130], 310, 64)])
+def test_window_of_any_width_on_either_side_of_the_limits(lens, heads, d):
+    """Numbers of groups of rows between the limits of narrow and wide windows: the same values whatever the width."""
+    note(f"window widths {lens} {heads} {d}")
+    torch = torch_cuda()
+    T = sum(lens)
+    host, (q, k, v) = qkv(rng_for(113, heads), T, heads, 2, d)
+    for window, sinks in ((1, 3), (100, 0), (263, 0), (264, 70), (265, 0), (T - 1, 0)):
+        out = torch.full((T, heads, d), NAN, device="cuda")
+        wqa.attn_prefill(q, k, v, cu=cu_of(lens), out=out, window=window, sinks=sinks)
+        got, part = few(heads, T, host, out)
+        check_window_prompt(got, part, lens, d ** -0.5, window, sinks, f"{window} {sinks}")

@@ -1100,14 +1100,19 @@ inline uint64_t meta_bytes(int64_t slots, int64_t kv_heads) { return round256((u
 // beside empty ones counts as several.
 //
 // Through a window no block is longer than another, and the other kernel's blocks of 128 rows
-// walk 96 keys more than 32 rows need: 16 heads of 128, one prompt of 3000, window 300 (384)
-// 54 / 62; 3500, 1000 (448) 115 / 116; 4000, 1000 (512) 135 / 124; 13 of 5003, 300 (832) 87 / 92; 8 of
-// 8000, 300 (1120) 139 / 133. Heads of 64: one of 8000, 300 (882) 58 / 73; 16000, 300 (1764) 108 / 112;
-// 16000, 1000 (2016) 276 / 271.
-inline int64_t few_groups(int D, int64_t B, bool window)
+// walk 96 keys more than 32 rows need. Heads of 128: one prompt of 3000, window 300 (384)
+// 54 / 62; 3500, 1000 (448) 115 / 111; 4000, 1000 (512) 132 / 119; 13 of 5003, 300 (832) 87 / 92; 8 of
+// 8000, 300 (1120) 139 / 133. Heads of 64, several prompts: 4 of 12000 (1358), 300 81 / 86, 2500 272 / 262; 8 of 11300 (1344),
+// 300 76 / 82, 1000 138 / 148, 3000 221 / 226; 16 of 10000 (1316), 1000 98 / 111; 8 of 15995 (1862), 1000 205 / 194. One:
+// 8000, 300 (882) 58 / 73; 9700 (1216), 300 97 / 99, 2000 276 / 262; 13000 (1632), 450 143 / 145 (157 / 167 on a slower
+// card), 800 190 / 187 (222 / 221), 2000 368 / 346.
+// A window that hides next to nothing counts as none: heads of 128, one prompt of 3700 (464), 2000 179 / 169, 3000
+// 209 / 220, 3699 213 / 240; 4000 (512), 2000 198 / 179, 3000 234 / 226, 3300 240 / 242, 3999 242 / 263.
+inline int64_t few_groups(int D, int64_t B, int64_t T, int64_t window)
 {
-    if (D == 64) return window ? 1800 : 1200;
-    return B >= 4 ? 880 : window ? 460 : 528;
+    const bool narrow = window > 0 && 5 * window < 4 * T;
+    if (D == 64) return narrow && (B >= 4 || window <= 700) ? 1800 : 1200;
+    return B >= 4 ? 880 : narrow ? 460 : 528;
 }
 
 // Prompts so short are not prepared: no wavefront has more than one tile of 128 values (two of
@@ -1138,7 +1143,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t rows = tile_slots(a.T, a.B, 32 * W);
-    if (rows * a.heads <= few_groups(D, a.B, WIN)) {
+    if (rows * a.heads <= few_groups(D, a.B, a.T, WIN ? a.window : 0)) {
         const int64_t blocks = tile_slots(a.T, a.B, 32);
         attend_shared_kernel<D, WIN><<<(unsigned)(blocks * a.heads), 64 * kShare, 0, stream>>>(a, tiles, metas, (float)(2.0 * c),
                                                                                                c_exp - 1, (int)blocks);
