@@ -493,7 +493,7 @@ int wq_kv_append_slots(const wq_kv_cache *cache, const float *k, int64_t k_strid
  * wq_attn_prefill_window -- wq_attn_prefill where a query at position t of its
  * sequence sees the keys u <= t with u > t - window or u < sinks: the last
  * `window` ones, itself included, and the sequence's first `sinks`. window >= 1,
- * sinks >= 0; sizes past T mean T. Workspace: wq_attn_prefill_ws. Error and
+ * sinks >= 0; sizes past T mean T. Workspace: wq_attn_prefill_ws. out must not alias an input. Error and
  * non-finite data as there, over the keys a query sees; for the term with 2^-36 and
  * 2^-37 max |v| is taken over the 32 keys (counted from the sequence's first) of
  * every key it sees, hidden ones included.
@@ -512,7 +512,7 @@ uint64_t wq_attn_decode_window_ws(int64_t B, int64_t heads, int64_t kv_heads, in
  * wq_attn_decode_window -- wq_attn_decode over the last `window` of the lens[b]
  * cached tokens and the first `sinks` ones. window >= 1, sinks >= 0. Pages that
  * hold none of those are not looked at: their table entries may be anything, so
- * they can be given to others.
+ * they can be given to others. out must not alias an input.
  */
 int wq_attn_decode_window(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
                           const int32_t *lens, int64_t B, const int32_t *table, int64_t max_pages, float scale,
@@ -532,7 +532,8 @@ uint64_t wq_attn_decode_shared_ws(int64_t B, int64_t heads, int64_t kv_heads, in
  * and non-finite data as wq_attn_decode's over all tokens a query sees; parts are
  * joined in a fixed order. Both lengths 0: a row of zeros. A prefix_len outside
  * [0, 64 * prefix_pages], or a page of the prefix outside the cache among those it
- * covers, gives NaN in all rows. prefix_pages is below 2^25; other limits as wq_attn_decode's.
+ * covers, gives NaN in all rows. out must not share memory with an input
+ * (WQ_ERR_SHAPE; columns of one buffer are apart). prefix_pages is below 2^25; other limits as wq_attn_decode's.
  */
 int wq_attn_decode_shared(const wq_kv_cache *cache, const float *q, int64_t q_stride, int64_t heads,
                           const int32_t *prefix, int64_t prefix_pages, const int32_t *prefix_len, const int32_t *lens,

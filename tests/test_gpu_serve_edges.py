@@ -8,7 +8,7 @@ from tests import layer_ref as ref
 from tests import serve_ref as sref
 from tests.gpu_util import note, torch_cuda
 from tests.test_gpu_layer import NAN, cu_of, dev, qkv, rng_for
-from tests.test_gpu_serve import check_window_prompt, freqs, ints
+from tests.test_gpu_serve import check_window_prompt, freqs, ints, shared_case
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,31 @@ def test_window_of_any_width_on_either_side_of_the_limits(lens, heads, d):
         wqa.attn_prefill(q, k, v, cu=cu_of(lens), out=out, window=window, sinks=sinks)
         got, part = few(heads, T, host, out)
         check_window_prompt(got, part, lens, d ** -0.5, window, sinks, f"{window} {sinks}")
+
+
+# ------------------------------------------------------------------ a shared prefix
+def test_shared_out_beside_its_query_but_not_in_it():
+    """Columns of one buffer are apart; anything that shares memory is refused."""
+    note("shared out")
+    torch = torch_cuda()
+    rng = rng_for(114)
+    heads, kv, d, B = 6, 2, 64, 70
+    pre, table, host, cache, q = shared_case(rng, heads, kv, d, 1000, [50] * B)
+    args = (cache, dev(pre), ints([1000]), dev(table), ints([50] * B))
+    want = wqa.attn_decode_shared(dev(q), *args)
+    w = heads * d
+    both = torch.full((B, 3 * w), NAN, device="cuda")
+    qs = both[:, w:2 * w].unflatten(1, (heads, d))
+    for at in (0, 2 * w):
+        qs.copy_(dev(q))
+        out = both[:, at:at + w].unflatten(1, (heads, d))
+        assert torch.equal(wqa.attn_decode_shared(qs, *args, out=out), want) and torch.equal(qs, dev(q))
+    before = both.clone()
+    for at in (w, w - 64, 64, 2 * w - 64):
+        with pytest.raises(wqa.WqError):
+            wqa.attn_decode_shared(qs, *args, out=both[:, at:at + w].unflatten(1, (heads, d)))
+    flat = dev(q).view(-1)
+    with pytest.raises(wqa.WqError):
+        wqa.attn_decode_shared(flat[:-w].view(B - 1, heads, d), cache, args[1], args[2], args[3][1:], args[4][1:], out=flat[w:].view(B - 1, heads, d))
+    torch.cuda.synchronize()
+    assert torch.equal(torch.nan_to_num(both), torch.nan_to_num(before))

@@ -225,3 +225,22 @@ def test_reference_window():
     w = np.exp(0.1 * k[[0, 9, 10], 0] @ q[10, 0])
     assert np.allclose(out[10, 0], w @ v[[0, 9, 10], 0] / w.sum())
     assert sref.seen(7, 2, 3).tolist() == [True] * 3 + [False] * 2 + [True] * 2
+
+
+def test_decode_shared_refuses_an_out_in_other_memory_of_the_call(lib):  # noqa: F811
+    """Finished rows would be written where other workgroups have inputs still to read."""
+    row, far = 2048 * 4, 1 << 32
+    at = dict(q=far, pre=2 * far, plen=3 * far, lens=4 * far, table=5 * far, ws=6 * far)
+    cache = _cache(kq=7 * far, ks=8 * far, vq=9 * far, vs=10 * far)
+    codes = cache.n_pages * cache.kv_heads * 64 * cache.head_dim // 2
+    size = dict(pre=20, plen=4, lens=8, table=32, kq=codes, ks=codes // 8, vq=codes, vs=codes // 8)
+    for qs, os in ((2048, 2048), (2048, 4096), (4096, 2048), (8192, 8192), (4096, 6144), (6144, 4096)):
+        spans = dict(size, q=(qs + 2048) * 4)
+        for name, base in list(at.items())[:-1] + [(n, getattr(cache, n)) for n in ("kq", "ks", "vq", "vs")]:
+            begin, end = base, base + spans[name]
+            # its first row's beginning or end, or its second row's
+            for where in (begin // 16 * 16, (end - 1) // 16 * 16, begin - row + 16, (begin - os * 4) // 16 * 16, (end - 16 - os * 4) // 16 * 16):
+                assert _shared(lib, cache, qs=qs, os=os, out=where, **at) == SHAPE, (name, qs, os, where - base)
+    # rows that pass between one another do not meet at first, but further on
+    assert _shared(lib, cache, qs=4096, os=4160, out=far + row, **dict(at, B=40, table=11 * far)) == SHAPE
+    assert _shared(lib, cache, qs=4160, os=4096, out=far + row, **dict(at, B=40, table=11 * far)) == SHAPE

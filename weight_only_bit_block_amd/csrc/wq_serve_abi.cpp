@@ -29,6 +29,35 @@ bool meet(const Span &a, const Span &b)
     return a.at && b.at && a.bytes && b.bytes && (uintptr_t)a.at < (uintptr_t)b.at + b.bytes && (uintptr_t)b.at < (uintptr_t)a.at + a.bytes;
 }
 
+// Rows of a call's memory: n of `bytes` each, `stride` bytes apart.
+struct Rows {
+    const void *at;
+    int64_t bytes, stride, n;
+};
+
+// Whether one of `a`'s rows shares memory with one of `b`'s: columns of one buffer do not, though their spans meet.
+bool rows_meet(const Rows &a, const Rows &b)
+{
+    if (!a.at || !b.at || a.bytes <= 0 || b.bytes <= 0 || a.n <= 0 || b.n <= 0) return false;
+    const int64_t pa = (int64_t)(uintptr_t)a.at, pb = (int64_t)(uintptr_t)b.at;
+    if (pa >= pb + (b.n - 1) * b.stride + b.bytes || pb >= pa + (a.n - 1) * a.stride + a.bytes) return false;
+    // Rows first to last of `a` against b's `bytes` from `begin` on: the first that ends behind it decides.
+    const auto any = [&](int64_t first, int64_t last, int64_t begin) {
+        int64_t i = first;
+        if (last > first) {
+            const int64_t gap = begin - pa - a.bytes, past = gap / a.stride - (gap % a.stride < 0) + 1;
+            i = past > first ? past : first;
+        }
+        return i <= last && pa + i * a.stride + a.bytes > begin && pa + i * a.stride < begin + b.bytes;
+    };
+    if (b.n == 1) return any(0, a.n - 1, pb);
+    if (a.n == 1) return rows_meet(b, a);
+    if (a.stride == b.stride) return any(1 - b.n, a.n - 1, pb);  // only the difference of two rows' numbers counts
+    for (int64_t j = 0; j < b.n; ++j)
+        if (any(0, a.n - 1, pb + j * b.stride)) return true;
+    return false;
+}
+
 int check_shared(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
 {
     int st = check_decode(B, heads, kv_heads, head_dim, max_pages);
@@ -191,6 +220,16 @@ int wq_attn_decode_shared(const wq_kv_cache *cache, const float *q, int64_t q_st
     st = check_ws(workspace, workspace_bytes,
                   wq::shared_ws_bytes(B, heads, cache->kv_heads, cache->head_dim, max_pages, prefix_pages));
     if (st) return st;
+    // Finished rows of own tokens go to out while other workgroups may still have to read any of the inputs.
+    const int64_t row = heads * cache->head_dim * 4, codes = cache->n_pages * cache->kv_heads * WQ_KV_PAGE * (cache->head_dim / 2);
+    const Rows y = {out, row, out_stride * 4, B};
+    const Rows in[] = {{q, row, q_stride * 4, B},           {lens, B * 4, 0, 1},
+                       {table, B * max_pages * 4, 0, 1},    {prefix, prefix_pages * 4, 0, 1},
+                       {prefix_len, 4, 0, 1},               {cache->kq, codes, 0, 1},
+                       {cache->vq, codes, 0, 1},            {cache->ks, codes / 8, 0, 1},
+                       {cache->vs, codes / 8, 0, 1}};
+    for (const Rows &i : in)
+        if (rows_meet(y, i)) return WQ_ERR_SHAPE;
     const wq::SharedArgs a = {{*cache, q, q_stride, (int)heads, lens, (int)B, table, max_pages, scale, out, out_stride, workspace, 0, 0, 0, nullptr},
                               prefix, prefix_len, prefix_pages};
     return hip_status(wq::launch_attn_decode_shared(a, stream));

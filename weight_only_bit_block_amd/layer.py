@@ -299,8 +299,9 @@ def attn_decode_shared(q, cache: KVCache, prefix, prefix_len, table, lens, scale
     [prefix_pages] and prefix_len int32 [1], the shared tokens' pages and number,
     read once for all queries; table int32 [sequences, max_pages] and lens int32
     [sequences] as in attn_decode, of each sequence's own tokens behind them.
-    Returns out like q: zeros where there is no token, NaN where a length or page
-    lies outside its table or the cache (of the prefix: in all rows)."""
+    Returns out like q (sharing no memory with an input): zeros where there is no
+    token, NaN where a length or page lies outside its table or the cache (of the
+    prefix: in all rows)."""
     B, H, D, qs = _heads(q, "q")
     at = q.get_device()
     c = cache._struct(at)
