@@ -9,11 +9,15 @@ namespace wq {
 
 // Workgroup barrier that orders LDS only: waits for this wave's LDS operations,
 // then s_barrier. Unlike __syncthreads() it does not wait for outstanding global
-// loads, so prefetched registers stay in flight across the barrier.
+// loads, so prefetched registers stay in flight across the barrier. (The two
+// builtins touch no memory in the compiler's eyes: the empty statements keep LDS
+// accesses on their side.)
 __device__ __forceinline__ void lds_barrier()
 {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0); vmcnt and expcnt untouched
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // Raw buffer descriptor over [p, p + bytes) (bytes < 2^32). Dword 3 selects
