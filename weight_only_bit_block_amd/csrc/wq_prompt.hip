@@ -629,8 +629,8 @@ __global__ __launch_bounds__(64 * W, 2) void attend_kernel(PromptArgs a, const _
                 (__attribute__((address_space(3))) void *)(dst + i * 1024 * W), 16, 0, 0);
     };
     auto meet = [&]() {                          // this wave's copies have arrived, its reads are done; so have all waves'
-        __builtin_amdgcn_s_waitcnt(0x0070);
         asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
