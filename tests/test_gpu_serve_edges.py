@@ -8,7 +8,7 @@ from tests import layer_ref as ref
 from tests import serve_ref as sref
 from tests.gpu_util import note, torch_cuda
 from tests.test_gpu_layer import NAN, cu_of, dev, qkv, rng_for
-from tests.test_gpu_serve import check_window_prompt, freqs, ints, shared_case
+from tests.test_gpu_serve import check_shared, check_window_prompt, freqs, ints, shared_case
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,21 @@ def test_shared_out_beside_its_query_but_not_in_it():
         wqa.attn_decode_shared(flat[:-w].view(B - 1, heads, d), cache, args[1], args[2], args[3][1:], args[4][1:], out=flat[w:].view(B - 1, heads, d))
     torch.cuda.synchronize()
     assert torch.equal(torch.nan_to_num(both), torch.nan_to_num(before))
+
+
+@pytest.mark.parametrize("count,heads,kv,d,prefix,longest", [(1, 16, 8, 128, 70, 100000), (40, 4, 2, 128, 100, 12500), (4, 16, 8, 128, 50, 27000),
+                                                              (60, 14, 2, 64, 30, 7000), (1, 8, 1, 64, 300, 800000), (90, 20, 4, 64, 0, 2500)])
+def test_shared_long_sequences_behind_a_short_prefix(count, heads, kv, d, prefix, longest):
+    """Own tokens that take nearly the whole card."""
+    note(f"shared short prefix {count} {heads} {kv} {d} {prefix} {longest}")
+    torch = torch_cuda()
+    rng = rng_for(115, count, longest)
+    lens = [int(x) for x in rng.integers(0, longest // 4, count)]
+    lens[-1] = longest
+    if count > 1:
+        lens[count // 2] = 0
+    pre, table, host, cache, q = shared_case(rng, heads, kv, d, prefix, lens)
+    out = torch.full(q.shape, NAN, device="cuda")
+    for n in (prefix, prefix // 2):
+        wqa.attn_decode_shared(dev(q), cache, dev(pre), ints([n]), dev(table), ints(lens), out=out)
+        check_shared(out, q, host, pre, n, table, lens, d ** -0.5, str(n))

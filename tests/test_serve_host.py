@@ -244,3 +244,13 @@ def test_decode_shared_refuses_an_out_in_other_memory_of_the_call(lib):  # noqa:
     # rows that pass between one another do not meet at first, but further on
     assert _shared(lib, cache, qs=4096, os=4160, out=far + row, **dict(at, B=40, table=11 * far)) == SHAPE
     assert _shared(lib, cache, qs=4160, os=4096, out=far + row, **dict(at, B=40, table=11 * far)) == SHAPE
+
+
+@pytest.mark.parametrize("B,heads,kv,d,pages", [(1, 16, 8, 128, 2048), (64, 32, 8, 128, 128), (1024, 16, 8, 128, 20), (4, 16, 8, 128, 500), (64, 14, 2, 64, 128),
+                                                (2, 100, 100, 64, 300), (3, 1024, 512, 128, 90), (1, 8, 1, 64, 16000)])
+def test_own_tokens_behind_a_short_prefix_have_room_for_as_many_runs_as_alone(lib, B, heads, kv, d, pages):  # noqa: F811
+    alone = lib.wq_attn_decode_ws(B, heads, kv, d, pages)
+    sizes = [lib.wq_attn_decode_shared_ws(B, heads, kv, d, pages, n) for n in (0, 1, 2, 4, 16, 64, 128, 129, 1000, 100000, (1 << 25) - 1)]
+    assert sizes == sorted(sizes) and sizes[0] >= alone
+    # the parts of the prefix and a maximum and a sum for each head come on top
+    assert sizes[2] <= alone + 512 + B * heads * (8 + 2 * (d + 4) * 4)

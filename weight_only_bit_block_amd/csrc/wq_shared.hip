@@ -548,10 +548,17 @@ inline int row_waves(int64_t rows, int64_t head_dim, int64_t prefix_pages)
 inline int run_unit(int64_t rows) { return rows <= kFewRows ? kDecodeWaves : 1; }        // pages
 // A sequence's own tokens are cut whenever that makes parts, since there is a join anyway, into no more
 // runs than there can be steps; the prefix into as many as fill what is left of the card, half of it at
-// least, and all of it where its runs are longer than kRunPages. With workgroups of 64 rows own tokens take
-// half of the card at most, so that a short prefix has a place from the start (64 sequences behind 4096
-// tokens 37.7 -> 31.1 us; with those of 128 rows and long prefixes it costs: 64 behind 16000 55.4 -> 58.2).
-constexpr int kRunPages = 4;
+// least, and all of it where its runs are longer than kRunPages. Own tokens leave it a place from the start (but
+// beside workgroups of 128 rows: 64 sequences behind 16000 tokens 55.4 us, 58.2 with a place): half of the card (64
+// behind 4096 37.7 -> 31.1), or, where it has little to do beside them, its share of the work. That is counted
+// in steps of own tokens, as the table's width allows them: a page of the prefix takes as long as one (with 8 rows:
+// four pages), and a part of it kStartSteps to begin. us, half / share, with the prefix's part of the work: 16/8 heads
+// of 128, 1 request of 131072 own tokens behind 64 (0.01) 39.7 / 38.6, behind 4096 (0.16) 40.1 / 41.2; 4 requests,
+// 120000, behind 1024 (0.02) 35.5 / 32.5, behind 4096 (0.07) 35.5 / 37.5; 32, 24864, behind 1024 (0.02) 25.4 / 23.2, behind 4096
+// (0.09) 28.6 / 31.8; 32/8 heads, 64, 524288, behind 64 (0.001) 143 / 127, behind 4096 (0.03) 159 / 149. Few steps gain nothing
+// by more runs: 14/2 heads of 64, 16 requests, 65536 in 87 steps at most, behind 256 17.0 / 17.6; 64, 262144 in 155, 28.5 / 25.2.
+constexpr int kRunPages = 4, kStartSteps = 4;
+constexpr int kLittle = 16, kShortRuns = 12;
 struct SharedCut {
     int groups, per_step;                        // of the sequences' own heads
     int own, chunks;                             // runs of own tokens (0: whole sequences), of the prefix
@@ -568,13 +575,19 @@ inline SharedCut shared_cut(int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     int64_t most = runs_per_head(c.per_step);
     c.waves = rows <= kFewRows ? 0 : row_waves(rows, head_dim, prefix_pages);
     c.together = c.waves == 4 ? 2 : 1;
-    if (c.waves != 4) most = (most + 1) / 2;     // beside the prefix, not before it
-    c.own = B > kCutMaxSeqs || steps <= 1 ? 0 : (int)(B * steps < most ? B * steps : most);
-    c.own_jobs = (unsigned)((int64_t)c.per_step * (c.own ? c.own : B));
     const int64_t each = c.waves ? 32 * c.waves : kMaxGroup;
     c.blocks = (rows + each - 1) / each * kv_heads;
-    const int64_t slots = c.waves == 4 ? kSharedFill / 2 : kSharedFill, taken = (c.own_jobs + c.together - 1) / c.together;
     const int64_t unit = run_unit(rows), units = (prefix_pages + unit - 1) / unit;
+    if (c.waves != 4) {                          // beside the prefix, not before it
+        const int64_t parts = c.blocks * ((prefix_pages + kRunPages - 1) / kRunPages);
+        const int64_t there = c.blocks * units + parts * kStartSteps, work = c.per_step * B * (steps + kChangeSteps);
+        if (kLittle * there >= work || c.per_step * B * steps <= kShortRuns * (kSharedFill / 2)) most = (most + 1) / 2;
+        else most = (kSharedFill - (there * (kSharedFill / 2) + there + work - 1) / (there + work)) / c.per_step;
+        if (most < 1) most = 1;
+    }
+    c.own = B > kCutMaxSeqs || steps <= 1 ? 0 : (int)(B * steps < most ? B * steps : most);
+    c.own_jobs = (unsigned)((int64_t)c.per_step * (c.own ? c.own : B));
+    const int64_t slots = c.waves == 4 ? kSharedFill / 2 : kSharedFill, taken = (c.own_jobs + c.together - 1) / c.together;
     const int64_t left = (taken > slots / 2 ? slots / 2 : slots - taken) / c.blocks, all = slots / c.blocks;
     int64_t n = prefix_pages / kRunPages < all ? prefix_pages / kRunPages : all;
     if (n < left) n = left;
@@ -590,7 +603,9 @@ inline uint64_t own_bytes(const SharedCut &c, int64_t head_dim) { return c.own ?
 uint64_t shared_ws_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_pages, int64_t prefix_pages)
 {
     const SharedCut c = shared_cut(B, heads, kv_heads, head_dim, max_pages, prefix_pages);
-    return own_bytes(c, head_dim) + sums_bytes(B, heads) + (uint64_t)c.chunks * B * heads * (uint64_t)(head_dim + kPartialExtra) * 4;
+    // (own tokens behind a short prefix may be cut into more runs: more pages never ask for less)
+    const SharedCut alone = shared_cut(B, heads, kv_heads, head_dim, max_pages, 0);
+    return own_bytes(alone.own > c.own ? alone : c, head_dim) + sums_bytes(B, heads) + (uint64_t)c.chunks * B * heads * (uint64_t)(head_dim + kPartialExtra) * 4;
 }
 
 hipError_t launch_attn_decode_shared(const SharedArgs &args, hipStream_t stream)
