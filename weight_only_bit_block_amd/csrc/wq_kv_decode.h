@@ -303,8 +303,11 @@ constexpr int decode_lds_bytes(int D, int H) { return kDecodeWaves * (decode_wav
 
 // The work of kDecodeWaves wavefronts, job `job` of a launch, thread `tid` of it.
 // `cut`: into how many runs the work of a kv head and group of heads is cut, 0: not.
-// (Where a workgroup does several jobs at once, their wavefronts meet at more barriers than they
-// need; those that are done do not hold up the others.)
+// (Where a workgroup does two jobs at once, shared_kernel's, their wavefronts come to unequal numbers of barriers, which
+// HIP leaves undefined. It is right by the instruction the barriers are on this machine: s_barrier counts arrivals of a
+// workgroup's wavefronts wherever in the program they are, and waits only for those that have not ended. So the n-th
+// arrivals of all eight meet, a job's four among them, a barrier more than a job needs only delays it, and a job
+// that is done holds up nobody. The condition around a job is the same for whole wavefronts.)
 template <int D, int H, Form FORM>
 __device__ __forceinline__ void decode_job(const DecodeArgs &a, int groups, int cut, float c_man, int c_exp, uint8_t *lds, unsigned job, int tid)
 {

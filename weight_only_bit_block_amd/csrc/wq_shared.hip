@@ -389,7 +389,7 @@ __global__ __launch_bounds__(128 * RW, D == 64 ? 3 : 2) void shared_kernel(Share
     const unsigned own_groups = (own_jobs + kJobs - 1) / kJobs;
     if (blockIdx.x < own_groups) {
         const int which = kJobs == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-        const unsigned job = blockIdx.x * kJobs + which;
+        const unsigned job = blockIdx.x * kJobs + which;             // (two meet at unequal barriers: decode_job)
         if (job < own_jobs) decode_job<D, H, Form::sums>(a.own, groups, cut, c_man, c_exp, lds + which * kJobBytes, job, threadIdx.x & 255);
         return;
     }
