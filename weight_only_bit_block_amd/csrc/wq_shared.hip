@@ -135,7 +135,7 @@ __device__ __forceinline__ void prefix_job(const SharedArgs &a, float *parts, in
         // magnitudes of the lane's scales of v in their order, what is not finite below zero
         if ((int64_t)page * kTile + lane >= runs.len) vs = hb{};
         typedef uint16_t ub __attribute__((ext_vector_type(NB)));
-        const ub rank = __builtin_bit_cast(ub, vs) * (uint16_t)2 + (uint16_t)kRankZero;
+        const ub rank = scale_rank(__builtin_bit_cast(ub, vs));
         uint16_t top = rank[0];
         int by = 0;
 #pragma unroll
