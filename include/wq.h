@@ -440,7 +440,9 @@ int wq_residual_norm(const float *h, const float *y, const float *post_weight, c
  *             list no longer covers becomes -1. Other entries stay;
  *   taken_out taken plus the pages the step wants (at most 2^31 - 1): more than
  *             n_free where the list was too short;
- *   positions of token t = cu[b] + i: start[b] + i;
+ *   positions of token t = cu[b] + i: start[b] + i (of a request behind a shared
+ *             prefix, which is not among its own tokens: for the rotation the caller adds
+ *             the prefix's length to those that are not -1);
  *   slots     the token's place in the cache, page * 64 + position % 64, for
  *             wq_kv_append_slots; -1 where the token has no page (past the row, or
  *             an entry below 0).
@@ -528,7 +530,8 @@ uint64_t wq_attn_decode_shared_ws(int64_t B, int64_t heads, int64_t kv_heads, in
  * tokens: every query sees the prefix's prefix_len[0] cached tokens, in the pages
  * prefix [prefix_pages], and its own lens[b] ones, in its table row, as one
  * softmax. The prefix is read once for all B queries of a head, whatever B;
- * it need not fill its last page, own tokens begin in pages of their own. Error
+ * it need not fill its last page, own tokens begin in pages of their own. (Where keys
+ * are rotated by position, own token i was at prefix_len + i.) Error
  * and non-finite data as wq_attn_decode's over all tokens a query sees; parts are
  * joined in a fixed order. Both lengths 0: a row of zeros. A prefix_len outside
  * [0, 64 * prefix_pages], or a page of the prefix outside the cache among those it

@@ -8,7 +8,7 @@ from tests import layer_ref as ref
 from tests import serve_ref as sref
 from tests.gpu_util import note, torch_cuda
 from tests.test_gpu_layer import NAN, cu_of, dev, qkv, rng_for
-from tests.test_gpu_serve import check_shared, check_window_prompt, freqs, ints, shared_case
+from tests.test_gpu_serve import check_rows, check_shared, check_window_prompt, freqs, ints, shared_case
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,56 @@ def test_shared_long_sequences_behind_a_short_prefix(count, heads, kv, d, prefix
     for n in (prefix, prefix // 2):
         wqa.attn_decode_shared(dev(q), cache, dev(pre), ints([n]), dev(table), ints(lens), out=out)
         check_shared(out, q, host, pre, n, table, lens, d ** -0.5, str(n))
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("prefix", [128, 100])
+def test_own_tokens_are_rotated_behind_the_prefix(prefix):
+    """Requests planned and cached whole, and the same as own tokens behind one copy of their common beginning: the same
+    cache rows and the same attention."""
+    note(f"rotated behind {prefix}")
+    torch = torch_cuda()
+    rng = rng_for(116, prefix)
+    heads, kv, d, pages, width = 8, 2, 128, 40, 6
+    own = [70, 1, 64]
+    inv, free, n = dev(freqs(64)), ints(rng.permutation(pages)), ints([prefix])
+    _, first = qkv(rng, prefix, heads, kv, d)
+    rest = [qkv(rng, m, heads, kv, d)[1] for m in own]
+
+    def fill(parts, fresh, shift):
+        """Plans, rotates and caches requests of these tokens; one more token in hand than there is."""
+        q, k, v = (torch.cat([p[i] for p in parts] + [parts[0][i][:1]]) for i in range(3))
+        cache, table = wqa.KVCache.empty(pages, kv, d), ints(np.full((len(fresh), width), -1))
+        p = wqa.kv_plan(ints(fresh), table, free, tokens=len(q))
+        at = torch.where(p.positions < 0, p.positions, p.positions + shift)
+        q, k = wqa.qk_norm_rope(q, k, at, inv)
+        wqa.kv_append(cache, k, v, slots=p.slots)
+        return q[p.cu[1:].long() - 1], cache, table, p
+
+    def rows(cache, table, b, lo, hi):
+        t = np.arange(lo, hi)
+        page = table.cpu().numpy()[b, t // 64]
+        return [x.cpu().numpy()[page, :, t % 64] for x in cache]
+    q, whole, tables, p = fill([x for r in rest for x in (first, r)], [prefix + m for m in own], 0)
+    _, pre, pre_table, _ = fill([first], [prefix], 0)
+    # the prefix's pages are the first of the list, own tokens' those behind them
+    free = free[-(-prefix // 64):].contiguous()
+    q2, cache, table, p2 = fill(rest, own, n)
+    for b, m in enumerate(own):
+        for x, y in zip(rows(whole, tables, b, prefix, prefix + m), rows(cache, table, b, 0, m)):
+            assert np.array_equal(x, y), b
+        for x, y in zip(rows(whole, tables, b, 0, prefix), rows(pre, pre_table, 0, 0, prefix)):
+            assert np.array_equal(x, y), b
+    assert torch.equal(q, q2)
+    for x, y in zip(cache, pre):
+        at = pre_table[0][pre_table[0] >= 0].long()
+        x[at] = y[at]
+    out = wqa.attn_decode_shared(q2, cache, pre_table[0], n, table, p2.lens)
+    codes = [t.cpu().numpy() for t in (cache.kq, cache.vq)]
+    codes = [np.stack((c & 15, c >> 4), -1).reshape(*c.shape[:-1], d).astype(np.int8) for c in codes]
+    kval, vval = (ref.values(np.where(c > 7, c - 16, c), t.view(torch.float16).cpu().numpy()) for c, t in zip(codes, (cache.ks, cache.vs)))
+    tab, first = table.cpu().numpy(), pre_table[0].cpu().numpy()
+    want, sums = sref.decode(q.cpu().numpy(), kval, vval, cache.vs.view(torch.float16).cpu().numpy(), d ** -0.5,
+                             lambda b: [(first, prefix, None), (tab[b], own[b], None)])
+    check_rows(out, want, sums, prefix + max(own), d)
+    check_rows(wqa.attn_decode(q, whole, tables, p.lens), want, sums, prefix + max(own), d)

@@ -298,7 +298,8 @@ def attn_decode_shared(q, cache: KVCache, prefix, prefix_len, table, lens, scale
     the same cached tokens: q [sequences, heads, head_dim] fp32; prefix int32
     [prefix_pages] and prefix_len int32 [1], the shared tokens' pages and number,
     read once for all queries; table int32 [sequences, max_pages] and lens int32
-    [sequences] as in attn_decode, of each sequence's own tokens behind them.
+    [sequences] as in attn_decode, of each sequence's own tokens behind them (rotated,
+    where they are, as tokens prefix_len + 0, 1, ...).
     Returns out like q (sharing no memory with an input): zeros where there is no
     token, NaN where a length or page lies outside its table or the cache (of the
     prefix: in all rows)."""
@@ -349,7 +350,8 @@ def kv_plan(fresh, table, free, taken: Optional[torch.Tensor] = None, tokens: in
     (past len(free): the list was too short). `out`: a plan to write into, which
     shares no memory with the inputs (start and taken are copies of the last step's
     lens and taken, or those of another plan). A request with a bad length gets
-    lens -1 and no tokens."""
+    lens -1 and no tokens. Of requests behind a shared prefix these are their own
+    tokens: for qk_norm_rope add the prefix's length to the positions that are not -1."""
     if not (isinstance(fresh, _Tensor) and fresh.dim() == 1 and fresh.is_cuda):
         raise ValueError("fresh must be an int32 device tensor [requests]")
     B, at = fresh.shape[0], fresh.get_device()
